@@ -76,9 +76,11 @@ enum {
   MOE_DEVERR_EXPERT_ID = 1,   /* a top-k id outside [0, E) */
   MOE_DEVERR_NOT_RESIDENT = 2,/* an active expert has no valid slot */
   MOE_DEVERR_TIMEOUT = 3,     /* a bounded pipeline wait ran out */
-  MOE_DEVERR_RANGE = 4        /* an activation x or an expert intermediate h
+  MOE_DEVERR_RANGE = 4,       /* an activation x or an expert intermediate h
                                  outside FP16's finite range (|v| > 65504):
                                  the FFN's FP16 operand copies cannot hold it */
+  MOE_DEVERR_OFFSETS = 5      /* row offsets that fall, start below zero or end
+                                 behind the last row (they are cut to the rows) */
 };
 
 /* Message for the last failed call on this host thread ("" if none). */
@@ -298,6 +300,108 @@ int moe_grouped_bf16_ffn(const moe_bf16 *x, const int32_t *sorted_pair,
                          int64_t record_bytes, int T, int k, int E, int H,
                          int I, float *y, void *ws, size_t ws_bytes,
                          moe_stream_t stream);
+
+/* Flags of the grouped products. */
+#define MOE_GEMM_OUT_F32 1    /* the output is fp32 instead of BF16 */
+#define MOE_GEMM_ACCUMULATE 2 /* add to the output (fp32 outputs only) */
+
+/*
+ * Grouped BF16 products: one nn.Linear weight W_e [N][K] per expert e, applied
+ * to that expert's rows, for experts kept in BF16 (training them, or running
+ * one of the FFN's matrices by itself). Rows are in group order: expert e owns
+ * rows offsets[e] <= r < offsets[e+1], as moe_group_tokens writes offsets.
+ *   moe_grouped_gemm        y[r]  = x[r] W_e^T           (forward)
+ *   moe_grouped_gemm_dgrad  dx[r] = dy[r] W_e            (the rows' gradient)
+ *   moe_grouped_gemm_wgrad  dW_e  = sum_r dy[r]^T x[r]   (the weights' gradient)
+ *   x, dx        [R][K], dy, y [R][N]: row strides ldx, lddx, lddy, ldy in elements.
+ *   offsets      [E+1] int32, 0 <= offsets[0] <= ... <= offsets[E] <= R. Rows
+ *                outside [offsets[0], offsets[E]) are neither read nor
+ *                written. Offsets outside [0, R] or falling ones are cut to
+ *                the rows and set MOE_DEVERR_OFFSETS.
+ *   w, dw        matrix e starts at element e * w_stride (dw_stride), rows of
+ *                K elements without gaps: a stack [E][N][K], or one part of
+ *                the records of a BF16 bank (moe_bf16_record_layout; stride =
+ *                record bytes / 2). dw of an expert without rows is zero (with
+ *                MOE_GEMM_ACCUMULATE: left as it is).
+ *   y, dx, dw    BF16, or fp32 with MOE_GEMM_OUT_F32; with
+ *                MOE_GEMM_ACCUMULATE the product is added to what they hold.
+ *                They must not overlap an input.
+ *   ws           at least moe_grouped_gemm_workspace_size(R, E, N, K) bytes
+ *                (one size for the three), 256-byte aligned, zeroed once before
+ *                first use; word 0 is the device error word. Calls that may
+ *                overlap on the GPU need a workspace each.
+ * Sums are fp32 and rounded once, in an order that depends on the shape alone:
+ * equal calls give equal bits. N and K are multiples of 8, strides multiples
+ * of 8, pointers 16-byte aligned. R may be 0.
+ */
+size_t moe_grouped_gemm_workspace_size(int R, int E, int N, int K);
+int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *offsets,
+                     const moe_bf16 *w, int64_t w_stride, int R, int E, int N,
+                     int K, int flags, void *y, int64_t ldy, void *ws,
+                     size_t ws_bytes, moe_stream_t stream);
+int moe_grouped_gemm_dgrad(const moe_bf16 *dy, int64_t lddy,
+                           const int32_t *offsets, const moe_bf16 *w,
+                           int64_t w_stride, int R, int E, int N, int K,
+                           int flags, void *dx, int64_t lddx, void *ws,
+                           size_t ws_bytes, moe_stream_t stream);
+int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
+                           int64_t ldx, const int32_t *offsets, int R, int E,
+                           int N, int K, int flags, void *dw,
+                           int64_t dw_stride, void *ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests at once beside a shared BF16 projection
+ * W [N][K] (the projections around the routed experts stay BF16: Abstract).
+ * Rows come in segments, one per request: segment s is rows
+ * seg_offsets[s] <= t < seg_offsets[s+1] and uses adapter a = seg_adapter[s];
+ * several segments may use one adapter, and -1 means none.
+ *   moe_lora_linear           u[t]  = scale[a] x[t] A_a^T
+ *                             y[t]  = x[t] W^T + u[t] B_a^T
+ *   moe_lora_linear_backward  du[t] = scale[a] dy[t] B_a
+ *                             dx[t] = dy[t] W + du[t] A_a
+ *                             dA_a  = sum_t du[t]^T x[t],  dB_a = sum_t dy[t]^T u[t]
+ *   x, dx        [T][K], y, dy [T][N] BF16: row strides ldx, lddx, ldy, lddy.
+ *   w            [N][K] BF16, frozen (no gradient).
+ *   seg_offsets  [S+1] int32, 0 = seg_offsets[0] <= ... <= seg_offsets[S] <= T.
+ *                A segment may be empty. Rows behind the last segment are
+ *                neither read nor written. Other offsets are cut to the rows
+ *                and set MOE_DEVERR_OFFSETS.
+ *   seg_adapter  [S] int32 in [-1, n_adapters); any other value counts as -1
+ *                and sets MOE_DEVERR_EXPERT_ID.
+ *   lora_a       [n_adapters][rank][K], lora_b [n_adapters][N][rank] BF16; an
+ *                adapter of a smaller rank is padded with zeros.
+ *   scale        [n_adapters] fp32, or NULL for 1.
+ *   u, du        [T][rank] BF16, written (0 for rows without an adapter): u is
+ *                kept for the backward pass, which reads it; du is scratch
+ *                that holds the adapters' inner gradient.
+ *   d_lora_a/b   shaped as lora_a and lora_b, BF16; every adapter's gradient
+ *                is written, zeros for one without rows. Both may be NULL (x
+ *                and u are then not read and may be NULL too), and so may dx.
+ *   ws           at least moe_lora_workspace_size bytes, 256-byte aligned,
+ *                zeroed once before first use; word 0 is the device error
+ *                word. Calls that may overlap on the GPU need a workspace each.
+ * Sums are fp32; u and du are rounded to BF16 once, as operands of the product
+ * they enter, and every other output once at the end. Equal calls give equal
+ * bits. N and K are multiples of 8, rank a multiple of 8 from 8 to 128, S <=
+ * 65535, strides multiples of 8, pointers 16-byte aligned. T and S may be 0.
+ */
+size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K);
+int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w,
+                    const int32_t *seg_offsets, const int32_t *seg_adapter,
+                    const moe_bf16 *lora_a, const moe_bf16 *lora_b,
+                    const float *scale, int T, int S, int n_adapters, int rank,
+                    int N, int K, moe_bf16 *u, moe_bf16 *y, int64_t ldy,
+                    void *ws, size_t ws_bytes, moe_stream_t stream);
+int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy,
+                             const moe_bf16 *x, int64_t ldx, const moe_bf16 *w,
+                             const moe_bf16 *u, const int32_t *seg_offsets,
+                             const int32_t *seg_adapter, const moe_bf16 *lora_a,
+                             const moe_bf16 *lora_b, const float *scale, int T,
+                             int S, int n_adapters, int rank, int N, int K,
+                             moe_bf16 *du, moe_bf16 *dx, int64_t lddx,
+                             moe_bf16 *d_lora_a, moe_bf16 *d_lora_b, void *ws,
+                             size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Test hook for the failure path of the tensor-core FFN: the next `calls`

@@ -17,7 +17,9 @@ _NATIVE_NAMES = {
     "moe_pool_save", "moe_pool_file_info", "moe_pool_load",
     "MOE_RENORM", "MOE_LOGITS_GIVEN", "MOE_IDS_GIVEN", "MOE_PATH_AUTO", "MOE_PATH_GEMV", "MOE_PATH_TC", "MOE_PATH_SEQUENTIAL", "MOE_SLOT_SKIP", "MOE_FFN_X_F16",
     "moe_bf16_record_layout", "moe_bf16_ffn_workspace_size", "moe_grouped_bf16_ffn",
-    "MOE_DEVERR_NONE", "MOE_DEVERR_EXPERT_ID", "MOE_DEVERR_NOT_RESIDENT", "MOE_DEVERR_TIMEOUT", "MOE_DEVERR_RANGE",
+    "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "MOE_GEMM_OUT_F32", "MOE_GEMM_ACCUMULATE",
+    "moe_lora_workspace_size", "moe_lora_linear", "moe_lora_linear_backward",
+    "MOE_DEVERR_NONE", "MOE_DEVERR_EXPERT_ID", "MOE_DEVERR_NOT_RESIDENT", "MOE_DEVERR_TIMEOUT", "MOE_DEVERR_RANGE", "MOE_DEVERR_OFFSETS",
 }
 _LAYER_NAMES = {"ExpertBank", "Bf16Bank", "LayerBuffers", "moe_layer_forward"}
 

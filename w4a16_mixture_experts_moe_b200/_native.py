@@ -22,7 +22,8 @@ if not os.path.exists(LIB_PATH):
 lib = C.CDLL(LIB_PATH)
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_CUDA, MOE_ERR_CAPACITY, MOE_ERR_DEVICE, MOE_ERR_UNSUPPORTED = range(7)
-MOE_DEVERR_NONE, MOE_DEVERR_EXPERT_ID, MOE_DEVERR_NOT_RESIDENT, MOE_DEVERR_TIMEOUT, MOE_DEVERR_RANGE = range(5)
+MOE_DEVERR_NONE, MOE_DEVERR_EXPERT_ID, MOE_DEVERR_NOT_RESIDENT, MOE_DEVERR_TIMEOUT, MOE_DEVERR_RANGE, MOE_DEVERR_OFFSETS = range(6)
+MOE_GEMM_OUT_F32, MOE_GEMM_ACCUMULATE = 1, 2
 MOE_RENORM, MOE_LOGITS_GIVEN, MOE_IDS_GIVEN = 1, 2, 4
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_TC, MOE_PATH_SEQUENTIAL = 0, 1, 2, 3
 MOE_SLOT_SKIP = -2
@@ -65,6 +66,13 @@ SIGNATURES = {
     "moe_bf16_record_layout": (_i, [_i, _i, C.POINTER(moe_bf16_layout)]),
     "moe_bf16_ffn_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "moe_grouped_bf16_ffn": (_i, [_p, _p, _p, _p, _i64, _i, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "moe_grouped_gemm_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_grouped_gemm": (_i, [_p, _i64, _p, _p, _i64, _i, _i, _i, _i, _i, _p, _i64, _p, _sz, _p]),
+    "moe_grouped_gemm_dgrad": (_i, [_p, _i64, _p, _p, _i64, _i, _i, _i, _i, _i, _p, _i64, _p, _sz, _p]),
+    "moe_grouped_gemm_wgrad": (_i, [_p, _i64, _p, _i64, _p, _i, _i, _i, _i, _i, _p, _i64, _p, _sz, _p]),
+    "moe_lora_workspace_size": (_sz, [_i] * 6),
+    "moe_lora_linear": (_i, [_p, _i64] + [_p] * 6 + [_i] * 6 + [_p, _p, _i64, _p, _sz, _p]),
+    "moe_lora_linear_backward": (_i, [_p, _i64, _p, _i64] + [_p] * 7 + [_i] * 6 + [_p, _p, _i64, _p, _p, _p, _sz, _p]),
     "moe_debug_stall_next_tc_ffn": (_i, [_i]),
     "moe_combine": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_read_device_error": (_i, [_p, _p, C.POINTER(C.c_int32)]),
@@ -195,6 +203,44 @@ def moe_grouped_bf16_ffn(x, sorted_pair, offsets, bank, record_bytes, T, k, E, H
                          stream=None):
     _check(lib.moe_grouped_bf16_ffn(_ptr(x), _ptr(sorted_pair), _ptr(offsets), _ptr(bank), record_bytes, T, k, E,
                                     H, I, _ptr(y), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grouped_gemm_workspace_size(R, E, N, K) -> int:
+    return lib.moe_grouped_gemm_workspace_size(R, E, N, K)
+
+
+def moe_grouped_gemm(x, ldx, offsets, w, w_stride, R, E, N, K, flags, y, ldy, ws, ws_bytes, stream=None):
+    _check(lib.moe_grouped_gemm(_ptr(x), ldx, _ptr(offsets), _ptr(w), w_stride, R, E, N, K, flags, _ptr(y), ldy,
+                                _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grouped_gemm_dgrad(dy, lddy, offsets, w, w_stride, R, E, N, K, flags, dx, lddx, ws, ws_bytes, stream=None):
+    _check(lib.moe_grouped_gemm_dgrad(_ptr(dy), lddy, _ptr(offsets), _ptr(w), w_stride, R, E, N, K, flags, _ptr(dx),
+                                      lddx, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grouped_gemm_wgrad(dy, lddy, x, ldx, offsets, R, E, N, K, flags, dw, dw_stride, ws, ws_bytes, stream=None):
+    _check(lib.moe_grouped_gemm_wgrad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(offsets), R, E, N, K, flags, _ptr(dw),
+                                      dw_stride, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
+    return lib.moe_lora_workspace_size(T, S, n_adapters, rank, N, K)
+
+
+def moe_lora_linear(x, ldx, w, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters, rank, N, K, u, y, ldy,
+                    ws, ws_bytes, stream=None):
+    _check(lib.moe_lora_linear(_ptr(x), ldx, _ptr(w), _ptr(seg_offsets), _ptr(seg_adapter), _ptr(lora_a), _ptr(lora_b),
+                               _ptr(scale), T, S, n_adapters, rank, N, K, _ptr(u), _ptr(y), ldy, _ptr(ws), ws_bytes,
+                               _stream(stream)))
+
+
+def moe_lora_linear_backward(dy, lddy, x, ldx, w, u, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters,
+                             rank, N, K, du, dx, lddx, d_lora_a, d_lora_b, ws, ws_bytes, stream=None):
+    _check(lib.moe_lora_linear_backward(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(u), _ptr(seg_offsets),
+                                        _ptr(seg_adapter), _ptr(lora_a), _ptr(lora_b), _ptr(scale), T, S, n_adapters,
+                                        rank, N, K, _ptr(du), _ptr(dx), lddx, _ptr(d_lora_a), _ptr(d_lora_b), _ptr(ws),
+                                        ws_bytes, _stream(stream)))
 
 
 def moe_debug_stall_next_tc_ffn(calls: int):

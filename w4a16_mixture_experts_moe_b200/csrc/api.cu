@@ -91,6 +91,7 @@ int moe_read_device_error(void *ws, moe_stream_t stream, int32_t *code) {
                        : v == MOE_DEVERR_NOT_RESIDENT ? "active expert not resident in any slot"
                        : v == MOE_DEVERR_TIMEOUT      ? "bounded pipeline wait timed out"
                        : v == MOE_DEVERR_RANGE        ? "activation outside FP16 range on the tensor-core path"
+                       : v == MOE_DEVERR_OFFSETS      ? "row offsets out of order or out of range"
                                                       : "unknown device error";
     return moe::set_error(MOE_ERR_DEVICE, "device error %d: %s", v, what);
   }

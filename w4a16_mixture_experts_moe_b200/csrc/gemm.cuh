@@ -1,0 +1,63 @@
+// Shared declarations of the BF16 products over ragged row groups (grouped
+// products, many-adapter projection): the tensor-core engine of gemm_tc.cu and
+// the weight-streaming kernel of gemm_gemv.cu.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+enum GemmMode { GEMM_FWD = 0, GEMM_DGRAD = 1, GEMM_WGRAD = 2 };
+
+// One product for the tensor-core engine (gemm_tc.cu), passed by value.
+struct TcGemmArgs {
+  const int32_t *offsets;  // [groups+1] row starts; with adapters: [segs+1] segment starts, one group
+  const int32_t *adapter;  // [segs] adapter of each segment (outside [0, n_adapters): none), or nullptr
+  int groups, segs, n_adapters, rank;
+  int R;       // rows of x / dy
+  int M;       // output columns: N (fwd), K (dgrad, wgrad)
+  int NC;      // wgrad: rows of one dW (N)
+  int KD;      // reduction length: K (fwd), N (dgrad); wgrad reduces over a group's rows
+  int bn;      // widest row tile
+  int out_f32, accumulate;
+  void *out;
+  int64_t ldo, out_gstride;  // elements
+  const uint16_t *ext_a, *ext_b;  // with adapters: lora_b [n][N][rank] (fwd) or lora_a [n][rank][K], and u / du [R][rank]
+  int32_t *err;
+};
+
+// Operands in global memory (BF16, elements). a: weights [groups][N][K] with
+// stride a_gstride (fwd, dgrad) or x [R][K] (wgrad); b: x or dy rows.
+struct TcGemmOperands {
+  const uint16_t *a, *b;
+  int64_t lda, a_gstride, ldb;
+};
+
+int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what);
+
+// One product for the weight-streaming kernel (gemm_gemv.cu): out[r] = in[r] W^T
+// for the rows of each group, W [N][K] at w + index * w_stride.
+struct GemvArgs {
+  const uint16_t *in;
+  int64_t ldi;
+  const int32_t *offsets;  // [groups+1]
+  const int32_t *index;    // [groups] weight matrix of each group (outside [0, n_weights): none), or nullptr (the group's own)
+  const uint16_t *w;
+  int64_t w_stride;
+  int groups, n_weights, R, N, K;
+  int compact;             // grid row y = the y-th group with rows
+  const float *scale;      // [n_weights] factor of each weight matrix, or nullptr
+  void *out;
+  int64_t ldo;
+  int out_f32, accumulate;
+  int32_t *err;
+  // adapters added to a single group's product: out[r] += u[r] B_a^T
+  const int32_t *seg_offsets, *seg_adapter;
+  int segs, n_adapters, rank;
+  const uint16_t *u, *lora_b;
+};
+
+// grid_groups: grid rows (groups, or R with `compact`).
+int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what);
+
+}  // namespace moe

@@ -1,0 +1,651 @@
+// BF16 products over ragged row groups on the 5th-generation tensor cores
+// (tcgen05.mma, fp32 accumulators in tensor memory). Three directions of one
+// weight matrix W_e [N][K] per group e of rows:
+//   fwd    y[r]  = x[r] W_e^T           dgrad  dx[r] = dy[r] W_e
+//   wgrad  dW_e[n] = sum_r dy[r][n] x[r]
+// and, for a single group, low-rank adapters added inside the same sums
+// (fwd: + u[r] B_a^T, dgrad: + du[r] A_a for the adapter a of row r's segment).
+//
+// Every direction puts the output's contiguous dimension on the MMA's M side
+// (lanes of tensor memory: a warp then stores neighbouring addresses) and the
+// output's rows on its N side, whose width follows the group: a group of 40
+// rows runs N = 48, so ragged groups cost little padding. A pair of CTAs
+// (cta_group::2) shares one tile of 256 output columns x up to 256 rows: each
+// CTA loads its own 128 columns of A and half of the rows of B, so a k-step of
+// 64 brings 32 KB into each SM for 2 x 128 x 256 x 64 multiply-adds. A tile
+// owned by one CTA would load 48 KB for the same work per SM.
+//
+// Operand layouts: a dimension that is contiguous in memory is contiguous in
+// shared memory too (128-byte swizzle), so dgrad and wgrad need no transposed
+// copies: the matrix descriptors name the operand MN-major where the reduction
+// runs over memory rows (W in dgrad, both operands in wgrad).
+//
+// Adapters ride on the reduction: after the k-steps over W, each segment that
+// covers whole 16-row blocks of the tile adds ceil(rank / 64) k-steps over
+// just those accumulator columns, whose A is the adapter's B_a (A_a) and whose
+// B is the segment's rows of u (du): the sums never leave tensor memory. A
+// block that several segments share is finished in the epilogue, row by row
+// (rank multiply-adds per value). No row is ever multiplied by another
+// request's adapter, not even as a zero: an adapter that holds infinities or
+// NaN spoils its own rows only.
+//
+// wgrad's last k-step ends inside a block of 64 rows: the rows of the next
+// group, whatever they hold, are set to zero in shared memory (both operands).
+//
+// Per CTA: warps 0-7 epilogue (two accumulators of 256 columns, so it overlaps
+// the next tile's MMAs), warp 8 issues TMA loads into a six-deep ring and
+// describes each k-step in shared memory, warp 9 waits for the loads, zeroes
+// what must be zero and reports the k-step to the pair's first CTA, whose warp
+// 10 issues the MMAs. All waits are bounded (see tma.cuh).
+#include "gemm.cuh"
+#include "tma.cuh"
+
+namespace moe {
+namespace gt {
+
+using namespace tma;
+
+constexpr int BK = 64;             // reduction per k-step (128 bytes: one swizzle row)
+constexpr int BMC = 128;           // output columns per CTA (256 per pair)
+constexpr int BN = 256;            // rows per tile
+constexpr int STAGES = 6;
+constexpr int A_BYTES = BMC * BK * 2;
+constexpr int B_BYTES = BN / 2 * BK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int PROD_WARP = 8, FWD_WARP = 9, MMA_WARP = 10;
+constexpr int THREADS = 352;
+constexpr int ROW_BOX = 32;        // rows per TMA box of a K-major B operand
+constexpr int ROW_BLOCK = 8;       // row tiles that share a sweep over the output columns
+constexpr int SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
+
+// One k-step, written by the producer, read by the forwarder and the MMA warp.
+struct Step {
+  int kk;      // MMAs of K = 16 (0: none)
+  int flags;   // STEP_*
+  int n16;     // MMA width / 16
+  int arg;     // first accumulator column; STEP_FIX_TAIL: rows kept
+};
+constexpr int STEP_FIRST = 1, STEP_LAST = 2, STEP_STOP = 4;
+constexpr int STEP_FIX_TAIL = 8;  // MN-major A and B: reduction rows >= arg become zero
+
+struct Shared {
+  uint64_t full[STAGES], ready[STAGES], empty[STAGES];
+  uint64_t tmem_full[2], tmem_empty[2];
+  Step step[STAGES];
+  uint32_t tmem_base;
+  int32_t abort;
+  int32_t total;
+  int32_t lo[MAX_E], cnt[MAX_E];
+  int32_t tstart[MAX_E + 1];  // first tile of each group (fwd, dgrad)
+  int16_t order[MAX_E];       // groups by falling row count (wgrad)
+};
+static_assert(sizeof(Shared) <= 4096, "shared tables budget");
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrives on the barrier at `bar`'s offset in the pair's first CTA.
+__device__ __forceinline__ void arrive_leader(uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool try_cluster(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait with cluster scope: the peer CTA's arrivals and what it did
+// before them. Gives up after WAIT_NS or, unless `drain`, once *abort is set.
+static __device__ __noinline__ bool wait_cluster(Shared &sh, uint64_t *bar, uint32_t parity, int32_t *err,
+                                                 bool drain = false) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    if (try_cluster(bar, parity)) return true;
+    if ((spin & 255) == 0) {
+      if (!drain && *(volatile int32_t *)&sh.abort) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > WAIT_NS) {
+        atomicExch(&sh.abort, 1);
+        flag_error(err, MOE_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle, version 1. K-major: rows
+// of 128 bytes, 8-row atoms 1024 bytes apart (stride offset). MN-major: rows
+// are reduction indices of 64 output indices each; 8-row atoms 1024 bytes
+// apart along the reduction (stride offset), the next 64 output indices `lbo`
+// bytes away (leading offset).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFF);
+  d |= uint64_t((lbo >> 4) & 0x3FFF) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
+// Instruction descriptor: fp32 sums, BF16 A and B, their major-ness, N and M = 256.
+__device__ __forceinline__ constexpr uint32_t idesc_bf16(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(256 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// Arrives on `bar` in both CTAs of the pair once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+// 16 accumulator columns of the warp's 32 lanes; the wait is part of the
+// statement, so no use of the registers can be scheduled before it.
+__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&a)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+      : "r"(ta)
+      : "memory");
+}
+
+struct Tile {
+  int e;       // group
+  int row;     // first row of the output tile (fwd, dgrad: row of x / dy; wgrad: row n of dW_e)
+  int nvalid;  // output rows of the tile
+  int f0;      // first output column of the pair
+};
+
+// Tile t of the list. fwd and dgrad: group by group; a group's rows are cut
+// into equal tiles of at most bn (a multiple of 16), and up to ROW_BLOCK row
+// tiles run over one 256-column slab of W before the next slab, so W streams
+// from HBM once per ROW_BLOCK row tiles while the rows stay in L2. wgrad:
+// groups by falling row count, so the longest reductions start first.
+template <int MODE>
+__device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &a, int t) {
+  Tile x;
+  const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
+  if (MODE == GEMM_WGRAD) {
+    const int NT = (a.NC + BN - 1) / BN;
+    const int g = t / (FT * NT), rem = t - g * FT * NT;
+    x.e = sh.order[g];
+    x.f0 = rem % FT * 2 * BMC;
+    x.row = rem / FT * BN;
+    x.nvalid = min(BN, a.NC - x.row);
+  } else {
+    int lo_e = 0, hi_e = a.groups;  // largest e with tstart[e] <= t
+    while (hi_e - lo_e > 1) {
+      const int mid = (lo_e + hi_e) >> 1;
+      if (sh.tstart[mid] <= t) lo_e = mid; else hi_e = mid;
+    }
+    const int cnt = sh.cnt[lo_e], idx = t - sh.tstart[lo_e];
+    const int rt = (cnt + a.bn - 1) / a.bn;
+    const int w = ((cnt + rt - 1) / rt + 15) & ~15;
+    const int blk = idx / (ROW_BLOCK * FT), rem = idx - blk * ROW_BLOCK * FT;
+    const int nr = min(ROW_BLOCK, rt - blk * ROW_BLOCK);
+    const int f = rem / nr, r = blk * ROW_BLOCK + rem - f * nr;
+    x.e = lo_e;
+    x.f0 = f * 2 * BMC;
+    x.row = sh.lo[lo_e] + r * w;
+    x.nvalid = min(w, cnt - r * w);
+  }
+  return x;
+}
+
+// The adapters' part of a block of n <= 16 rows that several segments share
+// (a block of one segment has it in its sums already): v[j] gets the dot
+// product of u (du) of row + j with row f of that row's B_a (column f of A_a).
+template <int MODE>
+__device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
+  int lo = 0, hi = a.segs;  // the first segment that ends behind `row`
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.offsets[mid + 1] > row) hi = mid; else lo = mid + 1;
+  }
+  if (lo >= a.segs || a.offsets[lo + 1] >= row + n) return;
+  const bool in = f < a.M;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= n) break;
+    while (lo < a.segs && a.offsets[lo + 1] <= row + j) ++lo;
+    const int ad = lo < a.segs && a.offsets[lo] <= row + j ? a.adapter[lo] : -1;
+    if (ad < 0 || ad >= a.n_adapters || !in) continue;
+    const uint4 *u = reinterpret_cast<const uint4 *>(a.ext_b + int64_t(row + j) * a.rank);
+    float d = 0.f;
+    if (MODE == GEMM_FWD) {
+      const uint4 *b = reinterpret_cast<const uint4 *>(a.ext_a + (int64_t(ad) * a.M + f) * a.rank);
+#pragma unroll 2
+      for (int i = 0; i < a.rank / 8; ++i) {
+        const uint4 x = b[i], y = u[i];
+        d = fmaf(bf16_lo(x.x), bf16_lo(y.x), d); d = fmaf(bf16_hi(x.x), bf16_hi(y.x), d);
+        d = fmaf(bf16_lo(x.y), bf16_lo(y.y), d); d = fmaf(bf16_hi(x.y), bf16_hi(y.y), d);
+        d = fmaf(bf16_lo(x.z), bf16_lo(y.z), d); d = fmaf(bf16_hi(x.z), bf16_hi(y.z), d);
+        d = fmaf(bf16_lo(x.w), bf16_lo(y.w), d); d = fmaf(bf16_hi(x.w), bf16_hi(y.w), d);
+      }
+    } else {
+      const uint16_t *b = a.ext_a + int64_t(ad) * a.rank * a.M + f;
+      for (int i = 0; i < a.rank / 8; ++i) {
+        const uint4 y = u[i];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          d = fmaf(bf16_to_f(b[int64_t(8 * i + 2 * q) * a.M]), bf16_lo(w[q]), d);
+          d = fmaf(bf16_to_f(b[int64_t(8 * i + 2 * q + 1) * a.M]), bf16_hi(w[q]), d);
+        }
+      }
+    }
+    v[j] = __float_as_uint(__uint_as_float(v[j]) + d);
+  }
+}
+
+// The pair's i-th tile, in a snake over the pairs.
+__device__ __forceinline__ int sched_pos(int i) {
+  const int G = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1;
+  return i * G + ((i & 1) ? G - 1 - c : c);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    gemm_kernel(const TcGemmArgs a, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_ea, const __grid_constant__ CUtensorMap tm_eb) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- prologue: barriers, tensor memory, tile table
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.ready[s], 2);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.tmem_full[b], 1);
+      mbar_init(&sh.tmem_empty[b], 2 * EPI_WARPS);
+    }
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (warp == 0) {
+    int v[8], local = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      v[i] = 0;
+      if (e < a.groups) {
+        const int o0 = a.adapter ? 0 : a.offsets[e], o1 = a.adapter ? a.offsets[a.segs] : a.offsets[e + 1];
+        bad |= o0 < 0 || o1 < o0 || o1 > a.R;
+        const int lo = min(max(o0, 0), a.R), cnt = max(0, min(o1, a.R) - lo);
+        sh.lo[e] = lo;
+        sh.cnt[e] = cnt;
+        v[i] = (cnt + a.bn - 1) / a.bn * FT;
+      }
+      local += v[i];
+    }
+    if (bad) flag_error(a.err, MOE_DEVERR_OFFSETS);
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    int run = incl - local;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      if (e < a.groups) sh.tstart[e] = run;
+      run += v[i];
+    }
+    if (lane == 31) {
+      sh.tstart[a.groups] = incl;
+      sh.total = MODE == GEMM_WGRAD ? a.groups * FT * ((a.NC + BN - 1) / BN) : incl;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (MODE == GEMM_WGRAD && tid < a.groups) {
+    const int mine = sh.cnt[tid];
+    int r = 0;
+    for (int e = 0; e < a.groups; ++e) r += sh.cnt[e] > mine || (sh.cnt[e] == mine && e < tid);
+    sh.order[r] = int16_t(tid);
+  }
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const int total = sh.total;
+
+  if (warp < EPI_WARPS) {
+    // ================================================================ epilogue
+    const int q = warp & 3, part = warp >> 2;
+    const bool odd = lane & 1;
+    for (int i = 0;; ++i) {
+      const int t = sched_pos(i);
+      if (t >= total) break;
+      const Tile tl = decode_tile<MODE>(sh, a, t);
+      const int b = i & 1;
+      if (!__all_sync(0xffffffffu, wait_cluster(sh, &sh.tmem_full[b], (i >> 1) & 1, a.err))) break;
+      tc_fence_after();
+      const int f = tl.f0 + int(rank) * BMC + q * 32 + lane;
+      const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
+      const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
+      const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
+      for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) {
+        uint32_t v[16];
+        tmem_ld16(tb + j0, v);
+        if (zero) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0;
+        }
+        const int n = min(16, tl.nvalid - j0);
+        if (MODE != GEMM_WGRAD && a.adapter) add_shared_block<MODE>(a, tl.row + j0, n, f, v);
+        if (a.out_f32) {
+          float *o = static_cast<float *>(a.out) + base + int64_t(j0) * a.ldo;
+          if (f < a.M) {
+            if (a.accumulate) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (j < n) v[j] = __float_as_uint(__uint_as_float(v[j]) + o[j * a.ldo]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < n) o[j * a.ldo] = __uint_as_float(v[j]);
+          }
+        } else {
+          // two rows per store: neighbouring lanes swap one value each, so an
+          // even lane holds columns f, f+1 of row j and an odd lane f-1, f of row j+1
+          uint16_t *o = static_cast<uint16_t *>(a.out) + base + int64_t(j0) * a.ldo;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const uint32_t pk = odd ? pack_bf16x2(__uint_as_float(got), __uint_as_float(keep))
+                                    : pack_bf16x2(__uint_as_float(keep), __uint_as_float(got));
+            const int jr = j + (odd ? 1 : 0);
+            if (jr < n && f < a.M) *reinterpret_cast<uint32_t *>(o + jr * a.ldo - (odd ? 1 : 0)) = pk;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
+    }
+  } else if (warp == PROD_WARP) {
+    // ================================================================ producer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      auto slot = [&]() {  // waits until the ring's next slot is free
+        ok = ok && wait_cluster(sh, &sh.empty[it % STAGES], ((it / STAGES) & 1) ^ 1, a.err);
+        return ok;
+      };
+      for (int i = 0; ok; ++i) {
+        const int t = sched_pos(i);
+        if (t >= total) break;
+        const Tile tl = decode_tile<MODE>(sh, a, t);
+        const int n16 = (tl.nvalid + 15) >> 4, half = n16 * 8;  // rows (wgrad: columns of dy) per CTA
+        const int f = tl.f0 + int(rank) * BMC, r0 = tl.row + int(rank) * half;
+        const int red = MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD;
+        const int KS = (red + BK - 1) / BK;
+        // adapters: the first segment that ends behind the tile's first row
+        int sg = 0;
+        int nsteps = MODE == GEMM_WGRAD && KS == 0 ? 1 : KS;
+        if (MODE != GEMM_WGRAD && a.adapter) {
+          int lo_s = 0, hi_s = a.segs;
+          while (lo_s < hi_s) {
+            const int mid = (lo_s + hi_s) >> 1;
+            if (a.offsets[mid + 1] > tl.row) hi_s = mid; else lo_s = mid + 1;
+          }
+          sg = lo_s;
+        }
+        // finds the next segment with an adapter that has whole 16-row blocks of the tile
+        int seg_lo = 0, seg_hi = 0, seg_a = -1;
+        auto next_seg = [&]() {
+          if (MODE == GEMM_WGRAD || !a.adapter) return false;
+          for (; sg < a.segs; ++sg) {
+            const int o0 = a.offsets[sg];
+            if (o0 >= tl.row + tl.nvalid) return false;
+            const int o1 = a.offsets[sg + 1], ad = a.adapter[sg];
+            seg_lo = (max(o0 - tl.row, 0) + 15) & ~15;
+            seg_hi = o1 - tl.row >= tl.nvalid ? n16 * 16 : (o1 - tl.row) & ~15;
+            seg_a = ad;
+            if (seg_hi > seg_lo && ad >= 0 && ad < a.n_adapters) { ++sg; return true; }
+          }
+          return false;
+        };
+        bool more = next_seg();
+        for (int ks = 0; ks < nsteps && slot(); ++ks) {
+          const int s = it % STAGES;
+          uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
+          Step st;
+          const int left = min(BK, red - ks * BK);
+          st.kk = max(0, (left + 15) >> 4);
+          st.flags = (ks == 0 ? STEP_FIRST : 0) | (ks + 1 == nsteps && !more ? STEP_LAST : 0);
+          st.n16 = n16;
+          st.arg = 0;
+          if (MODE == GEMM_WGRAD && (left & 15)) {
+            st.flags |= STEP_FIX_TAIL;
+            st.arg = left;
+          }
+          sh.step[s] = st;
+          if (st.kk == 0) {
+            mbar_arrive(&sh.full[s]);
+          } else if (MODE == GEMM_WGRAD) {
+            const int row = sh.lo[tl.e] + ks * BK;
+            const int nb = (half + 63) >> 6;
+            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * 8192);
+            tma_load_2d(sa, &tm_a, f, row, &sh.full[s]);
+            tma_load_2d(sa + 8192, &tm_a, f + 64, row, &sh.full[s]);
+            for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * 8192, &tm_b, r0 + j * 64, row, &sh.full[s]);
+          } else {
+            const int nb = (half + ROW_BOX - 1) / ROW_BOX;
+            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * ROW_BOX * BK * 2);
+            if (MODE == GEMM_FWD) {
+              tma_load_3d(sa, &tm_a, ks * BK, f, tl.e, &sh.full[s]);
+            } else {
+              tma_load_3d(sa, &tm_a, f, ks * BK, tl.e, &sh.full[s]);
+              tma_load_3d(sa + 8192, &tm_a, f + 64, ks * BK, tl.e, &sh.full[s]);
+            }
+            for (int j = 0; j < nb; ++j)
+              tma_load_2d(sb + j * ROW_BOX * BK * 2, &tm_b, ks * BK, r0 + j * ROW_BOX, &sh.full[s]);
+          }
+          ++it;
+        }
+        while (more && ok) {
+          const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
+          const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
+          more = next_seg();
+          for (int j0 = 0; j0 < a.rank && slot(); j0 += BK) {
+            const int s = it % STAGES;
+            uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
+            Step st;
+            st.kk = (min(BK, a.rank - j0) + 15) >> 4;
+            st.flags = j0 + BK >= a.rank && !more ? STEP_LAST : 0;
+            st.n16 = w16;
+            st.arg = col;
+            sh.step[s] = st;
+            const int nb = (whalf + ROW_BOX - 1) / ROW_BOX;
+            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * ROW_BOX * BK * 2);
+            if (MODE == GEMM_FWD) {
+              tma_load_3d(sa, &tm_ea, j0, f, ad, &sh.full[s]);
+            } else {
+              tma_load_3d(sa, &tm_ea, f, j0, ad, &sh.full[s]);
+              tma_load_3d(sa + 8192, &tm_ea, f + 64, j0, ad, &sh.full[s]);
+            }
+            for (int j = 0; j < nb; ++j)
+              tma_load_2d(sb + j * ROW_BOX * BK * 2, &tm_eb, j0, er0 + j * ROW_BOX, &sh.full[s]);
+            ++it;
+          }
+        }
+      }
+      int first = it > STAGES ? it - STAGES : 0;  // the oldest step whose slot may still be in use
+      if (ok && slot()) {
+        sh.step[it % STAGES] = Step{0, STEP_STOP, 0, 0};
+        mbar_arrive(&sh.full[it % STAGES]);
+        first = it >= STAGES ? it - STAGES + 1 : 0;  // slot() saw the one before the stop's slot through
+      }
+      // every load has landed and every MMA that reads it (in either CTA) is
+      // done, before shared memory is given up
+      for (int j = first; j < it; ++j) {
+        wait_cluster(sh, &sh.full[j % STAGES], (j / STAGES) & 1, a.err, true);
+        wait_cluster(sh, &sh.empty[j % STAGES], (j / STAGES) & 1, a.err, true);
+      }
+    }
+    __syncwarp();
+  } else if (warp == FWD_WARP) {
+    // ================================================================ forwarder
+    for (int it = 0;; ++it) {
+      const int s = it % STAGES;
+      if (!__all_sync(0xffffffffu, wait_cluster(sh, &sh.full[s], (it / STAGES) & 1, a.err))) break;
+      const Step st = sh.step[s];
+      if (MODE == GEMM_WGRAD && (st.flags & STEP_FIX_TAIL)) {
+        uint8_t *sa = smem + s * STAGE_BYTES;
+        const int hi = st.arg, rows = st.kk * 16 - hi;
+        // 64-column blocks of 64 rows x 128 bytes: two of A, up to two of B
+        const int nblk = 2 + ((st.n16 * 8 + 63) >> 6);
+        for (int p = lane; p < nblk * rows * 8; p += 32) {
+          const int blk = p / (rows * 8), rr = p - blk * rows * 8;
+          *reinterpret_cast<uint4 *>(sa + blk * 8192 + hi * 128 + rr * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) arrive_leader(&sh.ready[s]);
+      if (st.flags & STEP_STOP) break;
+    }
+  } else if (warp == MMA_WARP && rank == 0) {
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      constexpr bool A_MN = MODE != GEMM_FWD, B_MN = MODE == GEMM_WGRAD;
+      constexpr uint32_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;  // 16 reduction indices on
+      int tl = 0;
+      for (int it = 0;; ++it) {
+        const int s = it % STAGES;
+        if (!wait_cluster(sh, &sh.ready[s], (it / STAGES) & 1, a.err)) break;
+        const Step st = sh.step[s];
+        if (st.flags & STEP_STOP) break;
+        const int b = tl & 1;
+        if ((st.flags & STEP_FIRST) && !wait_cluster(sh, &sh.tmem_empty[b], ((tl >> 1) & 1) ^ 1, a.err)) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
+        const uint64_t da = sw128_desc(sa, 8192), db = sw128_desc(sa + A_BYTES, 8192);
+        const uint32_t idesc = idesc_bf16(A_MN, B_MN) | (uint32_t(st.n16 * 2) << 17);
+        const uint32_t d = tmem + b * BN + (MODE == GEMM_WGRAD ? 0 : st.arg);
+        for (int kk = 0; kk < st.kk; ++kk)
+          mma_pair(d, da + kk * KA, db + kk * KB, idesc, !(st.flags & STEP_FIRST) || kk > 0);
+        commit_pair(&sh.empty[s]);
+        if (st.flags & STEP_LAST) {
+          commit_pair(&sh.tmem_full[b]);
+          ++tl;
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+}  // namespace gt
+
+// A BF16 tensor map over up to three dimensions, 128-byte swizzle, box
+// (64, box1, 1); out-of-range elements read as zero.
+static bool map_bf16(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t ld1, int64_t d2, int64_t ld2,
+                     int box1) {
+  const cuuint64_t dims[3] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2 > 0 ? d2 : 1)};
+  const cuuint64_t strides[2] = {cuuint64_t(ld1) * 2, cuuint64_t(ld2) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box1), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 > 0 ? 3 : 2, const_cast<void *>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what) {
+  CUtensorMap ta, tb, tea, teb;
+  bool ok = true;
+  const int N = MODE == GEMM_FWD ? a.M : MODE == GEMM_DGRAD ? a.KD : a.NC;
+  const int K = MODE == GEMM_FWD ? a.KD : a.M;
+  if (MODE == GEMM_WGRAD) {
+    ok &= map_bf16(&ta, op.a, K, a.R, op.lda, 0, 0, 64);
+    ok &= map_bf16(&tb, op.b, N, a.R, op.ldb, 0, 0, 64);
+  } else {
+    ok &= map_bf16(&ta, op.a, K, N, op.lda, a.groups, op.a_gstride, MODE == GEMM_FWD ? gt::BMC : 64);
+    ok &= map_bf16(&tb, op.b, MODE == GEMM_FWD ? K : N, a.R, op.ldb, 0, 0, gt::ROW_BOX);
+  }
+  tea = ta;
+  teb = tb;
+  if (a.adapter) {
+    if (MODE == GEMM_FWD)
+      ok &= map_bf16(&tea, a.ext_a, a.rank, N, a.rank, a.n_adapters, int64_t(N) * a.rank, gt::BMC);
+    else
+      ok &= map_bf16(&tea, a.ext_a, K, a.rank, K, a.n_adapters, int64_t(K) * a.rank, 64);
+    ok &= map_bf16(&teb, a.ext_b, a.rank, a.R, a.rank, 0, 0, gt::ROW_BOX);
+  }
+  if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE>), gt::SMEM, what);
+  if (st != MOE_OK) return st;
+  const int grid = sm_count() & ~1;
+  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, ta, tb, tea, teb);
+  if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what) {
+  int dev = 0, major = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (major != 10) return set_error(MOE_ERR_UNSUPPORTED, "%s: needs sm_100", what);
+  if (!tensor_map_encoder()) return set_error(MOE_ERR_UNSUPPORTED, "%s: cuTensorMapEncodeTiled is not available", what);
+  return mode == GEMM_FWD     ? launch_mode<GEMM_FWD>(a, op, s, what)
+         : mode == GEMM_DGRAD ? launch_mode<GEMM_DGRAD>(a, op, s, what)
+                              : launch_mode<GEMM_WGRAD>(a, op, s, what);
+}
+
+}  // namespace moe
