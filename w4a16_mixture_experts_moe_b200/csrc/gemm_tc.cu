@@ -33,10 +33,14 @@
 // group, whatever they hold, are set to zero in shared memory (both operands).
 //
 // Per CTA: warps 0-7 epilogue (two accumulators of 256 columns, so it overlaps
-// the next tile's MMAs), warp 8 issues TMA loads into a six-deep ring and
-// describes each k-step in shared memory, warp 9 waits for the loads, zeroes
-// what must be zero and reports the k-step to the pair's first CTA, whose warp
-// 10 issues the MMAs. All waits are bounded (see tma.cuh).
+// the next tile's MMAs), warp 8 issues TMA loads into a six-deep ring, warp 9
+// zeroes the tail of wgrad's last k-steps, and in the pair's first CTA warp 11
+// waits for each k-step and hands it over a named barrier to warp 10, which
+// issues the MMAs of both CTAs and touches no memory between them (a warp's
+// shared-memory operations behind its MMAs are held until those finish, which
+// would drain the tensor core at every k-step). The loads of both CTAs count their bytes on the
+// first CTA's barrier (a load of a pair may name its peer's), so a k-step
+// costs no message between the CTAs. All waits are bounded (see tma.cuh).
 #include "gemm.cuh"
 #include "tma.cuh"
 
@@ -53,24 +57,28 @@ constexpr int A_BYTES = BMC * BK * 2;
 constexpr int B_BYTES = BN / 2 * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;
-constexpr int PROD_WARP = 8, FWD_WARP = 9, MMA_WARP = 10;
-constexpr int THREADS = 352;
+constexpr int PROD_WARP = 8, FIX_WARP = 9, MMA_WARP = 10, WAIT_WARP = 11;
+constexpr int THREADS = 384;
+constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
+constexpr int HAND_STOP = 31;
 constexpr int ROW_BOX = 32;        // rows per TMA box of a K-major B operand
-constexpr int ROW_BLOCK = 8;       // row tiles that share a sweep over the output columns
+constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the output columns
 constexpr int SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
 
-// One k-step, written by the producer, read by the forwarder and the MMA warp.
+// One k-step, written by the first CTA's producer for its waiter.
 struct Step {
   int kk;      // MMAs of K = 16 (0: none)
   int flags;   // STEP_*
   int n16;     // MMA width / 16
-  int arg;     // first accumulator column; STEP_FIX_TAIL: rows kept
+  int col;     // first accumulator column
 };
 constexpr int STEP_FIRST = 1, STEP_LAST = 2, STEP_STOP = 4;
-constexpr int STEP_FIX_TAIL = 8;  // MN-major A and B: reduction rows >= arg become zero
+constexpr int STEP_EXT = 16;      // an adapter's k-step: its own width and first column
+constexpr int STEP_FIX_TAIL = 8;  // wgrad: the reduction ends inside the last MMA's 16 rows; warp 9 zeroes the rest
 
 struct Shared {
-  uint64_t full[STAGES], ready[STAGES], empty[STAGES];
+  uint64_t full[STAGES], empty[STAGES];        // full: the first CTA's counts both CTAs' loads
+  uint64_t landed[STAGES], fixed[STAGES];      // k-steps with a tail to zero: this CTA's loads / both CTAs' zeroing
   uint64_t tmem_full[2], tmem_empty[2];
   Step step[STAGES];
   uint32_t tmem_base;
@@ -100,35 +108,48 @@ __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
       " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ bool try_cluster(uint64_t *b, uint32_t parity) {
-  uint32_t ok;
+// TMA tile loads whose bytes are counted on a barrier of the pair's first CTA
+// (`bar`: its shared::cluster address).
+__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *tm, int c0, int c1, uint32_t bar) {
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(b)), "r"(parity)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
-  return ok != 0;
+}
+__device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *tm, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_4d(void *dst, const CUtensorMap *tm, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
 }
 
-// Bounded wait with cluster scope: the peer CTA's arrivals and what it did
-// before them. Gives up after WAIT_NS or, unless `drain`, once *abort is set.
-static __device__ __noinline__ bool wait_cluster(Shared &sh, uint64_t *bar, uint32_t parity, int32_t *err,
-                                                 bool drain = false) {
-  uint64_t t0 = 0;
-  for (uint32_t spin = 1;; ++spin) {
-    if (try_cluster(bar, parity)) return true;
-    if ((spin & 255) == 0) {
-      if (!drain && *(volatile int32_t *)&sh.abort) return false;
-      const uint64_t now = globaltimer();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > WAIT_NS) {
-        atomicExch(&sh.abort, 1);
-        flag_error(err, MOE_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
+// Bounded wait (see tma::wait_bounded), its first poll inline.
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, int32_t *err, bool drain = false) {
+  return mbar_try(bar, parity) || wait_bounded(&sh.abort, bar, parity, err, drain);
+}
+
+// Waiter and MMA warp meet: returns how many of the 64 threads voted.
+__device__ __forceinline__ int handoff(bool vote) {
+  uint32_t cnt;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n bar.red.popc.u32 %0, %2, 64, p;\n}\n"
+               : "=r"(cnt)
+               : "r"(uint32_t(vote)), "n"(HANDOFF_BAR)
+               : "memory");
+  return int(cnt);
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle, version 1. K-major: rows
@@ -176,6 +197,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&a)[16]) {
       : "r"(ta)
       : "memory");
 }
+
+// Tensor maps of one launch. A k-step's operand is one load where the layout
+// allows it: each load instruction costs the TMA unit time of its own (five
+// loads a k-step instead of two took the wide product from 1.54 to 1.77 ms).
+struct Maps {
+  CUtensorMap a;   // fwd: 128 rows of W. dgrad, wgrad: 64 reduction rows x 64 columns (x 2 blocks if a_wide)
+  CUtensorMap b;   // fwd, dgrad: 32 rows. wgrad: 64 reduction rows x 64 columns
+  CUtensorMap bw;  // the same for a full half tile: 128 rows; wgrad: 2 blocks of 64 columns (if b_wide)
+  CUtensorMap ea, eb;  // adapters: like a and b
+  int a_wide, b_wide;
+};
 
 struct Tile {
   int e;       // group
@@ -274,8 +306,7 @@ __device__ __forceinline__ int sched_pos(int i) {
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    gemm_kernel(const TcGemmArgs a, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                const __grid_constant__ CUtensorMap tm_ea, const __grid_constant__ CUtensorMap tm_eb) {
+    gemm_kernel(const TcGemmArgs a, const __grid_constant__ Maps m) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES);
@@ -289,8 +320,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.ready[s], 2);
       mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.landed[s], 1);
+      mbar_init(&sh.fixed[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.tmem_full[b], 1);
@@ -363,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (t >= total) break;
       const Tile tl = decode_tile<MODE>(sh, a, t);
       const int b = i & 1;
-      if (!__all_sync(0xffffffffu, wait_cluster(sh, &sh.tmem_full[b], (i >> 1) & 1, a.err))) break;
+      if (!__all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (i >> 1) & 1, a.err))) break;
       tc_fence_after();
       const int f = tl.f0 + int(rank) * BMC + q * 32 + lane;
       const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
@@ -415,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int it = 0;
       bool ok = true;
       auto slot = [&]() {  // waits until the ring's next slot is free
-        ok = ok && wait_cluster(sh, &sh.empty[it % STAGES], ((it / STAGES) & 1) ^ 1, a.err);
+        ok = ok && wait(sh, &sh.empty[it % STAGES], ((it / STAGES) & 1) ^ 1, a.err);
         return ok;
       };
       for (int i = 0; ok; ++i) {
@@ -461,36 +493,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           st.kk = max(0, (left + 15) >> 4);
           st.flags = (ks == 0 ? STEP_FIRST : 0) | (ks + 1 == nsteps && !more ? STEP_LAST : 0);
           st.n16 = n16;
-          st.arg = 0;
-          if (MODE == GEMM_WGRAD && (left & 15)) {
-            st.flags |= STEP_FIX_TAIL;
-            st.arg = left;
-          }
+          st.col = 0;
+          if (MODE == GEMM_WGRAD && (left & 15)) st.flags |= STEP_FIX_TAIL;
           sh.step[s] = st;
-          if (st.kk == 0) {
-            mbar_arrive(&sh.full[s]);
-          } else if (MODE == GEMM_WGRAD) {
-            const int row = sh.lo[tl.e] + ks * BK;
-            const int nb = (half + 63) >> 6;
-            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * 8192);
-            tma_load_2d(sa, &tm_a, f, row, &sh.full[s]);
-            tma_load_2d(sa + 8192, &tm_a, f + 64, row, &sh.full[s]);
-            for (int j = 0; j < nb; ++j) tma_load_2d(sb + j * 8192, &tm_b, r0 + j * 64, row, &sh.full[s]);
+          const uint32_t bar = leader_addr(&sh.full[s]);
+          if (MODE == GEMM_WGRAD) {
+            const int row = sh.lo[tl.e] + ks * BK, nb = (half + 63) >> 6, bytes = A_BYTES + nb * 8192;
+            const bool fix = st.flags & STEP_FIX_TAIL;
+            uint32_t on = bar;
+            if (st.kk == 0) {
+              if (rank == 0) mbar_arrive(&sh.full[s]);
+            } else if (fix) {  // the zeroing warp sees this CTA's loads through, the MMA warp waits for both CTAs' zeroing
+              mbar_arrive_expect_tx(&sh.landed[s], bytes);
+              if (rank == 0) mbar_arrive(&sh.full[s]);
+              on = smem_u32(&sh.landed[s]);
+            } else if (rank == 0) {
+              mbar_arrive_expect_tx(&sh.full[s], 2 * bytes);
+            }
+            if (st.kk > 0) {
+              if (m.a_wide) {
+                pair_load_3d(sa, &m.a, 0, row, f >> 6, on);
+              } else {
+                pair_load_2d(sa, &m.a, f, row, on);
+                pair_load_2d(sa + 8192, &m.a, f + 64, row, on);
+              }
+              if (m.b_wide && half == BN / 2) {
+                pair_load_3d(sb, &m.bw, 0, row, r0 >> 6, on);
+              } else {
+                for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * 8192, &m.b, r0 + j * 64, row, on);
+              }
+            }
           } else {
             const int nb = (half + ROW_BOX - 1) / ROW_BOX;
-            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * ROW_BOX * BK * 2);
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + nb * ROW_BOX * BK * 2));
             if (MODE == GEMM_FWD) {
-              tma_load_3d(sa, &tm_a, ks * BK, f, tl.e, &sh.full[s]);
+              pair_load_3d(sa, &m.a, ks * BK, f, tl.e, bar);
+            } else if (m.a_wide) {
+              pair_load_4d(sa, &m.a, 0, ks * BK, f >> 6, tl.e, bar);
             } else {
-              tma_load_3d(sa, &tm_a, f, ks * BK, tl.e, &sh.full[s]);
-              tma_load_3d(sa + 8192, &tm_a, f + 64, ks * BK, tl.e, &sh.full[s]);
+              pair_load_3d(sa, &m.a, f, ks * BK, tl.e, bar);
+              pair_load_3d(sa + 8192, &m.a, f + 64, ks * BK, tl.e, bar);
             }
-            for (int j = 0; j < nb; ++j)
-              tma_load_2d(sb + j * ROW_BOX * BK * 2, &tm_b, ks * BK, r0 + j * ROW_BOX, &sh.full[s]);
+            if (nb * ROW_BOX == BN / 2) {
+              pair_load_2d(sb, &m.bw, ks * BK, r0, bar);
+            } else {
+              for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.b, ks * BK, r0 + j * ROW_BOX, bar);
+            }
           }
           ++it;
         }
-        while (more && ok) {
+        if constexpr (MODE != GEMM_WGRAD) while (more && ok) {
           const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
           const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
           more = next_seg();
@@ -499,20 +551,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
             Step st;
             st.kk = (min(BK, a.rank - j0) + 15) >> 4;
-            st.flags = j0 + BK >= a.rank && !more ? STEP_LAST : 0;
+            st.flags = STEP_EXT | (j0 + BK >= a.rank && !more ? STEP_LAST : 0);
             st.n16 = w16;
-            st.arg = col;
+            st.col = col;
             sh.step[s] = st;
             const int nb = (whalf + ROW_BOX - 1) / ROW_BOX;
-            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + nb * ROW_BOX * BK * 2);
+            const uint32_t bar = leader_addr(&sh.full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + nb * ROW_BOX * BK * 2));
             if (MODE == GEMM_FWD) {
-              tma_load_3d(sa, &tm_ea, j0, f, ad, &sh.full[s]);
+              pair_load_3d(sa, &m.ea, j0, f, ad, bar);
             } else {
-              tma_load_3d(sa, &tm_ea, f, j0, ad, &sh.full[s]);
-              tma_load_3d(sa + 8192, &tm_ea, f + 64, j0, ad, &sh.full[s]);
+              pair_load_3d(sa, &m.ea, f, j0, ad, bar);
+              pair_load_3d(sa + 8192, &m.ea, f + 64, j0, ad, bar);
             }
-            for (int j = 0; j < nb; ++j)
-              tma_load_2d(sb + j * ROW_BOX * BK * 2, &tm_eb, j0, er0 + j * ROW_BOX, &sh.full[s]);
+            for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.eb, j0, er0 + j * ROW_BOX, bar);
             ++it;
           }
         }
@@ -520,66 +572,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int first = it > STAGES ? it - STAGES : 0;  // the oldest step whose slot may still be in use
       if (ok && slot()) {
         sh.step[it % STAGES] = Step{0, STEP_STOP, 0, 0};
-        mbar_arrive(&sh.full[it % STAGES]);
+        if (rank == 0) mbar_arrive(&sh.full[it % STAGES]);
         first = it >= STAGES ? it - STAGES + 1 : 0;  // slot() saw the one before the stop's slot through
       }
-      // every load has landed and every MMA that reads it (in either CTA) is
-      // done, before shared memory is given up
-      for (int j = first; j < it; ++j) {
-        wait_cluster(sh, &sh.full[j % STAGES], (j / STAGES) & 1, a.err, true);
-        wait_cluster(sh, &sh.empty[j % STAGES], (j / STAGES) & 1, a.err, true);
-      }
+      // every MMA that reads shared memory (in either CTA) is done, so every
+      // load has landed, before shared memory is given up
+      for (int j = first; j < it; ++j) wait(sh, &sh.empty[j % STAGES], (j / STAGES) & 1, a.err, true);
     }
     __syncwarp();
-  } else if (warp == FWD_WARP) {
-    // ================================================================ forwarder
-    for (int it = 0;; ++it) {
-      const int s = it % STAGES;
-      if (!__all_sync(0xffffffffu, wait_cluster(sh, &sh.full[s], (it / STAGES) & 1, a.err))) break;
-      const Step st = sh.step[s];
-      if (MODE == GEMM_WGRAD && (st.flags & STEP_FIX_TAIL)) {
-        uint8_t *sa = smem + s * STAGE_BYTES;
-        const int hi = st.arg, rows = st.kk * 16 - hi;
+  } else if (warp == FIX_WARP) {
+    // ================================================================ tails
+    if (MODE == GEMM_WGRAD) {
+      int it = 0;
+      uint32_t phase = 0;  // of landed[], one bit per slot
+      for (int i = 0;; ++i) {
+        const int t = sched_pos(i);
+        if (t >= total) break;
+        const Tile tl = decode_tile<MODE>(sh, a, t);
+        const int red = sh.cnt[tl.e], left = red & 15;
+        it += red > 0 ? (red + BK - 1) / BK : 1;
+        if (left == 0) continue;
+        const int s = (it - 1) % STAGES;
+        if (!__all_sync(0xffffffffu, wait(sh, &sh.landed[s], (phase >> s) & 1, a.err))) break;
+        phase ^= 1u << s;
         // 64-column blocks of 64 rows x 128 bytes: two of A, up to two of B
-        const int nblk = 2 + ((st.n16 * 8 + 63) >> 6);
+        uint8_t *sa = smem + s * STAGE_BYTES;
+        const int hi = (red - 1) % BK + 1, rows = 16 - left;
+        const int nblk = 2 + ((((tl.nvalid + 15) >> 4) * 8 + 63) >> 6);
         for (int p = lane; p < nblk * rows * 8; p += 32) {
           const int blk = p / (rows * 8), rr = p - blk * rows * 8;
           *reinterpret_cast<uint4 *>(sa + blk * 8192 + hi * 128 + rr * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh.fixed[s]);
       }
-      __syncwarp();
-      if (lane == 0) arrive_leader(&sh.ready[s]);
-      if (st.flags & STEP_STOP) break;
+    }
+  } else if (warp == WAIT_WARP && rank == 0) {
+    // ================================================================ waiter
+    int tl = 0;
+    uint32_t phase = 0;  // of fixed[], one bit per slot
+    for (int it = 0;; ++it) {
+      const int s = it % STAGES;
+      bool ok = wait(sh, &sh.full[s], (it / STAGES) & 1, a.err);
+      const Step st = sh.step[s];
+      if (ok && !(st.flags & STEP_STOP)) {
+        if (MODE == GEMM_WGRAD && (st.flags & STEP_FIX_TAIL)) {
+          ok = wait(sh, &sh.fixed[s], (phase >> s) & 1, a.err);
+          phase ^= 1u << s;
+        }
+        if (ok && (st.flags & STEP_FIRST)) ok = wait(sh, &sh.tmem_empty[tl & 1], ((tl >> 1) & 1) ^ 1, a.err);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      const bool stop = !ok || (st.flags & STEP_STOP);
+      const int kind = (st.flags & STEP_FIRST) ? 1 : (st.flags & STEP_EXT) ? 2 : 0, last = (st.flags & STEP_LAST) ? 1 : 0;
+      handoff(lane < (stop ? HAND_STOP : kind * 10 + last * 5 + st.kk));
+      if (stop) break;
+      if (kind) handoff(lane < st.n16);
+      if (kind == 2) handoff(lane < st.col >> 4);
+      tl += last;
     }
   } else if (warp == MMA_WARP && rank == 0) {
     // ================================================================ MMA issuer
-    if (lane == 0) {
-      constexpr bool A_MN = MODE != GEMM_FWD, B_MN = MODE == GEMM_WGRAD;
-      constexpr uint32_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;  // 16 reduction indices on
-      int tl = 0;
-      for (int it = 0;; ++it) {
-        const int s = it % STAGES;
-        if (!wait_cluster(sh, &sh.ready[s], (it / STAGES) & 1, a.err)) break;
-        const Step st = sh.step[s];
-        if (st.flags & STEP_STOP) break;
-        const int b = tl & 1;
-        if ((st.flags & STEP_FIRST) && !wait_cluster(sh, &sh.tmem_empty[b], ((tl >> 1) & 1) ^ 1, a.err)) break;
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
-        const uint64_t da = sw128_desc(sa, 8192), db = sw128_desc(sa + A_BYTES, 8192);
-        const uint32_t idesc = idesc_bf16(A_MN, B_MN) | (uint32_t(st.n16 * 2) << 17);
-        const uint32_t d = tmem + b * BN + (MODE == GEMM_WGRAD ? 0 : st.arg);
-        for (int kk = 0; kk < st.kk; ++kk)
-          mma_pair(d, da + kk * KA, db + kk * KB, idesc, !(st.flags & STEP_FIRST) || kk > 0);
+    constexpr bool A_MN = MODE != GEMM_FWD, B_MN = MODE == GEMM_WGRAD;
+    constexpr uint32_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;  // 16 reduction indices on
+    int tl = 0, n16 = 0, s = 0;
+    for (;;) {
+      const int v = handoff(0);
+      if (v >= HAND_STOP) break;
+      const int kind = v / 10, last = v % 10 / 5, kk = v % 5;
+      int col = 0;
+      if (kind) n16 = handoff(0);
+      if (kind == 2) col = handoff(0) * 16;
+      tc_fence_after();
+      const uint32_t sa = smem_u32(smem) + s * STAGE_BYTES;
+      const uint64_t da = sw128_desc(sa, 8192), db = sw128_desc(sa + A_BYTES, 8192);
+      const uint32_t idesc = idesc_bf16(A_MN, B_MN) | (uint32_t(n16 * 2) << 17);
+      const uint32_t d = tmem + (tl & 1) * BN + col;
+      if (elect_one()) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < kk) mma_pair(d, da + q * KA, db + q * KB, idesc, kind != 1 || q > 0);
         commit_pair(&sh.empty[s]);
-        if (st.flags & STEP_LAST) {
-          commit_pair(&sh.tmem_full[b]);
-          ++tl;
-        }
+        if (last) commit_pair(&sh.tmem_full[tl & 1]);
       }
+      __syncwarp();
+      tl += last;
+      if (++s == STAGES) s = 0;
     }
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -593,46 +673,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 }  // namespace gt
 
-// A BF16 tensor map over up to three dimensions, 128-byte swizzle, box
-// (64, box1, 1); out-of-range elements read as zero.
-static bool map_bf16(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t ld1, int64_t d2, int64_t ld2,
-                     int box1) {
-  const cuuint64_t dims[3] = {cuuint64_t(d0), cuuint64_t(d1), cuuint64_t(d2 > 0 ? d2 : 1)};
-  const cuuint64_t strides[2] = {cuuint64_t(ld1) * 2, cuuint64_t(ld2) * 2};
-  const cuuint32_t box[3] = {64, cuuint32_t(box1), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 > 0 ? 3 : 2, const_cast<void *>(base), dims,
-                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+// A BF16 tensor map with the 128-byte swizzle: dimension 0 contiguous, the
+// others with strides in elements; out-of-range elements read as zero.
+static bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
+                     const int (&box)[4]) {
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4];
+  for (int i = 0; i < nd; ++i) {
+    d[i] = cuuint64_t(dim[i]);
+    bx[i] = cuuint32_t(box[i]);
+    es[i] = 1;
+    if (i) st[i - 1] = cuuint64_t(stride[i - 1]) * 2;
+  }
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(nd), const_cast<void *>(base), d, st, bx,
+                              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MODE>
 static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what) {
-  CUtensorMap ta, tb, tea, teb;
+  gt::Maps m = {};
   bool ok = true;
   const int N = MODE == GEMM_FWD ? a.M : MODE == GEMM_DGRAD ? a.KD : a.NC;
   const int K = MODE == GEMM_FWD ? a.KD : a.M;
-  if (MODE == GEMM_WGRAD) {
-    ok &= map_bf16(&ta, op.a, K, a.R, op.lda, 0, 0, 64);
-    ok &= map_bf16(&tb, op.b, N, a.R, op.ldb, 0, 0, 64);
-  } else {
-    ok &= map_bf16(&ta, op.a, K, N, op.lda, a.groups, op.a_gstride, MODE == GEMM_FWD ? gt::BMC : 64);
-    ok &= map_bf16(&tb, op.b, MODE == GEMM_FWD ? K : N, a.R, op.ldb, 0, 0, gt::ROW_BOX);
-  }
-  tea = ta;
-  teb = tb;
+  // Columns in whole blocks of 64 can be a dimension of their own, so that one
+  // load brings two blocks (the last block of another width would reach into
+  // the next row, and behind the last one).
+  m.a_wide = MODE != GEMM_FWD && K % 64 == 0;
+  m.b_wide = MODE == GEMM_WGRAD && N % 64 == 0;
+  if (MODE == GEMM_FWD)
+    ok &= map_bf16(&m.a, op.a, 3, {K, N, a.groups, 1}, {K, op.a_gstride, 0}, {64, gt::BMC, 1, 1});
+  else if (MODE == GEMM_DGRAD)
+    ok &= m.a_wide ? map_bf16(&m.a, op.a, 4, {64, N, K / 64, a.groups}, {K, 64, op.a_gstride}, {64, 64, 2, 1})
+                   : map_bf16(&m.a, op.a, 3, {K, N, a.groups, 1}, {K, op.a_gstride, 0}, {64, 64, 1, 1});
+  else
+    ok &= m.a_wide ? map_bf16(&m.a, op.a, 3, {64, a.R, K / 64, 1}, {op.lda, 64, 0}, {64, 64, 2, 1})
+                   : map_bf16(&m.a, op.a, 2, {K, a.R, 1, 1}, {op.lda, 0, 0}, {64, 64, 1, 1});
+  const int64_t width = MODE == GEMM_FWD ? K : N;
+  const int rows = MODE == GEMM_WGRAD ? 64 : gt::ROW_BOX;
+  ok &= map_bf16(&m.b, op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, rows, 1, 1});
+  if (MODE != GEMM_WGRAD)
+    ok &= map_bf16(&m.bw, op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, gt::BN / 2, 1, 1});
+  else if (m.b_wide)
+    ok &= map_bf16(&m.bw, op.b, 3, {64, a.R, N / 64, 1}, {op.ldb, 64, 0}, {64, 64, 2, 1});
   if (a.adapter) {
     if (MODE == GEMM_FWD)
-      ok &= map_bf16(&tea, a.ext_a, a.rank, N, a.rank, a.n_adapters, int64_t(N) * a.rank, gt::BMC);
+      ok &= map_bf16(&m.ea, a.ext_a, 3, {a.rank, N, a.n_adapters, 1}, {a.rank, int64_t(N) * a.rank, 0},
+                     {64, gt::BMC, 1, 1});
     else
-      ok &= map_bf16(&tea, a.ext_a, K, a.rank, K, a.n_adapters, int64_t(K) * a.rank, 64);
-    ok &= map_bf16(&teb, a.ext_b, a.rank, a.R, a.rank, 0, 0, gt::ROW_BOX);
+      ok &= map_bf16(&m.ea, a.ext_a, 3, {K, a.rank, a.n_adapters, 1}, {K, int64_t(K) * a.rank, 0}, {64, 64, 1, 1});
+    ok &= map_bf16(&m.eb, a.ext_b, 2, {a.rank, a.R, 1, 1}, {a.rank, 0, 0}, {64, gt::ROW_BOX, 1, 1});
   }
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE>), gt::SMEM, what);
   if (st != MOE_OK) return st;
   const int grid = sm_count() & ~1;
-  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, ta, tb, tea, teb);
+  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, m);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }

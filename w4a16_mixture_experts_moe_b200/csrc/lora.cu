@@ -91,8 +91,8 @@ template <int BJ, bool TRANS>
 __global__ void __launch_bounds__(128) shrink_kernel(const ShrinkArgs a) {
   using Cfg = ShrinkCfg<BJ, TRANS>;
   extern __shared__ __align__(16) uint16_t sm[];
-  pdl_trigger();
-  pdl_wait();
+  pdl_wait();     // in this order: the projection may start before u is there (gemm_gemv.cu), but
+  pdl_trigger();  // not before what this launch itself waits for
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     for (int s = tid; s < a.segs; s += 128) {
@@ -364,9 +364,9 @@ static int check_rows(const char *who, const char *name, const void *p, int64_t 
   return MOE_OK;
 }
 
-// Up to this many rows the projection runs as a weight stream (two passes of
-// 32 rows would read W twice from L2).
-constexpr int GEMV_MAX_T = 32;
+// Up to this many rows the projection runs as a weight stream, all rows in one
+// pass over W.
+constexpr int GEMV_MAX_T = 64;
 
 static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const int32_t *seg_adapter, int T, int S,
                              int n_adapters, int rank, int N, int K, void *out, int64_t ldo, int32_t *err) {
