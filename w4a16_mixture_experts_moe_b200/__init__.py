@@ -26,7 +26,10 @@ _LAYER_NAMES = {"ExpertBank", "Bf16Bank", "LayerBuffers", "moe_layer_forward"}
 
 def __getattr__(name):
     if name in _NATIVE_NAMES:
-        return getattr(importlib.import_module("._native", __name__), name)
-    if name in _LAYER_NAMES:
-        return getattr(importlib.import_module(".layer", __name__), name)
-    raise AttributeError(name)
+        value = getattr(importlib.import_module("._native", __name__), name)
+    elif name in _LAYER_NAMES:
+        value = getattr(importlib.import_module(".layer", __name__), name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value  # later uses skip this lookup (3 us of host time each)
+    return value

@@ -263,38 +263,46 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
     if (a.offsets[mid + 1] > row) hi = mid; else lo = mid + 1;
   }
   if (lo >= a.segs || a.offsets[lo + 1] >= row + n) return;
-  const bool in = f < a.M;
+  const int fc = min(f, a.M - 1);  // lanes past the last column repeat it (and store nothing)
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (j >= n) break;
-    while (lo < a.segs && a.offsets[lo + 1] <= row + j) ++lo;
-    const int ad = lo < a.segs && a.offsets[lo] <= row + j ? a.adapter[lo] : -1;
-    if (ad < 0 || ad >= a.n_adapters || !in) continue;
-    const uint4 *u = reinterpret_cast<const uint4 *>(a.ext_b + int64_t(row + j) * a.rank);
-    float d = 0.f;
-    if (MODE == GEMM_FWD) {
-      const uint4 *b = reinterpret_cast<const uint4 *>(a.ext_a + (int64_t(ad) * a.M + f) * a.rank);
-#pragma unroll 2
-      for (int i = 0; i < a.rank / 8; ++i) {
-        const uint4 x = b[i], y = u[i];
-        d = fmaf(bf16_lo(x.x), bf16_lo(y.x), d); d = fmaf(bf16_hi(x.x), bf16_hi(y.x), d);
-        d = fmaf(bf16_lo(x.y), bf16_lo(y.y), d); d = fmaf(bf16_hi(x.y), bf16_hi(y.y), d);
-        d = fmaf(bf16_lo(x.z), bf16_lo(y.z), d); d = fmaf(bf16_hi(x.z), bf16_hi(y.z), d);
-        d = fmaf(bf16_lo(x.w), bf16_lo(y.w), d); d = fmaf(bf16_hi(x.w), bf16_hi(y.w), d);
-      }
-    } else {
-      const uint16_t *b = a.ext_a + int64_t(ad) * a.rank * a.M + f;
-      for (int i = 0; i < a.rank / 8; ++i) {
-        const uint4 y = u[i];
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+  for (int j0 = 0; j0 < 16; j0 += 4) {  // four rows at a time, their loads together
+    if (j0 >= n) break;
+    int ad[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d = fmaf(bf16_to_f(b[int64_t(8 * i + 2 * q) * a.M]), bf16_lo(w[q]), d);
-          d = fmaf(bf16_to_f(b[int64_t(8 * i + 2 * q + 1) * a.M]), bf16_hi(w[q]), d);
+    for (int j = 0; j < 4; ++j) {
+      const int r = row + j0 + j;
+      while (lo < a.segs && a.offsets[lo + 1] <= r) ++lo;
+      ad[j] = j0 + j < n && lo < a.segs && a.offsets[lo] <= r ? a.adapter[lo] : -1;
+      if (ad[j] >= a.n_adapters) ad[j] = -1;
+    }
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < a.rank; i += 8) {
+      uint4 y[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = b[j] = make_uint4(0, 0, 0, 0);
+        if (ad[j] < 0) continue;
+        y[j] = *reinterpret_cast<const uint4 *>(a.ext_b + int64_t(row + j0 + j) * a.rank + i);
+        if (MODE == GEMM_FWD) {
+          b[j] = *reinterpret_cast<const uint4 *>(a.ext_a + (int64_t(ad[j]) * a.M + fc) * a.rank + i);
+        } else {
+          const uint16_t *c = a.ext_a + (int64_t(ad[j]) * a.rank + i) * a.M + fc;
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = c[int64_t(2 * q) * a.M] | uint32_t(c[int64_t(2 * q + 1) * a.M]) << 16;
+          b[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = fmaf(bf16_lo(b[j].x), bf16_lo(y[j].x), d[j]); d[j] = fmaf(bf16_hi(b[j].x), bf16_hi(y[j].x), d[j]);
+        d[j] = fmaf(bf16_lo(b[j].y), bf16_lo(y[j].y), d[j]); d[j] = fmaf(bf16_hi(b[j].y), bf16_hi(y[j].y), d[j]);
+        d[j] = fmaf(bf16_lo(b[j].z), bf16_lo(y[j].z), d[j]); d[j] = fmaf(bf16_hi(b[j].z), bf16_hi(y[j].z), d[j]);
+        d[j] = fmaf(bf16_lo(b[j].w), bf16_lo(y[j].w), d[j]); d[j] = fmaf(bf16_hi(b[j].w), bf16_hi(y[j].w), d[j]);
+      }
     }
-    v[j] = __float_as_uint(__uint_as_float(v[j]) + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j0 + j] = __float_as_uint(__uint_as_float(v[j0 + j]) + d[j]);
   }
 }
 

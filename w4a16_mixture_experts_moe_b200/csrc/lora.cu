@@ -16,6 +16,7 @@
 // tensor cores' balance point, so they are bound by memory and run on
 // mma.sync from shared memory filled by cp.async.
 #include "gemm.cuh"
+#include "tma.cuh"
 
 namespace moe {
 namespace lora {
@@ -73,36 +74,42 @@ struct ShrinkArgs {
   int32_t *err;
 };
 
-constexpr int SH_ROWS = 64, SH_C = 64, SH_LD = 72, SH_STAGES = 4;
-
-template <int BJ, bool TRANS>
+// RW x KW warps: RW 16-row tiles, and KW warps that split each stage's
+// reduction (64 wide each).
+template <int BJ, bool TRANS, int RW, int KW>
 struct ShrinkCfg {
-  static constexpr int Z = SH_ROWS * SH_LD;                        // elements per stage
-  static constexpr int PLD = TRANS ? BJ + 8 : SH_LD;               // 8 elements of padding: no bank conflicts
-  static constexpr int P = TRANS ? SH_C * PLD : BJ * PLD;
-  static constexpr int SMEM = SH_STAGES * (Z + P) * 2;
+  static constexpr int ROWS = 16 * RW, C = 64 * KW, THREADS = 32 * RW * KW;
+  static constexpr int STAGES = 4;
+  static constexpr int ZLD = C + 8;                      // 8 elements of padding: no bank conflicts
+  static constexpr int Z = ROWS * ZLD;                   // elements per stage
+  static constexpr int PLD = TRANS ? BJ + 8 : C + 8;
+  static constexpr int P = TRANS ? C * PLD : BJ * PLD;
+  static constexpr int SMEM = STAGES * (Z + P) * 2;
+  static_assert(KW * ROWS * (BJ + 1) * 4 <= SMEM, "the partial sums reuse the stages");
+  static_assert(SMEM <= 200 * 1024, "shared memory budget");
 };
 
-// out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]) for a tile of 64 rows (16
-// per warp) and BJ ranks. A tile may hold several segments: each CTA of the
-// tile (blockIdx.y of `split`) takes every split-th of them, reads that
-// segment's rows only (the others enter as zeros) and stores them.
-template <int BJ, bool TRANS>
-__global__ void __launch_bounds__(128) shrink_kernel(const ShrinkArgs a) {
-  using Cfg = ShrinkCfg<BJ, TRANS>;
+// out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]) for a tile of 16 RW rows and
+// BJ ranks. A tile may hold several segments: each CTA of the tile (blockIdx.y
+// of `split`) takes every split-th of them, reads that segment's rows only
+// (the others enter as zeros) and stores them.
+template <int BJ, bool TRANS, int RW, int KW>
+__global__ void __launch_bounds__(32 * RW * KW) shrink_kernel(const ShrinkArgs a) {
+  using Cfg = ShrinkCfg<BJ, TRANS, RW, KW>;
   extern __shared__ __align__(16) uint16_t sm[];
   pdl_wait();     // in this order: the projection may start before u is there (gemm_gemv.cu), but
   pdl_trigger();  // not before what this launch itself waits for
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int rw = warp % RW, kw = warp / RW;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-    for (int s = tid; s < a.segs; s += 128) {
+    for (int s = tid; s < a.segs; s += Cfg::THREADS) {
       const int o0 = a.seg_offsets[s], o1 = a.seg_offsets[s + 1], ad = a.seg_adapter[s];
       if (o0 < 0 || o1 < o0 || o1 > a.T || (s == 0 && o0 != 0)) flag_error(a.err, MOE_DEVERR_OFFSETS);
       if (ad < -1 || ad >= a.n_adapters) flag_error(a.err, MOE_DEVERR_EXPERT_ID);
     }
   }
-  const int row0 = blockIdx.x * SH_ROWS, row1 = min(row0 + SH_ROWS, a.T), j0 = blockIdx.z * BJ;
-  const int nc = (a.C + SH_C - 1) / SH_C;
+  const int row0 = blockIdx.x * Cfg::ROWS, row1 = min(row0 + Cfg::ROWS, a.T), j0 = blockIdx.z * BJ;
+  const int nc = (a.C + Cfg::C - 1) / Cfg::C;
   int turn = 0;
   for (int sg = first_segment(a.seg_offsets, a.segs, row0); sg < a.segs; ++sg) {
     const int o0 = a.seg_offsets[sg];
@@ -110,28 +117,32 @@ __global__ void __launch_bounds__(128) shrink_kernel(const ShrinkArgs a) {
     const int lo = max(o0, row0), hi = min(a.seg_offsets[sg + 1], row1), ad = a.seg_adapter[sg];
     if (hi <= lo || turn++ % a.split != int(blockIdx.y)) continue;
     if (ad < 0 || ad >= a.n_adapters) {  // no adapter: nothing is added to these rows
-      for (int p = tid; p < (hi - lo) * BJ; p += 128)
+      for (int p = tid; p < (hi - lo) * BJ; p += Cfg::THREADS)
         if (j0 + p % BJ < a.rank) a.out[int64_t(lo + p / BJ) * a.rank + j0 + p % BJ] = 0;
       continue;
     }
     const uint16_t *pa = a.p + int64_t(ad) * a.rank * a.C;
     auto load = [&](int c) {
-      uint16_t *zs = sm + (c % SH_STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
-      const int c0 = c * SH_C;
-      for (int i = tid; i < SH_ROWS * 8; i += 128) {
-        const int r = i >> 3, cc = (i & 7) * 8;
+      uint16_t *zs = sm + (c % Cfg::STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
+      const int c0 = c * Cfg::C;
+      constexpr int CP = Cfg::C / 8;  // 16-byte pieces of a row
+#pragma unroll
+      for (int i = tid; i < Cfg::ROWS * CP; i += Cfg::THREADS) {
+        const int r = i / CP, cc = i % CP * 8;
         const bool ok = row0 + r >= lo && row0 + r < hi && c0 + cc < a.C;
-        cp16(zs + r * SH_LD + cc, a.z + (ok ? int64_t(row0 + r) * a.ldz + c0 + cc : 0), ok);
+        cp16(zs + r * Cfg::ZLD + cc, a.z + (ok ? int64_t(row0 + r) * a.ldz + c0 + cc : 0), ok);
       }
       if (TRANS) {
-        for (int i = tid; i < SH_C * (BJ / 8); i += 128) {
+#pragma unroll
+        for (int i = tid; i < Cfg::C * (BJ / 8); i += Cfg::THREADS) {
           const int r = i / (BJ / 8), jj = i % (BJ / 8) * 8;
           const bool ok = c0 + r < a.C && j0 + jj < a.rank;
           cp16(ps + r * Cfg::PLD + jj, pa + (ok ? int64_t(c0 + r) * a.rank + j0 + jj : 0), ok);
         }
       } else {
-        for (int i = tid; i < BJ * 8; i += 128) {
-          const int r = i >> 3, cc = (i & 7) * 8;
+#pragma unroll
+        for (int i = tid; i < BJ * CP; i += Cfg::THREADS) {
+          const int r = i / CP, cc = i % CP * 8;
           const bool ok = j0 + r < a.rank && c0 + cc < a.C;
           cp16(ps + r * Cfg::PLD + cc, pa + (ok ? int64_t(j0 + r) * a.C + c0 + cc : 0), ok);
         }
@@ -142,47 +153,57 @@ __global__ void __launch_bounds__(128) shrink_kernel(const ShrinkArgs a) {
     for (int j = 0; j < BJ / 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-    const bool mine = row0 + warp * 16 < hi && row0 + warp * 16 + 16 > lo;  // rows of the segment in this warp
-    __syncthreads();  // the previous segment's stages are read
+    const bool mine = row0 + rw * 16 < hi && row0 + rw * 16 + 16 > lo;  // rows of the segment in this warp
+    __syncthreads();  // the previous segment's sums are read
 #pragma unroll
-    for (int c = 0; c < SH_STAGES - 1; ++c) {
+    for (int c = 0; c < Cfg::STAGES - 1; ++c) {
       if (c < nc) load(c);
       cp_commit();
     }
     for (int c = 0; c < nc; ++c) {
-      cp_wait<SH_STAGES - 2>();
+      cp_wait<Cfg::STAGES - 2>();
       __syncthreads();
-      if (c + SH_STAGES - 1 < nc) load(c + SH_STAGES - 1);
+      if (c + Cfg::STAGES - 1 < nc) load(c + Cfg::STAGES - 1);
       cp_commit();
-      const uint16_t *zs = sm + (c % SH_STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
+      const uint16_t *zs = sm + (c % Cfg::STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
       if (!mine) continue;
 #pragma unroll
-      for (int kk = 0; kk < SH_C / 16; ++kk) {
+      for (int kk = kw * 64; kk < kw * 64 + 64; kk += 16) {
         uint32_t af[4];
-        ldsm4<false>(af, zs + (warp * 16 + (lane & 15)) * SH_LD + kk * 16 + (lane >> 4) * 8);
+        ldsm4<false>(af, zs + (rw * 16 + (lane & 15)) * Cfg::ZLD + kk + (lane >> 4) * 8);
 #pragma unroll
         for (int jp = 0; jp < BJ / 16; ++jp) {
           uint32_t bf[4];
           if (TRANS)  // stored [c][j]
-            ldsm4<true>(bf, ps + (kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
+            ldsm4<true>(bf, ps + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
           else        // stored [j][c]
-            ldsm4<false>(bf, ps + (jp * 16 + (lane & 7) + (lane >> 4) * 8) * Cfg::PLD + kk * 16 + ((lane >> 3) & 1) * 8);
+            ldsm4<false>(bf, ps + (jp * 16 + (lane & 7) + (lane >> 4) * 8) * Cfg::PLD + kk + ((lane >> 3) & 1) * 8);
           mma_16816(acc[2 * jp], af, bf[0], bf[1]);
           mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
         }
       }
     }
     cp_wait<0>();
-    const float sc = a.scale ? a.scale[ad] : 1.f;
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(sm);  // [KW][ROWS][BJ + 1]
 #pragma unroll
     for (int j = 0; j < BJ / 8; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = row0 + warp * 16 + g + h * 8, jj = j0 + j * 8 + 2 * t4;
-        if (row >= lo && row < hi && jj < a.rank)
-          *reinterpret_cast<uint32_t *>(a.out + int64_t(row) * a.rank + jj) =
-              pack_bf16x2(acc[j][2 * h] * sc, acc[j][2 * h + 1] * sc);
+      for (int q = 0; q < 4; ++q)
+        red[(kw * Cfg::ROWS + rw * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
+    __syncthreads();
+    const float sc = a.scale ? a.scale[ad] : 1.f;
+    for (int p = tid; p < (hi - lo) * (BJ / 2); p += Cfg::THREADS) {
+      const int r = lo - row0 + p / (BJ / 2), jj = p % (BJ / 2) * 2;
+      if (j0 + jj >= a.rank) continue;
+      float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        v0 += red[(k * Cfg::ROWS + r) * (BJ + 1) + jj];
+        v1 += red[(k * Cfg::ROWS + r) * (BJ + 1) + jj + 1];
       }
+      *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = pack_bf16x2(v0 * sc, v1 * sc);
+    }
   }
 }
 
@@ -195,7 +216,7 @@ struct AdapterGradArgs {
   uint16_t *da, *db;  // [n][rank][K], [n][N][rank]
 };
 
-constexpr int AG_COLS = 64, AG_ROWS = 64, AG_LD = 72, AG_STAGES = 3;
+constexpr int AG_COLS = 64, AG_ROWS = 64, AG_LD = 72, AG_STAGES = 4;
 
 template <int RJ>
 struct AdapterGradCfg {
@@ -214,7 +235,7 @@ template <int RJ>
 __global__ void __launch_bounds__(128) adapter_grad_kernel(const AdapterGradArgs a) {
   using Cfg = AdapterGradCfg<RJ>;
   extern __shared__ __align__(16) uint16_t sm[];
-  __shared__ int hits[128], nhits[4];
+  __shared__ int seg_lo[128], seg_hi[128], first[128], wsum[4];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -229,63 +250,77 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const AdapterGradArgs
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
 
+  // A window of the segment list at a time: this adapter's segments in order,
+  // as one sequence of 64-row chunks, so the loads run on across segments.
   for (int s0 = 0; s0 < a.segs; s0 += 128) {
-    // this adapter's segments among the next 128, in order
     const int s = s0 + tid;
-    const bool hit = s < a.segs && a.seg_adapter[s] == ad && a.seg_offsets[s + 1] > a.seg_offsets[s];
-    const uint32_t m = __ballot_sync(0xffffffffu, hit);
-    __syncthreads();
-    if (lane == 0) nhits[warp] = __popc(m);
-    __syncthreads();
-    int at = __popc(m & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) at += nhits[w];
-    if (hit) hits[at] = s;
-    const int n = nhits[0] + nhits[1] + nhits[2] + nhits[3];
-    __syncthreads();
-    for (int h = 0; h < n; ++h) {
-      const int lo = max(a.seg_offsets[hits[h]], 0), hi = min(a.seg_offsets[hits[h] + 1], a.T);
-      const int nch = (hi - lo + AG_ROWS - 1) / AG_ROWS;
-      auto load = [&](int c) {
-        uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
-        const int r0 = lo + c * AG_ROWS;
-        for (int i = tid; i < AG_ROWS * 8; i += 128) {
-          const int r = i >> 3, cc = (i & 7) * 8;
-          const bool ok = r0 + r < hi && c0 + cc < C;
-          cp16(zs + r * AG_LD + cc, z + (ok ? int64_t(r0 + r) * ldz + c0 + cc : 0), ok);
-        }
-        for (int i = tid; i < AG_ROWS * (RJ / 8); i += 128) {
-          const int r = i / (RJ / 8), jj = i % (RJ / 8) * 8;
-          const bool ok = r0 + r < hi && jj < a.rank;
-          cp16(ps + r * Cfg::PLD + jj, p + (ok ? int64_t(r0 + r) * a.rank + jj : 0), ok);
-        }
-      };
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < AG_STAGES - 1; ++c) {
-        if (c < nch) load(c);
-        cp_commit();
-      }
-      for (int c = 0; c < nch; ++c) {
-        cp_wait<AG_STAGES - 2>();
-        __syncthreads();
-        if (c + AG_STAGES - 1 < nch) load(c + AG_STAGES - 1);
-        cp_commit();
-        const uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
-#pragma unroll
-        for (int kk = 0; kk < AG_ROWS / 16; ++kk) {
-          uint32_t af[4];
-          ldsm4<true>(af, zs + (kk * 16 + (lane & 7) + (lane >> 4) * 8) * AG_LD + warp * 16 + ((lane >> 3) & 1) * 8);
-#pragma unroll
-          for (int jp = 0; jp < RJ / 16; ++jp) {
-            uint32_t bf[4];
-            ldsm4<true>(bf, ps + (kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
-            mma_16816(acc[2 * jp], af, bf[0], bf[1]);
-            mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
-          }
-        }
-      }
-      cp_wait<0>();
+    int lo = 0, nch = 0;
+    if (s < a.segs && a.seg_adapter[s] == ad) {
+      lo = max(a.seg_offsets[s], 0);
+      nch = max(0, min(a.seg_offsets[s + 1], a.T) - lo);
+      seg_hi[tid] = lo + nch;
+      nch = (nch + AG_ROWS - 1) / AG_ROWS;
     }
+    int incl = nch;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += wsum[w];
+    const int total = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    seg_lo[tid] = lo;
+    first[tid] = incl - nch;  // the segment's first chunk
+    __syncthreads();
+    auto load = [&](int c) {
+      int l = 0, h = 128;  // the last segment whose first chunk is at most c (it has chunks: c lies in it)
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (first[mid] <= c) l = mid; else h = mid;
+      }
+      const int r0 = seg_lo[l] + (c - first[l]) * AG_ROWS, hi = seg_hi[l];
+      uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
+#pragma unroll
+      for (int i = tid; i < AG_ROWS * 8; i += 128) {
+        const int r = i >> 3, cc = (i & 7) * 8;
+        const bool ok = r0 + r < hi && c0 + cc < C;
+        cp16(zs + r * AG_LD + cc, z + (ok ? int64_t(r0 + r) * ldz + c0 + cc : 0), ok);
+      }
+#pragma unroll
+      for (int i = tid; i < AG_ROWS * (RJ / 8); i += 128) {
+        const int r = i / (RJ / 8), jj = i % (RJ / 8) * 8;
+        const bool ok = r0 + r < hi && jj < a.rank;
+        cp16(ps + r * Cfg::PLD + jj, p + (ok ? int64_t(r0 + r) * a.rank + jj : 0), ok);
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < AG_STAGES - 1; ++c) {
+      if (c < total) load(c);
+      cp_commit();
+    }
+    for (int c = 0; c < total; ++c) {
+      cp_wait<AG_STAGES - 2>();
+      __syncthreads();
+      if (c + AG_STAGES - 1 < total) load(c + AG_STAGES - 1);
+      cp_commit();
+      const uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
+#pragma unroll
+      for (int kk = 0; kk < AG_ROWS / 16; ++kk) {
+        uint32_t af[4];
+        ldsm4<true>(af, zs + (kk * 16 + (lane & 7) + (lane >> 4) * 8) * AG_LD + warp * 16 + ((lane >> 3) & 1) * 8);
+#pragma unroll
+        for (int jp = 0; jp < RJ / 16; ++jp) {
+          uint32_t bf[4];
+          ldsm4<true>(bf, ps + (kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
+          mma_16816(acc[2 * jp], af, bf[0], bf[1]);
+          mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
+        }
+      }
+    }
+    cp_wait<0>();
+    __syncthreads();
   }
   // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
 #pragma unroll
@@ -305,25 +340,33 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const AdapterGradArgs
     }
 }
 
-template <int BJ, bool TRANS>
-static int launch_shrink_as(const ShrinkArgs &a, cudaStream_t s, const char *what) {
-  const size_t smem = ShrinkCfg<BJ, TRANS>::SMEM;
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS>), smem, what);
+template <int BJ, bool TRANS, int RW, int KW>
+static int launch_shrink_as(ShrinkArgs a, cudaStream_t s, const char *what) {
+  using Cfg = ShrinkCfg<BJ, TRANS, RW, KW>;
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, RW, KW>), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
-  const dim3 grid(unsigned((a.T + SH_ROWS - 1) / SH_ROWS), unsigned(a.split), unsigned((a.rank + BJ - 1) / BJ));
-  const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS>, grid, dim3(128), smem, s, a);
+  // as many CTAs per row tile as it holds segments on average
+  const int64_t per = (int64_t(a.segs) * Cfg::ROWS + a.T - 1) / a.T;
+  a.split = int(per < 1 ? 1 : per > Cfg::ROWS ? Cfg::ROWS : per);
+  const dim3 grid(unsigned((a.T + Cfg::ROWS - 1) / Cfg::ROWS), unsigned(a.split), unsigned((a.rank + BJ - 1) / BJ));
+  const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS, RW, KW>, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
 
+// 16-row tiles until they fill the SMs about twice over; then 64-row tiles,
+// which read each adapter a quarter as often.
+constexpr int SHRINK_WIDE_T = 4096;
+
 template <bool TRANS>
-static int launch_shrink(ShrinkArgs a, cudaStream_t s, const char *what) {
-  // as many CTAs per row tile as it holds segments on average
-  const int64_t per = (int64_t(a.segs) * SH_ROWS + a.T - 1) / a.T;
-  a.split = int(per < 1 ? 1 : per > SH_ROWS ? SH_ROWS : per);
-  return a.rank <= 16 ? launch_shrink_as<16, TRANS>(a, s, what)
-         : a.rank <= 32 ? launch_shrink_as<32, TRANS>(a, s, what)
-                        : launch_shrink_as<64, TRANS>(a, s, what);
+static int launch_shrink(const ShrinkArgs &a, cudaStream_t s, const char *what) {
+  if (a.T < SHRINK_WIDE_T)
+    return a.rank <= 16   ? launch_shrink_as<16, TRANS, 1, 4>(a, s, what)
+           : a.rank <= 32 ? launch_shrink_as<32, TRANS, 1, 4>(a, s, what)
+                          : launch_shrink_as<64, TRANS, 1, 4>(a, s, what);
+  return a.rank <= 16   ? launch_shrink_as<16, TRANS, 4, 2>(a, s, what)
+         : a.rank <= 32 ? launch_shrink_as<32, TRANS, 4, 2>(a, s, what)
+                        : launch_shrink_as<64, TRANS, 4, 2>(a, s, what);
 }
 
 template <int RJ>
@@ -380,9 +423,16 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
   g.R = T;
   g.M = mode == GEMM_FWD ? N : K;
   g.KD = mode == GEMM_FWD ? K : N;
-  // row tiles narrow enough that the tiles fill the SM pairs, at least 64 rows
+  // The row tile width with the least time by the loads that bound a k-step: each
+  // CTA loads 128 rows of W and bn / 2 rows of x in every round of tiles.
+  const int pairs = sm_count() / 2;
   int bn = 256;
-  while (bn > 64 && int64_t((T + bn - 1) / bn) * ((g.M + 255) / 256) < 74) bn /= 2;
+  int64_t best = INT64_MAX;
+  for (int w = 256; w >= 64; w -= 16) {
+    const int64_t tiles = int64_t((T + w - 1) / w) * ((g.M + 255) / 256);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (128 + w / 2);
+    if (cost < best) { best = cost; bn = w; }
+  }
   g.bn = bn;
   g.out = out;
   g.ldo = ldo;
