@@ -33,6 +33,16 @@ struct TcGemmOperands {
   int64_t lda, a_gstride, ldb;
 };
 
+// The first segment that ends behind `row` (segs if none does).
+__device__ __forceinline__ int first_segment(const int32_t *off, int segs, int row) {
+  int lo = 0, hi = segs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid + 1] > row) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
 int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what);
 
 // One product for the weight-streaming kernel (gemm_gemv.cu): out[r] = in[r] W^T

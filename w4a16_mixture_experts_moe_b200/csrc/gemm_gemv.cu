@@ -91,11 +91,7 @@ __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, 
 
 // The dot product of u[row] and row n of the adapter of row's segment.
 __device__ __forceinline__ float adapter_dot(const GemvArgs &a, int row, int n) {
-  int lo = 0, hi = a.segs;  // the first segment that ends behind the row
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.seg_offsets[mid + 1] > row) hi = mid; else lo = mid + 1;
-  }
+  const int lo = first_segment(a.seg_offsets, a.segs, row);
   const int ad = lo < a.segs && a.seg_offsets[lo] <= row ? a.seg_adapter[lo] : -1;
   float d = 0.f;
   if (ad >= 0 && ad < a.n_adapters) {

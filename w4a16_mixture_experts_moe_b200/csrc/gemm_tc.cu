@@ -33,14 +33,15 @@
 // group, whatever they hold, are set to zero in shared memory (both operands).
 //
 // Per CTA: warps 0-7 epilogue (two accumulators of 256 columns, so it overlaps
-// the next tile's MMAs), warp 8 issues TMA loads into a six-deep ring, warp 9
-// zeroes the tail of wgrad's last k-steps, and in the pair's first CTA warp 11
-// waits for each k-step and hands it over a named barrier to warp 10, which
-// issues the MMAs of both CTAs and touches no memory between them (a warp's
-// shared-memory operations behind its MMAs are held until those finish, which
-// would drain the tensor core at every k-step). The loads of both CTAs count their bytes on the
-// first CTA's barrier (a load of a pair may name its peer's), so a k-step
-// costs no message between the CTAs. All waits are bounded (see tma.cuh).
+// the next tile's MMAs), warps 8 and 12 issue the TMA loads of A and B into a
+// six-deep ring, warp 9 zeroes the tail of wgrad's last k-steps, and in the
+// pair's first CTA warp 11 waits for each k-step and hands it over a named
+// barrier to warp 10, which issues the MMAs of both CTAs and touches no memory
+// between them (a warp's shared-memory operations behind its MMAs are held
+// until those finish, which would drain the tensor core at every k-step). The
+// loads of both CTAs count their bytes on the first CTA's barrier (a load of a
+// pair may name its peer's), so a k-step costs no message between the CTAs.
+// All waits are bounded (see tma.cuh).
 #include "gemm.cuh"
 #include "tma.cuh"
 
@@ -57,8 +58,8 @@ constexpr int A_BYTES = BMC * BK * 2;
 constexpr int B_BYTES = BN / 2 * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;
-constexpr int PROD_WARP = 8, FIX_WARP = 9, MMA_WARP = 10, WAIT_WARP = 11;
-constexpr int THREADS = 384;
+constexpr int A_WARP = 8, FIX_WARP = 9, MMA_WARP = 10, WAIT_WARP = 11, B_WARP = 12;
+constexpr int THREADS = 416;
 constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
 constexpr int HAND_STOP = 31;
 constexpr int ROW_BOX = 32;        // rows per TMA box of a K-major B operand
@@ -257,11 +258,7 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
 // product of u (du) of row + j with row f of that row's B_a (column f of A_a).
 template <int MODE>
 __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
-  int lo = 0, hi = a.segs;  // the first segment that ends behind `row`
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid + 1] > row) hi = mid; else lo = mid + 1;
-  }
+  int lo = first_segment(a.offsets, a.segs, row);
   if (lo >= a.segs || a.offsets[lo + 1] >= row + n) return;
   const int fc = min(f, a.M - 1);  // lanes past the last column repeat it (and store nothing)
 #pragma unroll
@@ -310,6 +307,151 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
 __device__ __forceinline__ int sched_pos(int i) {
   const int G = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1;
   return i * G + ((i & 1) ? G - 1 - c : c);
+}
+
+// One producer warp: A_SIDE issues the loads of A, announces each k-step's
+// bytes and describes it to the waiter; the other issues the loads of B. (One
+// warp issuing both took 490 cycles a k-step, as long as its MMAs.) The warp
+// stays converged and elects the issuing lane, which keeps the loads' operands
+// in uniform registers.
+template <int MODE, bool A_SIDE>
+__device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const Maps &m, uint8_t *smem, uint32_t rank,
+                                        int total) {
+  int s = 0, round = 0;  // ring slot and its use
+  bool ok = true;
+  const uint32_t full0 = leader_addr(&sh.full[0]);
+  auto slot = [&]() {  // waits until the ring's next slot is free
+    ok = __all_sync(0xffffffffu, wait(sh, &sh.empty[s], (round & 1) ^ 1, a.err));
+    return ok;
+  };
+  auto next = [&]() {
+    if (++s == STAGES) { s = 0; ++round; }
+  };
+  for (int i = 0; ok; ++i) {
+    const int t = sched_pos(i);
+    if (t >= total) break;
+    const Tile tl = decode_tile<MODE>(sh, a, t);
+    const int n16 = (tl.nvalid + 15) >> 4, half = n16 * 8;  // rows (wgrad: columns of dy) per CTA
+    const int f = tl.f0 + int(rank) * BMC, r0 = tl.row + int(rank) * half;
+    const int red = MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD;
+    const int nsteps = MODE == GEMM_WGRAD && red == 0 ? 1 : (red + BK - 1) / BK;
+    const int nb = MODE == GEMM_WGRAD ? (half + 63) >> 6 : (half + ROW_BOX - 1) / ROW_BOX;  // loads of B
+    const int b_bytes = nb * (MODE == GEMM_WGRAD ? 8192 : ROW_BOX * BK * 2);
+    // adapters: the next segment that has one and covers whole 16-row blocks of the tile
+    int sg = MODE != GEMM_WGRAD && a.adapter ? first_segment(a.offsets, a.segs, tl.row) : 0;
+    int seg_lo = 0, seg_hi = 0, seg_a = -1;
+    auto next_seg = [&]() {
+      if (MODE == GEMM_WGRAD || !a.adapter) return false;
+      while (sg < a.segs) {
+        const int o0 = a.offsets[sg], o1 = a.offsets[sg + 1], ad = a.adapter[sg];
+        if (o0 >= tl.row + tl.nvalid) return false;
+        ++sg;
+        seg_lo = (max(o0 - tl.row, 0) + 15) & ~15;
+        seg_hi = o1 - tl.row >= tl.nvalid ? n16 * 16 : (o1 - tl.row) & ~15;
+        seg_a = ad;
+        if (seg_hi > seg_lo && ad >= 0 && ad < a.n_adapters) return true;
+      }
+      return false;
+    };
+    bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
+    for (int ks = 0; ks < nsteps && slot(); ++ks) {
+      if (ks + 1 == nsteps) { more = next_seg(); known = true; }
+      uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
+      const int left = min(BK, red - ks * BK);
+      const bool fix = MODE == GEMM_WGRAD && (left & 15);
+      // a k-step with a tail to zero: the zeroing warp sees this CTA's loads
+      // through, and the waiter waits for both CTAs' zeroing
+      const uint32_t bar = fix ? smem_u32(&sh.landed[s]) : full0 + s * 8;
+      if (elect_one()) {
+        if (A_SIDE) {
+          sh.step[s] = Step{max(0, (left + 15) >> 4),
+                            (ks == 0 ? STEP_FIRST : 0) | (ks + 1 == nsteps && !more ? STEP_LAST : 0) | (fix ? STEP_FIX_TAIL : 0),
+                            n16, 0};
+          if (fix) mbar_arrive_expect_tx(&sh.landed[s], A_BYTES + b_bytes);
+          if (rank == 0) {
+            if (fix || left <= 0) mbar_arrive(&sh.full[s]);
+            else mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + b_bytes));
+          }
+        }
+        if (MODE == GEMM_WGRAD) {
+          const int row = sh.lo[tl.e] + ks * BK;
+          if (left <= 0) {  // an empty group: no loads
+          } else if (A_SIDE) {
+            if (m.a_wide) {
+              pair_load_3d(sa, &m.a, 0, row, f >> 6, bar);
+            } else {
+              pair_load_2d(sa, &m.a, f, row, bar);
+              pair_load_2d(sa + 8192, &m.a, f + 64, row, bar);
+            }
+          } else if (m.b_wide && half == BN / 2) {
+            pair_load_3d(sb, &m.bw, 0, row, r0 >> 6, bar);
+          } else {
+            for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * 8192, &m.b, r0 + j * 64, row, bar);
+          }
+        } else if (A_SIDE) {
+          if (MODE == GEMM_FWD) {
+            pair_load_3d(sa, &m.a, ks * BK, f, tl.e, bar);
+          } else if (m.a_wide) {
+            pair_load_4d(sa, &m.a, 0, ks * BK, f >> 6, tl.e, bar);
+          } else {
+            pair_load_3d(sa, &m.a, f, ks * BK, tl.e, bar);
+            pair_load_3d(sa + 8192, &m.a, f + 64, ks * BK, tl.e, bar);
+          }
+        } else if (nb * ROW_BOX == BN / 2) {
+          pair_load_2d(sb, &m.bw, ks * BK, r0, bar);
+        } else {
+          for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.b, ks * BK, r0 + j * ROW_BOX, bar);
+        }
+      }
+      __syncwarp();
+      next();
+    }
+    if constexpr (MODE != GEMM_WGRAD) {
+      while (known && more && ok) {
+        const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
+        const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
+        const int enb = (whalf + ROW_BOX - 1) / ROW_BOX;
+        more = next_seg();
+        for (int j0 = 0; j0 < a.rank && slot(); j0 += BK) {
+          uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
+          const uint32_t bar = full0 + s * 8;
+          if (elect_one()) {
+            if (A_SIDE) {
+              sh.step[s] = Step{(min(BK, a.rank - j0) + 15) >> 4, STEP_EXT | (j0 + BK >= a.rank && !more ? STEP_LAST : 0),
+                                w16, col};
+              if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + enb * ROW_BOX * BK * 2));
+              if (MODE == GEMM_FWD) {
+                pair_load_3d(sa, &m.ea, j0, f, ad, bar);
+              } else {
+                pair_load_3d(sa, &m.ea, f, j0, ad, bar);
+                pair_load_3d(sa + 8192, &m.ea, f + 64, j0, ad, bar);
+              }
+            } else {
+              for (int j = 0; j < enb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.eb, j0, er0 + j * ROW_BOX, bar);
+            }
+          }
+          __syncwarp();
+          next();
+        }
+      }
+    }
+  }
+  if (A_SIDE && ok && slot()) {
+    if (elect_one()) {
+      sh.step[s] = Step{0, STEP_STOP, 0, 0};
+      if (rank == 0) mbar_arrive(&sh.full[s]);
+    }
+    __syncwarp();
+  }
+  // Every MMA that reads shared memory (in either CTA) is done, so every load
+  // has landed, before shared memory is given up: the last use of each slot.
+  // (The stop's own slot is not released; slot() saw its use before through.)
+  for (int j = 1; j < STAGES; ++j) {
+    const int q = (s + j) % STAGES, uses = round + (q < s ? 1 : 0);
+    if (uses > 0) wait(sh, &sh.empty[q], (uses - 1) & 1, a.err, true);
+  }
+  if (!A_SIDE && round > 0) wait(sh, &sh.empty[s], (round - 1) & 1, a.err, true);
+  __syncwarp();
 }
 
 template <int MODE>
@@ -449,145 +591,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
     }
-  } else if (warp == PROD_WARP) {
-    // ================================================================ producer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      auto slot = [&]() {  // waits until the ring's next slot is free
-        ok = ok && wait(sh, &sh.empty[it % STAGES], ((it / STAGES) & 1) ^ 1, a.err);
-        return ok;
-      };
-      for (int i = 0; ok; ++i) {
-        const int t = sched_pos(i);
-        if (t >= total) break;
-        const Tile tl = decode_tile<MODE>(sh, a, t);
-        const int n16 = (tl.nvalid + 15) >> 4, half = n16 * 8;  // rows (wgrad: columns of dy) per CTA
-        const int f = tl.f0 + int(rank) * BMC, r0 = tl.row + int(rank) * half;
-        const int red = MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD;
-        const int KS = (red + BK - 1) / BK;
-        // adapters: the first segment that ends behind the tile's first row
-        int sg = 0;
-        int nsteps = MODE == GEMM_WGRAD && KS == 0 ? 1 : KS;
-        if (MODE != GEMM_WGRAD && a.adapter) {
-          int lo_s = 0, hi_s = a.segs;
-          while (lo_s < hi_s) {
-            const int mid = (lo_s + hi_s) >> 1;
-            if (a.offsets[mid + 1] > tl.row) hi_s = mid; else lo_s = mid + 1;
-          }
-          sg = lo_s;
-        }
-        // finds the next segment with an adapter that has whole 16-row blocks of the tile
-        int seg_lo = 0, seg_hi = 0, seg_a = -1;
-        auto next_seg = [&]() {
-          if (MODE == GEMM_WGRAD || !a.adapter) return false;
-          for (; sg < a.segs; ++sg) {
-            const int o0 = a.offsets[sg];
-            if (o0 >= tl.row + tl.nvalid) return false;
-            const int o1 = a.offsets[sg + 1], ad = a.adapter[sg];
-            seg_lo = (max(o0 - tl.row, 0) + 15) & ~15;
-            seg_hi = o1 - tl.row >= tl.nvalid ? n16 * 16 : (o1 - tl.row) & ~15;
-            seg_a = ad;
-            if (seg_hi > seg_lo && ad >= 0 && ad < a.n_adapters) { ++sg; return true; }
-          }
-          return false;
-        };
-        bool more = next_seg();
-        for (int ks = 0; ks < nsteps && slot(); ++ks) {
-          const int s = it % STAGES;
-          uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
-          Step st;
-          const int left = min(BK, red - ks * BK);
-          st.kk = max(0, (left + 15) >> 4);
-          st.flags = (ks == 0 ? STEP_FIRST : 0) | (ks + 1 == nsteps && !more ? STEP_LAST : 0);
-          st.n16 = n16;
-          st.col = 0;
-          if (MODE == GEMM_WGRAD && (left & 15)) st.flags |= STEP_FIX_TAIL;
-          sh.step[s] = st;
-          const uint32_t bar = leader_addr(&sh.full[s]);
-          if (MODE == GEMM_WGRAD) {
-            const int row = sh.lo[tl.e] + ks * BK, nb = (half + 63) >> 6, bytes = A_BYTES + nb * 8192;
-            const bool fix = st.flags & STEP_FIX_TAIL;
-            uint32_t on = bar;
-            if (st.kk == 0) {
-              if (rank == 0) mbar_arrive(&sh.full[s]);
-            } else if (fix) {  // the zeroing warp sees this CTA's loads through, the MMA warp waits for both CTAs' zeroing
-              mbar_arrive_expect_tx(&sh.landed[s], bytes);
-              if (rank == 0) mbar_arrive(&sh.full[s]);
-              on = smem_u32(&sh.landed[s]);
-            } else if (rank == 0) {
-              mbar_arrive_expect_tx(&sh.full[s], 2 * bytes);
-            }
-            if (st.kk > 0) {
-              if (m.a_wide) {
-                pair_load_3d(sa, &m.a, 0, row, f >> 6, on);
-              } else {
-                pair_load_2d(sa, &m.a, f, row, on);
-                pair_load_2d(sa + 8192, &m.a, f + 64, row, on);
-              }
-              if (m.b_wide && half == BN / 2) {
-                pair_load_3d(sb, &m.bw, 0, row, r0 >> 6, on);
-              } else {
-                for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * 8192, &m.b, r0 + j * 64, row, on);
-              }
-            }
-          } else {
-            const int nb = (half + ROW_BOX - 1) / ROW_BOX;
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + nb * ROW_BOX * BK * 2));
-            if (MODE == GEMM_FWD) {
-              pair_load_3d(sa, &m.a, ks * BK, f, tl.e, bar);
-            } else if (m.a_wide) {
-              pair_load_4d(sa, &m.a, 0, ks * BK, f >> 6, tl.e, bar);
-            } else {
-              pair_load_3d(sa, &m.a, f, ks * BK, tl.e, bar);
-              pair_load_3d(sa + 8192, &m.a, f + 64, ks * BK, tl.e, bar);
-            }
-            if (nb * ROW_BOX == BN / 2) {
-              pair_load_2d(sb, &m.bw, ks * BK, r0, bar);
-            } else {
-              for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.b, ks * BK, r0 + j * ROW_BOX, bar);
-            }
-          }
-          ++it;
-        }
-        if constexpr (MODE != GEMM_WGRAD) while (more && ok) {
-          const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
-          const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
-          more = next_seg();
-          for (int j0 = 0; j0 < a.rank && slot(); j0 += BK) {
-            const int s = it % STAGES;
-            uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
-            Step st;
-            st.kk = (min(BK, a.rank - j0) + 15) >> 4;
-            st.flags = STEP_EXT | (j0 + BK >= a.rank && !more ? STEP_LAST : 0);
-            st.n16 = w16;
-            st.col = col;
-            sh.step[s] = st;
-            const int nb = (whalf + ROW_BOX - 1) / ROW_BOX;
-            const uint32_t bar = leader_addr(&sh.full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + nb * ROW_BOX * BK * 2));
-            if (MODE == GEMM_FWD) {
-              pair_load_3d(sa, &m.ea, j0, f, ad, bar);
-            } else {
-              pair_load_3d(sa, &m.ea, f, j0, ad, bar);
-              pair_load_3d(sa + 8192, &m.ea, f + 64, j0, ad, bar);
-            }
-            for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.eb, j0, er0 + j * ROW_BOX, bar);
-            ++it;
-          }
-        }
-      }
-      int first = it > STAGES ? it - STAGES : 0;  // the oldest step whose slot may still be in use
-      if (ok && slot()) {
-        sh.step[it % STAGES] = Step{0, STEP_STOP, 0, 0};
-        if (rank == 0) mbar_arrive(&sh.full[it % STAGES]);
-        first = it >= STAGES ? it - STAGES + 1 : 0;  // slot() saw the one before the stop's slot through
-      }
-      // every MMA that reads shared memory (in either CTA) is done, so every
-      // load has landed, before shared memory is given up
-      for (int j = first; j < it; ++j) wait(sh, &sh.empty[j % STAGES], (j / STAGES) & 1, a.err, true);
-    }
-    __syncwarp();
+  } else if (warp == A_WARP) {
+    produce<MODE, true>(sh, a, m, smem, rank, total);
+  } else if (warp == B_WARP) {
+    produce<MODE, false>(sh, a, m, smem, rank, total);
   } else if (warp == FIX_WARP) {
     // ================================================================ tails
     if (MODE == GEMM_WGRAD) {

@@ -52,16 +52,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The first segment that ends behind `row` (segs if none does).
-__device__ __forceinline__ int first_segment(const int32_t *off, int segs, int row) {
-  int lo = 0, hi = segs;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid + 1] > row) hi = mid; else lo = mid + 1;
-  }
-  return lo;
-}
-
 struct ShrinkArgs {
   const uint16_t *z;  // [T][C] rows of x or dy
   int64_t ldz;
