@@ -103,6 +103,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Arrives on the barrier at `bar`'s offset in the pair's first CTA.
+// `arrive_leader` publishes what the thread wrote to shared memory;
+// `arrive_leader_read` only says that its reads of tensor memory are done (a
+// release at cluster scope would wait for the epilogue's global stores, 1700
+// cycles a tile).
+__device__ __forceinline__ void arrive_leader_read(uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
@@ -300,6 +310,38 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j0 + j] = __float_as_uint(__uint_as_float(v[j0 + j]) + d[j]);
+  }
+}
+
+// Stores n <= 16 output rows of column f (rows a.ldo elements apart from
+// element `at`); `whole`: all of the warp's columns exist. BF16 values go two
+// rows per store: neighbouring lanes swap one value each, so an even lane holds
+// columns f, f + 1 of row j and an odd lane f - 1, f of row j + 1.
+__device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int n, int f, bool whole, const uint32_t (&v)[16]) {
+  if (a.out_f32) {
+    float *o = static_cast<float *>(a.out) + at;
+    if (n == 16 && whole && !a.accumulate) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += a.ldo) *o = __uint_as_float(v[j]);
+    } else if (f < a.M) {
+      float add[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) add[j] = a.accumulate && j < n ? o[j * a.ldo] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < n) o[j * a.ldo] = __uint_as_float(v[j]) + add[j];
+    }
+  } else {
+    const int odd = threadIdx.x & 1;
+    uint16_t *o = static_cast<uint16_t *>(a.out) + at + odd * a.ldo - odd;
+    const int64_t two = 2 * a.ldo;
+    const bool full = n == 16 && whole;
+#pragma unroll
+    for (int j = 0; j < 16; j += 2, o += two) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+      const uint32_t pk = pack_bf16x2(__uint_as_float(odd ? got : v[j]), __uint_as_float(odd ? v[j + 1] : got));
+      if (full || (j + odd < n && f < a.M)) *reinterpret_cast<uint32_t *>(o) = pk;
+    }
   }
 }
 
@@ -539,7 +581,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp < EPI_WARPS) {
     // ================================================================ epilogue
     const int q = warp & 3, part = warp >> 2;
-    const bool odd = lane & 1;
     for (int i = 0;; ++i) {
       const int t = sched_pos(i);
       if (t >= total) break;
@@ -547,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int b = i & 1;
       if (!__all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (i >> 1) & 1, a.err))) break;
       tc_fence_after();
-      const int f = tl.f0 + int(rank) * BMC + q * 32 + lane;
+      const int fw = tl.f0 + int(rank) * BMC + q * 32, f = fw + lane;
       const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
       const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
       const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
@@ -560,36 +601,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const int n = min(16, tl.nvalid - j0);
         if (MODE != GEMM_WGRAD && a.adapter) add_shared_block<MODE>(a, tl.row + j0, n, f, v);
-        if (a.out_f32) {
-          float *o = static_cast<float *>(a.out) + base + int64_t(j0) * a.ldo;
-          if (f < a.M) {
-            if (a.accumulate) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (j < n) v[j] = __float_as_uint(__uint_as_float(v[j]) + o[j * a.ldo]);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j < n) o[j * a.ldo] = __uint_as_float(v[j]);
-          }
-        } else {
-          // two rows per store: neighbouring lanes swap one value each, so an
-          // even lane holds columns f, f+1 of row j and an odd lane f-1, f of row j+1
-          uint16_t *o = static_cast<uint16_t *>(a.out) + base + int64_t(j0) * a.ldo;
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const uint32_t pk = odd ? pack_bf16x2(__uint_as_float(got), __uint_as_float(keep))
-                                    : pack_bf16x2(__uint_as_float(keep), __uint_as_float(got));
-            const int jr = j + (odd ? 1 : 0);
-            if (jr < n && f < a.M) *reinterpret_cast<uint32_t *>(o + jr * a.ldo - (odd ? 1 : 0)) = pk;
-          }
-        }
+        store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, v);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
+      if (lane == 0) arrive_leader_read(&sh.tmem_empty[b]);
     }
   } else if (warp == A_WARP) {
     produce<MODE, true>(sh, a, m, smem, rank, total);
