@@ -268,20 +268,24 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
 // product of u (du) of row + j with row f of that row's B_a (column f of A_a).
 template <int MODE>
 __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
-  int lo = first_segment(a.offsets, a.segs, row);
-  if (lo >= a.segs || a.offsets[lo + 1] >= row + n) return;
+  // lane j (and j + 16) finds the segment of row j
+  const int mine = row + min(int(threadIdx.x & 15), n - 1);
+  const int sg = first_segment(a.offsets, a.segs, mine);
+  if (__all_sync(0xffffffffu, sg == __shfl_sync(0xffffffffu, sg, 0))) return;
+  int my_ad = sg < a.segs && a.offsets[sg] <= mine ? a.adapter[sg] : -1;
+  if (my_ad >= a.n_adapters) my_ad = -1;
   const int fc = min(f, a.M - 1);  // lanes past the last column repeat it (and store nothing)
 #pragma unroll
   for (int j0 = 0; j0 < 16; j0 += 4) {  // four rows at a time, their loads together
-    if (j0 >= n) break;
     int ad[4];
+    bool any = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = row + j0 + j;
-      while (lo < a.segs && a.offsets[lo + 1] <= r) ++lo;
-      ad[j] = j0 + j < n && lo < a.segs && a.offsets[lo] <= r ? a.adapter[lo] : -1;
-      if (ad[j] >= a.n_adapters) ad[j] = -1;
+      ad[j] = __shfl_sync(0xffffffffu, my_ad, j0 + j);
+      if (j0 + j >= n) ad[j] = -1;
+      any |= ad[j] >= 0;
     }
+    if (!any) continue;
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < a.rank; i += 8) {
       uint4 y[4], b[4];
@@ -290,7 +294,9 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
         y[j] = b[j] = make_uint4(0, 0, 0, 0);
         if (ad[j] < 0) continue;
         y[j] = *reinterpret_cast<const uint4 *>(a.ext_b + int64_t(row + j0 + j) * a.rank + i);
-        if (MODE == GEMM_FWD) {
+        if (j > 0 && ad[j] == ad[j - 1]) {  // rows of one adapter share its values
+          b[j] = b[j - 1];
+        } else if (MODE == GEMM_FWD) {
           b[j] = *reinterpret_cast<const uint4 *>(a.ext_a + (int64_t(ad[j]) * a.M + fc) * a.rank + i);
         } else {
           const uint16_t *c = a.ext_a + (int64_t(ad[j]) * a.rank + i) * a.M + fc;
@@ -379,21 +385,31 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
     const int nsteps = MODE == GEMM_WGRAD && red == 0 ? 1 : (red + BK - 1) / BK;
     const int nb = MODE == GEMM_WGRAD ? (half + 63) >> 6 : (half + ROW_BOX - 1) / ROW_BOX;  // loads of B
     const int b_bytes = nb * (MODE == GEMM_WGRAD ? 8192 : ROW_BOX * BK * 2);
-    // adapters: the next segment that has one and covers whole 16-row blocks of the tile
+    // adapters: the next segment that has one and covers whole 16-row blocks of
+    // the tile; the lanes look at 32 segments at a time
+    const int lane = threadIdx.x & 31, tile_end = tl.row + tl.nvalid;
     int sg = MODE != GEMM_WGRAD && a.adapter ? first_segment(a.offsets, a.segs, tl.row) : 0;
-    int seg_lo = 0, seg_hi = 0, seg_a = -1;
+    int my_lo = 0, my_hi = 0, my_a = -1, seg_lo = 0, seg_hi = 0, seg_a = -1;
+    uint32_t found = 0;
+    bool end = MODE == GEMM_WGRAD || !a.adapter;
     auto next_seg = [&]() {
-      if (MODE == GEMM_WGRAD || !a.adapter) return false;
-      while (sg < a.segs) {
-        const int o0 = a.offsets[sg], o1 = a.offsets[sg + 1], ad = a.adapter[sg];
-        if (o0 >= tl.row + tl.nvalid) return false;
-        ++sg;
-        seg_lo = (max(o0 - tl.row, 0) + 15) & ~15;
-        seg_hi = o1 - tl.row >= tl.nvalid ? n16 * 16 : (o1 - tl.row) & ~15;
-        seg_a = ad;
-        if (seg_hi > seg_lo && ad >= 0 && ad < a.n_adapters) return true;
+      while (found == 0) {
+        if (end) return false;
+        const bool in = sg + lane < a.segs;
+        const int o0 = in ? a.offsets[sg + lane] : INT32_MAX, o1 = in ? a.offsets[sg + lane + 1] : 0;
+        my_a = in ? a.adapter[sg + lane] : -1;
+        my_lo = o0 < tile_end ? (max(o0 - tl.row, 0) + 15) & ~15 : 0;
+        my_hi = o1 >= tile_end ? n16 * 16 : (o1 - tl.row) & ~15;
+        found = __ballot_sync(0xffffffffu, o0 < tile_end && my_hi > my_lo && my_a >= 0 && my_a < a.n_adapters);
+        end = __any_sync(0xffffffffu, o0 >= tile_end);
+        sg += 32;
       }
-      return false;
+      const int l = __ffs(found) - 1;
+      found &= found - 1;
+      seg_lo = __shfl_sync(0xffffffffu, my_lo, l);
+      seg_hi = __shfl_sync(0xffffffffu, my_hi, l);
+      seg_a = __shfl_sync(0xffffffffu, my_a, l);
+      return true;
     };
     bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
