@@ -259,19 +259,19 @@ def test_no_rows_and_partial_gradients(M):
     p = Problem([30, 20], [0, 1], 2, 16, 72, 64, seed=6)
     p.strided()
     ws = p.workspace(M)
-    M.moe_lora_linear(None, 64, p.w, p.seg_off, p.seg_ad, p.a, p.b, None, 0, 2, 2, 16, 72, 64, None, None, 72, ws, 256)
+    M.moe_lora_linear(None, 64, p.w, p.seg_off, p.seg_ad, p.a, p.b, None, 0, 2, 2, 16, 72, 64, None, None, 72, ws, ws.numel())
     M.moe_lora_linear_backward(None, 72, None, 64, p.w, None, p.seg_off, p.seg_ad, p.a, p.b, None, 0, 2, 2, 16, 72, 64,
-                               None, None, 64, p.da, p.db, ws, 256)
+                               None, None, 64, p.da, p.db, ws, ws.numel())
     assert (p.da == 0).all() and (p.db == 0).all()
     p.forward(M, ws)
     p.backward(M, ws)
     dx, da, db = p.dx.clone(), p.da.clone(), p.db.clone()
     p.dx.fill_(3), p.da.fill_(3), p.db.fill_(3)
     args = (p.dys, 72, None, 64, p.w, None, p.seg_off, p.seg_ad, p.a, p.b, p.scale, 50, 2, 2, 16, 72, 64, p.du)
-    M.moe_lora_linear_backward(*args, p.dx, 64, None, None, ws, 256)
+    M.moe_lora_linear_backward(*args, p.dx, 64, None, None, ws, ws.numel())
     assert torch.equal(p.dx, dx) and (p.da == 3).all()
     args = (p.dys, 72, p.xs, 64, p.w, p.u, p.seg_off, p.seg_ad, p.a, p.b, p.scale, 50, 2, 2, 16, 72, 64, p.du)
-    M.moe_lora_linear_backward(*args, None, 64, p.da, p.db, ws, 256)
+    M.moe_lora_linear_backward(*args, None, 64, p.da, p.db, ws, ws.numel())
     assert torch.equal(p.da, da) and torch.equal(p.db, db)
 
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "tma.cuh"
 
 namespace moe {
 
@@ -23,6 +24,10 @@ struct TcGemmArgs {
   void *out;
   int64_t ldo, out_gstride;  // elements
   const uint16_t *ext_a, *ext_b;  // with adapters: lora_b [n][N][rank] (fwd) or lora_a [n][rank][K], and u / du [R][rank]
+  // adapters: fp32 sums for the 16-row blocks that several segments share, from
+  // the launch before (lora.cu); row of block b: 16 b, or 16 owner if delta_by_seg
+  const float *delta;
+  int delta_by_seg;
   int32_t *err;
 };
 
@@ -42,6 +47,15 @@ __device__ __forceinline__ int first_segment(const int32_t *off, int segs, int r
   }
   return lo;
 }
+
+// Segments and 16-row blocks: block b holds rows 16 b .. 16 b + 15 (cut at the
+// last segment's end). Several segments share it if one starts strictly inside;
+// the first that does owns the block.
+
+// A BF16 tensor map with the 128-byte swizzle: dimension 0 contiguous, the
+// others with strides in elements; out-of-range elements read as zero.
+bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
+              const int (&box)[4]);
 
 int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what);
 

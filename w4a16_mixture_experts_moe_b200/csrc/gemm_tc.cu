@@ -23,11 +23,11 @@
 // Adapters ride on the reduction: after the k-steps over W, each segment that
 // covers whole 16-row blocks of the tile adds ceil(rank / 64) k-steps over
 // just those accumulator columns, whose A is the adapter's B_a (A_a) and whose
-// B is the segment's rows of u (du): the sums never leave tensor memory. A
-// block that several segments share is finished in the epilogue, row by row
-// (rank multiply-adds per value). No row is ever multiplied by another
-// request's adapter, not even as a zero: an adapter that holds infinities or
-// NaN spoils its own rows only.
+// B is the segment's rows of u (du): the sums never leave tensor memory. The
+// blocks that several segments share get their part in the epilogue, from fp32
+// sums that a small launch before this one has made row by row (lora.cu). No
+// row is ever multiplied by another request's adapter, not even as a zero: an
+// adapter that holds infinities or NaN spoils its own rows only.
 //
 // wgrad's last k-step ends inside a block of 64 rows: the rows of the next
 // group, whatever they hold, are set to zero in shared memory (both operands).
@@ -43,7 +43,6 @@
 // pair may name its peer's), so a k-step costs no message between the CTAs.
 // All waits are bounded (see tma.cuh).
 #include "gemm.cuh"
-#include "tma.cuh"
 
 namespace moe {
 namespace gt {
@@ -263,60 +262,20 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
   return x;
 }
 
-// The adapters' part of a block of n <= 16 rows that several segments share
-// (a block of one segment has it in its sums already): v[j] gets the dot
-// product of u (du) of row + j with row f of that row's B_a (column f of A_a).
-template <int MODE>
+// The adapters' part of a 16-row block that several segments share (a block
+// of one segment has it in its sums already): n <= 16 rows from `row`.
 __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
-  // lane j (and j + 16) finds the segment of row j
-  const int mine = row + min(int(threadIdx.x & 15), n - 1);
-  const int sg = first_segment(a.offsets, a.segs, mine);
-  if (__all_sync(0xffffffffu, sg == __shfl_sync(0xffffffffu, sg, 0))) return;
-  int my_ad = sg < a.segs && a.offsets[sg] <= mine ? a.adapter[sg] : -1;
-  if (my_ad >= a.n_adapters) my_ad = -1;
-  const int fc = min(f, a.M - 1);  // lanes past the last column repeat it (and store nothing)
+  const int last = row + n - 1;
+  const int sg = first_segment(a.offsets, a.segs, (threadIdx.x & 1) ? last : row);
+  const int s0 = __shfl_sync(0xffffffffu, sg, 0);
+  if (s0 == __shfl_sync(0xffffffffu, sg, 1)) return;
+  const int64_t r0 = a.delta_by_seg ? int64_t(min(s0 + 1, a.segs - 1)) * 16 : row;
+  const float *d = a.delta + r0 * a.M + min(f, a.M - 1);
+  float add[16];
 #pragma unroll
-  for (int j0 = 0; j0 < 16; j0 += 4) {  // four rows at a time, their loads together
-    int ad[4];
-    bool any = false;
+  for (int j = 0; j < 16; ++j) add[j] = j < n ? d[int64_t(j) * a.M] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      ad[j] = __shfl_sync(0xffffffffu, my_ad, j0 + j);
-      if (j0 + j >= n) ad[j] = -1;
-      any |= ad[j] >= 0;
-    }
-    if (!any) continue;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < a.rank; i += 8) {
-      uint4 y[4], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = b[j] = make_uint4(0, 0, 0, 0);
-        if (ad[j] < 0) continue;
-        y[j] = *reinterpret_cast<const uint4 *>(a.ext_b + int64_t(row + j0 + j) * a.rank + i);
-        if (j > 0 && ad[j] == ad[j - 1]) {  // rows of one adapter share its values
-          b[j] = b[j - 1];
-        } else if (MODE == GEMM_FWD) {
-          b[j] = *reinterpret_cast<const uint4 *>(a.ext_a + (int64_t(ad[j]) * a.M + fc) * a.rank + i);
-        } else {
-          const uint16_t *c = a.ext_a + (int64_t(ad[j]) * a.rank + i) * a.M + fc;
-          uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = c[int64_t(2 * q) * a.M] | uint32_t(c[int64_t(2 * q + 1) * a.M]) << 16;
-          b[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[j] = fmaf(bf16_lo(b[j].x), bf16_lo(y[j].x), d[j]); d[j] = fmaf(bf16_hi(b[j].x), bf16_hi(y[j].x), d[j]);
-        d[j] = fmaf(bf16_lo(b[j].y), bf16_lo(y[j].y), d[j]); d[j] = fmaf(bf16_hi(b[j].y), bf16_hi(y[j].y), d[j]);
-        d[j] = fmaf(bf16_lo(b[j].z), bf16_lo(y[j].z), d[j]); d[j] = fmaf(bf16_hi(b[j].z), bf16_hi(y[j].z), d[j]);
-        d[j] = fmaf(bf16_lo(b[j].w), bf16_lo(y[j].w), d[j]); d[j] = fmaf(bf16_hi(b[j].w), bf16_hi(y[j].w), d[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j0 + j] = __float_as_uint(__uint_as_float(v[j0 + j]) + d[j]);
-  }
+  for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + add[j]);
 }
 
 // Stores n <= 16 output rows of column f (rows a.ldo elements apart from
@@ -465,6 +424,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       next();
     }
     if constexpr (MODE != GEMM_WGRAD) {
+      if (more && a.delta) pdl_wait();  // returns at once when the launches before are done
       while (known && more && ok) {
         const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
         const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
@@ -522,7 +482,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_rank();
   const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
   pdl_trigger();
-  pdl_wait();
+  // Only the epilogue needs the launch before this one when that launch
+  // computes the shared blocks: it waits for what this kernel otherwise reads
+  // before it lets this kernel start.
+  if (MODE == GEMM_WGRAD || !a.delta) pdl_wait();
 
   // ---- prologue: barriers, tensor memory, tile table
   if (tid == 0) {
@@ -597,6 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp < EPI_WARPS) {
     // ================================================================ epilogue
     const int q = warp & 3, part = warp >> 2;
+    if (MODE != GEMM_WGRAD && a.delta) pdl_wait();
     for (int i = 0;; ++i) {
       const int t = sched_pos(i);
       if (t >= total) break;
@@ -616,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 16; ++j) v[j] = 0;
         }
         const int n = min(16, tl.nvalid - j0);
-        if (MODE != GEMM_WGRAD && a.adapter) add_shared_block<MODE>(a, tl.row + j0, n, f, v);
+        if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
         store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, v);
       }
       tc_fence_before();
@@ -720,9 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 }  // namespace gt
 
-// A BF16 tensor map with the 128-byte swizzle: dimension 0 contiguous, the
-// others with strides in elements; out-of-range elements read as zero.
-static bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
+bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
                      const int (&box)[4]) {
   cuuint64_t d[4], st[3];
   cuuint32_t bx[4], es[4];

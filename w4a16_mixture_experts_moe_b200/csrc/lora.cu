@@ -13,10 +13,10 @@
 //
 // The small-rank products read each row of x (dy) once and do 2 rank
 // operations per value: at rank 64 that is 64 operations a byte, far below the
-// tensor cores' balance point, so they are bound by memory and run on
-// mma.sync from shared memory filled by cp.async.
+// tensor cores' balance point, so they are bound by memory: mma.sync from
+// shared memory that TMA fills, a ring of stages deep enough to keep the loads
+// in flight.
 #include "gemm.cuh"
-#include "tma.cuh"
 
 namespace moe {
 namespace lora {
@@ -24,16 +24,6 @@ namespace lora {
 constexpr int MAX_RANK = 128;
 constexpr int MAX_SEGS = 65535;  // a grid dimension of the decode form
 
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src), "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <bool TRANS>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *p) {
   if (TRANS)
@@ -52,294 +42,427 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 16-byte piece c of row r in a 128-byte-swizzled tile.
+__device__ __forceinline__ const uint8_t *sw128(const uint8_t *tile, int r, int c) {
+  return tile + r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+constexpr int CONSUMERS = 256;  // warps 0-7; warp 8 issues the loads
+constexpr int RING_MAX = 12;
+constexpr int CONSUMER_BAR = 1;
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync %0, %1;" ::"n"(CONSUMER_BAR), "n"(CONSUMERS) : "memory"); }
+
+struct Ring {
+  uint64_t full[RING_MAX], empty[RING_MAX];
+  int rows[RING_MAX];  // valid rows of the stage (adapter gradients; 0: no further stage)
+  int32_t abort;
+};
+
+__device__ __forceinline__ void ring_init(Ring &ring, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      tma::mbar_init(&ring.full[s], 1);
+      tma::mbar_init(&ring.empty[s], CONSUMERS / 32);
+    }
+    ring.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ bool ring_wait(Ring &ring, uint64_t *bar, uint32_t parity, int32_t *err, bool drain = false) {
+  const bool ok = tma::mbar_try(bar, parity) || tma::wait_bounded(&ring.abort, bar, parity, err, drain);
+  return __all_sync(0xffffffffu, ok);
+}
+
 struct ShrinkArgs {
-  const uint16_t *z;  // [T][C] rows of x or dy
-  int64_t ldz;
-  const uint16_t *p;  // [n][rank][C] (lora_a), or [n][C][rank] (lora_b, TRANS)
   const int32_t *seg_offsets, *seg_adapter;
   const float *scale;
   int segs, n_adapters, T, C, rank;
   int split;          // CTAs that share a row tile's segments
+  int stages;
   uint16_t *out;      // [T][rank]
   int32_t *err;
 };
 
-// RW x KW warps: RW 16-row tiles, and KW warps that split each stage's
-// reduction (64 wide each).
-template <int BJ, bool TRANS, int RW, int KW>
+// A tile of ROWS rows and BJ ranks; RW x KW = 8 warps: RW 16-row tiles, KW
+// warps that split each stage's CC reduction columns.
+template <int BJ, bool TRANS, int ROWS>
 struct ShrinkCfg {
-  static constexpr int ROWS = 16 * RW, C = 64 * KW, THREADS = 32 * RW * KW;
-  static constexpr int STAGES = 4;
-  static constexpr int ZLD = C + 8;                      // 8 elements of padding: no bank conflicts
-  static constexpr int Z = ROWS * ZLD;                   // elements per stage
-  static constexpr int PLD = TRANS ? BJ + 8 : C + 8;
-  static constexpr int P = TRANS ? C * PLD : BJ * PLD;
-  static constexpr int SMEM = STAGES * (Z + P) * 2;
-  static_assert(KW * ROWS * (BJ + 1) * 4 <= SMEM, "the partial sums reuse the stages");
-  static_assert(SMEM <= 200 * 1024, "shared memory budget");
+  static constexpr int RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 128 : 64;
+  static constexpr int Z = ROWS * CC * 2;              // bytes: boxes of 64 columns
+  static constexpr int P = TRANS ? CC * 128 : BJ * CC * 2;  // TRANS: CC rows of 64 ranks
+  static constexpr int STAGE = Z + P;
+  static constexpr int RED = KW * ROWS * (BJ + 1) * 4;
+  static constexpr int STAGES = 120 * 1024 / STAGE < RING_MAX ? 120 * 1024 / STAGE : RING_MAX;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + RED + int(sizeof(Ring));
+  static_assert(KW * 16 <= CC && CC % (KW * 16) == 0 && SMEM <= 200 * 1024, "tile shape");
 };
 
-// out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]) for a tile of 16 RW rows and
-// BJ ranks. A tile may hold several segments: each CTA of the tile (blockIdx.y
-// of `split`) takes every split-th of them, reads that segment's rows only
-// (the others enter as zeros) and stores them.
-template <int BJ, bool TRANS, int RW, int KW>
-__global__ void __launch_bounds__(32 * RW * KW) shrink_kernel(const ShrinkArgs a) {
-  using Cfg = ShrinkCfg<BJ, TRANS, RW, KW>;
-  extern __shared__ __align__(16) uint16_t sm[];
-  pdl_wait();     // in this order: the projection may start before u is there (gemm_gemv.cu), but
+// out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]), z = x and P = lora_a, or
+// z = dy and P_a[j][c] = lora_b[a][c][j] (TRANS). A tile may hold several
+// segments: each CTA of the tile (blockIdx.y of `split`) takes every split-th
+// of them, runs the whole tile through that segment's adapter (rows are
+// independent) and stores the segment's rows.
+template <int BJ, bool TRANS, int ROWS>
+__global__ void __launch_bounds__(CONSUMERS + 32)
+    shrink_kernel(const ShrinkArgs a, const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_p) {
+  using Cfg = ShrinkCfg<BJ, TRANS, ROWS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *red = reinterpret_cast<float *>(sm + Cfg::STAGES * Cfg::STAGE);
+  Ring &ring = *reinterpret_cast<Ring *>(sm + Cfg::STAGES * Cfg::STAGE + Cfg::RED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ring_init(ring, Cfg::STAGES);
+  pdl_wait();     // in this order: the launches behind this one may start before u is there, but
   pdl_trigger();  // not before what this launch itself waits for
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int rw = warp % RW, kw = warp / RW;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-    for (int s = tid; s < a.segs; s += Cfg::THREADS) {
+    for (int s = tid; s < a.segs; s += CONSUMERS + 32) {
       const int o0 = a.seg_offsets[s], o1 = a.seg_offsets[s + 1], ad = a.seg_adapter[s];
       if (o0 < 0 || o1 < o0 || o1 > a.T || (s == 0 && o0 != 0)) flag_error(a.err, MOE_DEVERR_OFFSETS);
       if (ad < -1 || ad >= a.n_adapters) flag_error(a.err, MOE_DEVERR_EXPERT_ID);
     }
   }
-  const int row0 = blockIdx.x * Cfg::ROWS, row1 = min(row0 + Cfg::ROWS, a.T), j0 = blockIdx.z * BJ;
-  const int nc = (a.C + Cfg::C - 1) / Cfg::C;
-  int turn = 0;
-  for (int sg = first_segment(a.seg_offsets, a.segs, row0); sg < a.segs; ++sg) {
+  const int row0 = blockIdx.x * ROWS, row1 = min(row0 + ROWS, a.T), j0 = blockIdx.z * BJ;
+  const int nc = (a.C + Cfg::CC - 1) / Cfg::CC;
+  int turn = 0, slot = 0, round = 0;
+  bool ok = true;
+  for (int sg = first_segment(a.seg_offsets, a.segs, row0); sg < a.segs && ok; ++sg) {
     const int o0 = a.seg_offsets[sg];
     if (o0 >= row1) break;
     const int lo = max(o0, row0), hi = min(a.seg_offsets[sg + 1], row1), ad = a.seg_adapter[sg];
     if (hi <= lo || turn++ % a.split != int(blockIdx.y)) continue;
     if (ad < 0 || ad >= a.n_adapters) {  // no adapter: nothing is added to these rows
-      for (int p = tid; p < (hi - lo) * BJ; p += Cfg::THREADS)
-        if (j0 + p % BJ < a.rank) a.out[int64_t(lo + p / BJ) * a.rank + j0 + p % BJ] = 0;
+      if (warp < 8)
+        for (int p = tid; p < (hi - lo) * BJ; p += CONSUMERS)
+          if (j0 + p % BJ < a.rank) a.out[int64_t(lo + p / BJ) * a.rank + j0 + p % BJ] = 0;
       continue;
     }
-    const uint16_t *pa = a.p + int64_t(ad) * a.rank * a.C;
-    auto load = [&](int c) {
-      uint16_t *zs = sm + (c % Cfg::STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
-      const int c0 = c * Cfg::C;
-      constexpr int CP = Cfg::C / 8;  // 16-byte pieces of a row
+    if (warp == 8) {
+      for (int c = 0; c < nc; ++c) {
+        ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
+        if (!ok) break;
+        if (tma::elect_one()) {
+          uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+          tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
 #pragma unroll
-      for (int i = tid; i < Cfg::ROWS * CP; i += Cfg::THREADS) {
-        const int r = i / CP, cc = i % CP * 8;
-        const bool ok = row0 + r >= lo && row0 + r < hi && c0 + cc < a.C;
-        cp16(zs + r * Cfg::ZLD + cc, a.z + (ok ? int64_t(row0 + r) * a.ldz + c0 + cc : 0), ok);
-      }
-      if (TRANS) {
+          for (int b = 0; b < Cfg::CC / 64; ++b)
+            tma::tma_load_2d(z + b * ROWS * 128, &tm_z, c * Cfg::CC + b * 64, row0, &ring.full[slot]);
+          if (TRANS) {
+            tma::tma_load_3d(p, &tm_p, j0, c * Cfg::CC, ad, &ring.full[slot]);
+          } else {
 #pragma unroll
-        for (int i = tid; i < Cfg::C * (BJ / 8); i += Cfg::THREADS) {
-          const int r = i / (BJ / 8), jj = i % (BJ / 8) * 8;
-          const bool ok = c0 + r < a.C && j0 + jj < a.rank;
-          cp16(ps + r * Cfg::PLD + jj, pa + (ok ? int64_t(c0 + r) * a.rank + j0 + jj : 0), ok);
+            for (int b = 0; b < Cfg::CC / 64; ++b)
+              tma::tma_load_3d(p + b * BJ * 128, &tm_p, c * Cfg::CC + b * 64, j0, ad, &ring.full[slot]);
+          }
         }
-      } else {
-#pragma unroll
-        for (int i = tid; i < BJ * CP; i += Cfg::THREADS) {
-          const int r = i / CP, cc = i % CP * 8;
-          const bool ok = j0 + r < a.rank && c0 + cc < a.C;
-          cp16(ps + r * Cfg::PLD + cc, pa + (ok ? int64_t(j0 + r) * a.C + c0 + cc : 0), ok);
-        }
+        __syncwarp();
+        if (++slot == Cfg::STAGES) { slot = 0; ++round; }
       }
-    };
+      continue;
+    }
+    const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
     float acc[BJ / 8][4];
 #pragma unroll
     for (int j = 0; j < BJ / 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-    const bool mine = row0 + rw * 16 < hi && row0 + rw * 16 + 16 > lo;  // rows of the segment in this warp
-    __syncthreads();  // the previous segment's sums are read
-#pragma unroll
-    for (int c = 0; c < Cfg::STAGES - 1; ++c) {
-      if (c < nc) load(c);
-      cp_commit();
-    }
     for (int c = 0; c < nc; ++c) {
-      cp_wait<Cfg::STAGES - 2>();
-      __syncthreads();
-      if (c + Cfg::STAGES - 1 < nc) load(c + Cfg::STAGES - 1);
-      cp_commit();
-      const uint16_t *zs = sm + (c % Cfg::STAGES) * (Cfg::Z + Cfg::P), *ps = zs + Cfg::Z;
-      if (!mine) continue;
+      ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
+      if (!ok) break;
+      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
 #pragma unroll
-      for (int kk = kw * 64; kk < kw * 64 + 64; kk += 16) {
+      for (int i = 0; i < Cfg::CC / (16 * Cfg::KW); ++i) {
+        const int kk = kw * (Cfg::CC / (16 * Cfg::KW)) + i;  // 16 columns of the stage
         uint32_t af[4];
-        ldsm4<false>(af, zs + (rw * 16 + (lane & 15)) * Cfg::ZLD + kk + (lane >> 4) * 8);
+        ldsm4<false>(af, sw128(z + (kk >> 2) * ROWS * 128, rw * 16 + (lane & 15), (kk & 3) * 2 + (lane >> 4)));
 #pragma unroll
         for (int jp = 0; jp < BJ / 16; ++jp) {
           uint32_t bf[4];
           if (TRANS)  // stored [c][j]
-            ldsm4<true>(bf, ps + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
+            ldsm4<true>(bf, sw128(p, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, jp * 2 + (lane >> 4)));
           else        // stored [j][c]
-            ldsm4<false>(bf, ps + (jp * 16 + (lane & 7) + (lane >> 4) * 8) * Cfg::PLD + kk + ((lane >> 3) & 1) * 8);
+            ldsm4<false>(bf, sw128(p + (kk >> 2) * BJ * 128, jp * 16 + (lane & 7) + (lane >> 4) * 8,
+                                   (kk & 3) * 2 + ((lane >> 3) & 1)));
           mma_16816(acc[2 * jp], af, bf[0], bf[1]);
           mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
         }
       }
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+      if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
-    cp_wait<0>();
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(sm);  // [KW][ROWS][BJ + 1]
+    // the KW partial sums, added in a fixed order
 #pragma unroll
     for (int j = 0; j < BJ / 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        red[(kw * Cfg::ROWS + rw * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
-    __syncthreads();
+        red[(kw * ROWS + rw * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
+    consumer_sync();
     const float sc = a.scale ? a.scale[ad] : 1.f;
-    for (int p = tid; p < (hi - lo) * (BJ / 2); p += Cfg::THREADS) {
+    for (int p = tid; p < (hi - lo) * (BJ / 2); p += CONSUMERS) {
       const int r = lo - row0 + p / (BJ / 2), jj = p % (BJ / 2) * 2;
       if (j0 + jj >= a.rank) continue;
       float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        v0 += red[(k * Cfg::ROWS + r) * (BJ + 1) + jj];
-        v1 += red[(k * Cfg::ROWS + r) * (BJ + 1) + jj + 1];
+      for (int k = 0; k < Cfg::KW; ++k) {
+        v0 += red[(k * ROWS + r) * (BJ + 1) + jj];
+        v1 += red[(k * ROWS + r) * (BJ + 1) + jj + 1];
       }
       *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = pack_bf16x2(v0 * sc, v1 * sc);
     }
+    consumer_sync();
+  }
+}
+
+struct DeltaArgs {
+  const int32_t *seg_offsets, *seg_adapter;
+  const uint16_t *u, *w;  // u / du [T][rank]; lora_b [n][M][rank], or lora_a [n][rank][M] (COLS)
+  int segs, n_adapters, T, rank, M, by_seg;
+  float *delta;
+};
+
+// The adapters' part of the 16-row blocks that several segments share, as fp32
+// rows for the projection's epilogue: delta[j][f] = u[row j] . w_a[f], row j's
+// own adapter a. One CTA per 128 columns and segment; the block's owner does
+// the block, the others leave. A thread keeps its column of the adapter in
+// registers while rows share it.
+template <bool COLS>
+__global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
+  __shared__ __align__(16) uint16_t us[16][MAX_RANK];
+  __shared__ int ads[16];
+  pdl_wait();
+  pdl_trigger();  // behind the wait, as in shrink_kernel
+  const int s = blockIdx.y, o = a.seg_offsets[s], end = min(a.seg_offsets[a.segs], a.T);
+  const int row = o & ~15;
+  if (o <= 0 || o == row || o >= end || (s > 0 && a.seg_offsets[s - 1] > row)) return;
+  const int n = min(16, end - row), tid = threadIdx.x;
+  if (tid < 16) {
+    int ad = -1;
+    if (tid < n) {
+      const int sg = first_segment(a.seg_offsets, a.segs, row + tid);
+      if (sg < a.segs && a.seg_offsets[sg] <= row + tid) ad = a.seg_adapter[sg];
+      if (ad >= a.n_adapters) ad = -1;
+    }
+    ads[tid] = ad;
+  }
+  const int pieces = a.rank / 8;
+  for (int p = tid; p < n * pieces; p += 128)
+    *reinterpret_cast<uint4 *>(&us[p / pieces][p % pieces * 8]) =
+        *reinterpret_cast<const uint4 *>(a.u + int64_t(row + p / pieces) * a.rank + p % pieces * 8);
+  __syncthreads();
+  const int f = blockIdx.x * 128 + tid;
+  if (f >= a.M) return;
+  float *out = a.delta + (a.by_seg ? int64_t(s) * 16 : int64_t(row)) * a.M + f;
+  uint4 w[MAX_RANK / 8];
+  int prev = -1;
+  for (int j = 0; j < n; ++j) {
+    const int ad = ads[j];
+    float d = 0.f;
+    if (ad >= 0) {
+      if (ad != prev) {
+        prev = ad;
+#pragma unroll
+        for (int i = 0; i < MAX_RANK / 8; ++i) {
+          if (i * 8 >= a.rank) break;
+          if (COLS) {
+            const uint16_t *c = a.w + (int64_t(ad) * a.rank + i * 8) * a.M + f;
+            uint32_t q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = c[int64_t(2 * k) * a.M] | uint32_t(c[int64_t(2 * k + 1) * a.M]) << 16;
+            w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+          } else {
+            w[i] = *(reinterpret_cast<const uint4 *>(a.w + (int64_t(ad) * a.M + f) * a.rank) + i);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MAX_RANK / 8; ++i) {
+        if (i * 8 >= a.rank) break;
+        const uint4 y = *reinterpret_cast<const uint4 *>(&us[j][i * 8]);
+        d = fmaf(bf16_lo(w[i].x), bf16_lo(y.x), d); d = fmaf(bf16_hi(w[i].x), bf16_hi(y.x), d);
+        d = fmaf(bf16_lo(w[i].y), bf16_lo(y.y), d); d = fmaf(bf16_hi(w[i].y), bf16_hi(y.y), d);
+        d = fmaf(bf16_lo(w[i].z), bf16_lo(y.z), d); d = fmaf(bf16_hi(w[i].z), bf16_hi(y.z), d);
+        d = fmaf(bf16_lo(w[i].w), bf16_lo(y.w), d); d = fmaf(bf16_hi(w[i].w), bf16_hi(y.w), d);
+      }
+    }
+    out[int64_t(j) * a.M] = d;
   }
 }
 
 struct AdapterGradArgs {
-  const uint16_t *x, *dy, *u, *du;
-  int64_t ldx, lddy;
   const int32_t *seg_offsets, *seg_adapter;
-  int segs, n_adapters, T, N, K, rank;
+  int segs, T, N, K, rank;
   int slabs_a;        // 64-column slabs of x; the others are dy's
+  int stages;
   uint16_t *da, *db;  // [n][rank][K], [n][N][rank]
+  int32_t *err;
 };
 
-constexpr int AG_COLS = 64, AG_ROWS = 64, AG_LD = 72, AG_STAGES = 4;
+constexpr int AG_COLS = 64, AG_ROWS = 64;
 
 template <int RJ>
 struct AdapterGradCfg {
-  static constexpr int PLD = RJ + 8;
-  static constexpr int STAGE = AG_ROWS * (AG_LD + PLD);
-  static constexpr int SMEM = AG_STAGES * STAGE * 2;
+  static constexpr int Z = AG_ROWS * 128, P = AG_ROWS * (RJ == 128 ? 256 : 128);
+  static constexpr int STAGE = Z + P;
+  static constexpr int LD = AG_COLS + 2;                 // fp32 partial sums [RJ][LD]
+  static constexpr int RED = RJ * LD * 4;
+  static constexpr int smem(int stages) { return 1024 + stages * STAGE + RED + int(sizeof(Ring)); }
 };
 
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
 // with p = du, z = x or p = u, z = dy. Rows pass 64 at a time through shared
 // memory, read transposed (ldmatrix.trans): M = columns (16 per warp), N =
-// ranks, K = rows. The segments are taken in order by one CTA, so the sum's
-// order is fixed. An adapter without rows gets zeros.
+// ranks, K = rows (two warps share a chunk's rows). The rows behind a
+// segment's end are cleared in the fragments. The segments are taken in order
+// by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
 template <int RJ>
-__global__ void __launch_bounds__(128) adapter_grad_kernel(const AdapterGradArgs a) {
+__global__ void __launch_bounds__(CONSUMERS + 32)
+    adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_u,
+                        const __grid_constant__ CUtensorMap tm_du) {
   using Cfg = AdapterGradCfg<RJ>;
-  extern __shared__ __align__(16) uint16_t sm[];
-  __shared__ int seg_lo[128], seg_hi[128], first[128], wsum[4];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *red = reinterpret_cast<float *>(sm + a.stages * Cfg::STAGE);
+  Ring &ring = *reinterpret_cast<Ring *>(sm + a.stages * Cfg::STAGE + Cfg::RED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ring_init(ring, a.stages);
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int ad = blockIdx.y;
   const bool is_a = int(blockIdx.x) < a.slabs_a;
   const int c0 = (is_a ? blockIdx.x : blockIdx.x - a.slabs_a) * AG_COLS, C = is_a ? a.K : a.N;
-  const uint16_t *z = is_a ? a.x : a.dy, *p = is_a ? a.du : a.u;
-  const int64_t ldz = is_a ? a.ldx : a.lddy;
+  int slot = 0, round = 0;
+  bool ok = true;
+  if (warp == 8) {
+    const CUtensorMap *tz = is_a ? &tm_x : &tm_dy, *tp = is_a ? &tm_du : &tm_u;
+    for (int s0 = 0; s0 < a.segs && ok; s0 += 32) {  // the lanes look at 32 segments
+      const int s = s0 + lane;
+      int lo = 0, hi = 0;
+      if (s < a.segs && a.seg_adapter[s] == ad) {
+        lo = max(a.seg_offsets[s], 0);
+        hi = min(a.seg_offsets[s + 1], a.T);
+      }
+      for (uint32_t m = __ballot_sync(0xffffffffu, hi > lo); m && ok; m &= m - 1) {
+        const int l = __ffs(m) - 1, e = __shfl_sync(0xffffffffu, hi, l);
+        for (int r = __shfl_sync(0xffffffffu, lo, l); r < e && ok; r += AG_ROWS) {
+          ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
+          if (ok && tma::elect_one()) {
+            uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+            ring.rows[slot] = min(AG_ROWS, e - r);
+            tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
+            tma::tma_load_2d(z, tz, c0, r, &ring.full[slot]);
+            tma::tma_load_2d(p, tp, 0, r, &ring.full[slot]);
+            if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp, 64, r, &ring.full[slot]);
+          }
+          __syncwarp();
+          if (++slot == a.stages) { slot = 0; ++round; }
+        }
+      }
+    }
+    if (ok && ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err) && tma::elect_one()) {
+      ring.rows[slot] = 0;
+      tma::mbar_arrive(&ring.full[slot]);
+    }
+    __syncwarp();
+    return;
+  }
+  const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;
   float acc[RJ / 8][4];
 #pragma unroll
   for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-
-  // A window of the segment list at a time: this adapter's segments in order,
-  // as one sequence of 64-row chunks, so the loads run on across segments.
-  for (int s0 = 0; s0 < a.segs; s0 += 128) {
-    const int s = s0 + tid;
-    int lo = 0, nch = 0;
-    if (s < a.segs && a.seg_adapter[s] == ad) {
-      lo = max(a.seg_offsets[s], 0);
-      nch = max(0, min(a.seg_offsets[s + 1], a.T) - lo);
-      seg_hi[tid] = lo + nch;
-      nch = (nch + AG_ROWS - 1) / AG_ROWS;
-    }
-    int incl = nch;
+  for (;;) {
+    if (!ring_wait(ring, &ring.full[slot], round & 1, a.err)) break;
+    const int rows = ring.rows[slot];
+    if (rows == 0) break;
+    const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += wsum[w];
-    const int total = wsum[0] + wsum[1] + wsum[2] + wsum[3];
-    seg_lo[tid] = lo;
-    first[tid] = incl - nch;  // the segment's first chunk
-    __syncthreads();
-    auto load = [&](int c) {
-      int l = 0, h = 128;  // the last segment whose first chunk is at most c (it has chunks: c lies in it)
-      while (h - l > 1) {
-        const int mid = (l + h) >> 1;
-        if (first[mid] <= c) l = mid; else h = mid;
-      }
-      const int r0 = seg_lo[l] + (c - first[l]) * AG_ROWS, hi = seg_hi[l];
-      uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
-#pragma unroll
-      for (int i = tid; i < AG_ROWS * 8; i += 128) {
-        const int r = i >> 3, cc = (i & 7) * 8;
-        const bool ok = r0 + r < hi && c0 + cc < C;
-        cp16(zs + r * AG_LD + cc, z + (ok ? int64_t(r0 + r) * ldz + c0 + cc : 0), ok);
+    for (int i = 0; i < 2; ++i) {
+      const int kk = kg * 2 + i;
+      uint32_t af[4];
+      ldsm4<true>(af, sw128(z, kk * 16 + (lane & 7) + (lane >> 4) * 8, cg * 2 + ((lane >> 3) & 1)));
+      uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
+      if (rows < kk * 16 + 16) {
+        const int left = rows - kk * 16 - 2 * t4;
+        m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+        m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
+        af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1;
       }
 #pragma unroll
-      for (int i = tid; i < AG_ROWS * (RJ / 8); i += 128) {
-        const int r = i / (RJ / 8), jj = i % (RJ / 8) * 8;
-        const bool ok = r0 + r < hi && jj < a.rank;
-        cp16(ps + r * Cfg::PLD + jj, p + (ok ? int64_t(r0 + r) * a.rank + jj : 0), ok);
-      }
-    };
-#pragma unroll
-    for (int c = 0; c < AG_STAGES - 1; ++c) {
-      if (c < total) load(c);
-      cp_commit();
-    }
-    for (int c = 0; c < total; ++c) {
-      cp_wait<AG_STAGES - 2>();
-      __syncthreads();
-      if (c + AG_STAGES - 1 < total) load(c + AG_STAGES - 1);
-      cp_commit();
-      const uint16_t *zs = sm + (c % AG_STAGES) * Cfg::STAGE, *ps = zs + AG_ROWS * AG_LD;
-#pragma unroll
-      for (int kk = 0; kk < AG_ROWS / 16; ++kk) {
-        uint32_t af[4];
-        ldsm4<true>(af, zs + (kk * 16 + (lane & 7) + (lane >> 4) * 8) * AG_LD + warp * 16 + ((lane >> 3) & 1) * 8);
-#pragma unroll
-        for (int jp = 0; jp < RJ / 16; ++jp) {
-          uint32_t bf[4];
-          ldsm4<true>(bf, ps + (kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * Cfg::PLD + jp * 16 + (lane >> 4) * 8);
-          mma_16816(acc[2 * jp], af, bf[0], bf[1]);
-          mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
-        }
+      for (int jp = 0; jp < RJ / 16; ++jp) {
+        uint32_t bf[4];
+        ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8,
+                              (jp & 3) * 2 + (lane >> 4)));
+        mma_16816(acc[2 * jp], af, bf[0] & m0, bf[1] & m1);
+        mma_16816(acc[2 * jp + 1], af, bf[2] & m0, bf[3] & m1);
       }
     }
-    cp_wait<0>();
-    __syncthreads();
+    __syncwarp();
+    if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+    if (++slot == a.stages) { slot = 0; ++round; }
   }
   // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
+  auto at = [&](int j, int q) -> float & { return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8]; };
+  if (kg == 1) {
 #pragma unroll
-  for (int j = 0; j < RJ / 8; ++j)
+    for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + warp * 16 + g + h * 8, jj = j * 8 + 2 * t4;
-      if (c >= C || jj >= a.rank) continue;
-      if (is_a) {
-        uint16_t *o = a.da + (int64_t(ad) * a.rank + jj) * a.K + c;
-        o[0] = f_to_bf16(acc[j][2 * h]);
-        o[a.K] = f_to_bf16(acc[j][2 * h + 1]);
-      } else {
-        *reinterpret_cast<uint32_t *>(a.db + (int64_t(ad) * a.N + c) * a.rank + jj) =
-            pack_bf16x2(acc[j][2 * h], acc[j][2 * h + 1]);
-      }
+      for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
+  }
+  consumer_sync();
+  if (kg == 0) {
+#pragma unroll
+    for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+  }
+  consumer_sync();
+  if (is_a) {  // [rank][K]: 64 columns of each row
+    for (int p = tid; p < a.rank * (AG_COLS / 2); p += CONSUMERS) {
+      const int j = p / (AG_COLS / 2), c = p % (AG_COLS / 2) * 2;
+      if (c0 + c < C)
+        *reinterpret_cast<uint32_t *>(a.da + (int64_t(ad) * a.rank + j) * a.K + c0 + c) =
+            pack_bf16x2(red[j * Cfg::LD + c], red[j * Cfg::LD + c + 1]);
     }
+  } else {     // [N][rank]: 64 whole rows
+    for (int p = tid; p < AG_COLS * (a.rank / 2); p += CONSUMERS) {
+      const int c = p / (a.rank / 2), j = p % (a.rank / 2) * 2;
+      if (c0 + c < C)
+        *reinterpret_cast<uint32_t *>(a.db + (int64_t(ad) * a.N + c0 + c) * a.rank + j) =
+            pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
+    }
+  }
 }
 
-template <int BJ, bool TRANS, int RW, int KW>
-static int launch_shrink_as(ShrinkArgs a, cudaStream_t s, const char *what) {
-  using Cfg = ShrinkCfg<BJ, TRANS, RW, KW>;
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, RW, KW>), Cfg::SMEM, what);
+// Small-rank operands of one call, for the tensor maps.
+struct Rows {
+  const uint16_t *p;
+  int64_t ld;
+  int width;
+};
+
+template <int BJ, bool TRANS, int ROWS>
+static int launch_shrink_as(ShrinkArgs a, const Rows &z, const uint16_t *p, cudaStream_t s, const char *what) {
+  using Cfg = ShrinkCfg<BJ, TRANS, ROWS>;
+  CUtensorMap tz, tp;
+  bool ok = map_bf16(&tz, z.p, 2, {z.width, a.T, 1, 1}, {z.ld, 0, 0}, {64, ROWS, 1, 1});
+  if (TRANS)
+    ok &= map_bf16(&tp, p, 3, {a.rank, a.C, a.n_adapters, 1}, {a.rank, int64_t(a.C) * a.rank, 0}, {64, Cfg::CC, 1, 1});
+  else
+    ok &= map_bf16(&tp, p, 3, {a.C, a.rank, a.n_adapters, 1}, {a.C, int64_t(a.C) * a.rank, 0}, {64, BJ, 1, 1});
+  if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, ROWS>), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
-  // as many CTAs per row tile as it holds segments on average
-  const int64_t per = (int64_t(a.segs) * Cfg::ROWS + a.T - 1) / a.T;
-  a.split = int(per < 1 ? 1 : per > Cfg::ROWS ? Cfg::ROWS : per);
-  const dim3 grid(unsigned((a.T + Cfg::ROWS - 1) / Cfg::ROWS), unsigned(a.split), unsigned((a.rank + BJ - 1) / BJ));
-  const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS, RW, KW>, grid, dim3(Cfg::THREADS), Cfg::SMEM, s, a);
+  // as many CTAs per row tile as it holds segments on average, and one more:
+  // a tile with a boundary inside does not run twice as long (a CTA without a
+  // segment leaves at once)
+  const int64_t per = (int64_t(a.segs) * ROWS + a.T - 1) / a.T + (a.segs > 1 ? 1 : 0);
+  a.split = int(per < 1 ? 1 : per > ROWS ? ROWS : per);
+  const dim3 grid(unsigned((a.T + ROWS - 1) / ROWS), unsigned(a.split), unsigned((a.rank + BJ - 1) / BJ));
+  const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS, ROWS>, grid, dim3(CONSUMERS + 32), Cfg::SMEM, s, a, tz, tp);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -349,25 +472,52 @@ static int launch_shrink_as(ShrinkArgs a, cudaStream_t s, const char *what) {
 constexpr int SHRINK_WIDE_T = 4096;
 
 template <bool TRANS>
-static int launch_shrink(const ShrinkArgs &a, cudaStream_t s, const char *what) {
+static int launch_shrink(const ShrinkArgs &a, const Rows &z, const uint16_t *p, cudaStream_t s, const char *what) {
   if (a.T < SHRINK_WIDE_T)
-    return a.rank <= 16   ? launch_shrink_as<16, TRANS, 1, 4>(a, s, what)
-           : a.rank <= 32 ? launch_shrink_as<32, TRANS, 1, 4>(a, s, what)
-                          : launch_shrink_as<64, TRANS, 1, 4>(a, s, what);
-  return a.rank <= 16   ? launch_shrink_as<16, TRANS, 4, 2>(a, s, what)
-         : a.rank <= 32 ? launch_shrink_as<32, TRANS, 4, 2>(a, s, what)
-                        : launch_shrink_as<64, TRANS, 4, 2>(a, s, what);
+    return a.rank <= 16   ? launch_shrink_as<16, TRANS, 16>(a, z, p, s, what)
+           : a.rank <= 32 ? launch_shrink_as<32, TRANS, 16>(a, z, p, s, what)
+                          : launch_shrink_as<64, TRANS, 16>(a, z, p, s, what);
+  return a.rank <= 16   ? launch_shrink_as<16, TRANS, 64>(a, z, p, s, what)
+         : a.rank <= 32 ? launch_shrink_as<32, TRANS, 64>(a, z, p, s, what)
+                        : launch_shrink_as<64, TRANS, 64>(a, z, p, s, what);
+}
+
+template <bool COLS>
+static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
+  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.segs));
+  const cudaError_t e = launch_pdl(delta_kernel<COLS>, grid, dim3(128), 0, s, a);
+  if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
 }
 
 template <int RJ>
-static int launch_adapter_grad_as(const AdapterGradArgs &a, cudaStream_t s, const char *what) {
-  const size_t smem = AdapterGradCfg<RJ>::SMEM;
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ>), smem, what);
+static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows &x, const Rows &dy, const Rows &u,
+                                  const Rows &du, cudaStream_t s, const char *what) {
+  using Cfg = AdapterGradCfg<RJ>;
+  CUtensorMap tx, tdy, tu, tdu;
+  bool ok = true;
+  const Rows *r[4] = {&x, &dy, &u, &du};
+  CUtensorMap *m[4] = {&tx, &tdy, &tu, &tdu};
+  for (int i = 0; i < 4; ++i)
+    ok &= map_bf16(m[i], r[i]->p, 2, {r[i]->width, a.T, 1, 1}, {r[i]->ld, 0, 0}, {64, AG_ROWS, 1, 1});
+  if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
+  const dim3 grid(unsigned(a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS), unsigned(n_adapters));
+  // one CTA per SM: a deep ring; more: shallow rings, so that several CTAs share an SM
+  a.stages = int64_t(grid.x) * grid.y <= sm_count() ? 7 : 3;
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ>), Cfg::smem(7), what);
   if (st != MOE_OK) return st;
-  const dim3 grid(unsigned(a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS), unsigned(a.n_adapters));
-  const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ>, grid, dim3(128), smem, s, a);
+  const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
+                                   tx, tdy, tu, tdu);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
+}
+
+// Rows of the fp32 sums for shared 16-row blocks: 16 per segment, or one per
+// row if that is less.
+static size_t delta_rows(int T, int S) {
+  if (T < 1 || S < 2) return 0;
+  const size_t by_seg = size_t(S) * 16, by_row = (size_t(T) + 15) / 16 * 16;
+  return by_seg < by_row ? by_seg : by_row;
 }
 
 // The arguments both entry points share.
@@ -430,12 +580,24 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
   return g;
 }
 
+// Launches the sums of the blocks that several segments share and points the
+// projection at them (one segment shares no block).
+template <bool COLS>
+static int shared_blocks(TcGemmArgs &g, int T, int S, void *ws, cudaStream_t s, const char *what) {
+  if (S < 2) return MOE_OK;
+  g.delta = reinterpret_cast<const float *>(static_cast<char *>(ws) + WS_HEADER);
+  g.delta_by_seg = int64_t(S) * 16 < (int64_t(T) + 15) / 16 * 16;
+  const DeltaArgs d = {g.offsets, g.adapter, g.ext_b, g.ext_a, S, g.n_adapters, T, g.rank, g.M, g.delta_by_seg,
+                       const_cast<float *>(g.delta)};
+  return launch_delta<COLS>(d, s, what);
+}
+
 }  // namespace lora
 }  // namespace moe
 
 extern "C" size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K) {
-  (void)T; (void)S; (void)n_adapters; (void)rank; (void)N; (void)K;
-  return moe::WS_HEADER;
+  (void)n_adapters; (void)rank;
+  return moe::WS_HEADER + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4;
 }
 
 extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w, const int32_t *seg_offsets,
@@ -463,8 +625,8 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.scale = scale; v.out = u; v.ldo = rank; v.err = err;
     st = launch_gemm_gemv(v, S, s, "moe_lora_linear (adapters)");
   } else {
-    lora::ShrinkArgs h = {x, ldx, lora_a, seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, u, err};
-    st = lora::launch_shrink<false>(h, s, "moe_lora_linear (adapters)");
+    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, 0, u, err};
+    st = lora::launch_shrink<false>(h, {x, ldx, K}, lora_a, s, "moe_lora_linear (adapters)");
   }
   if (st != MOE_OK) return st;
   if (T <= lora::GEMV_MAX_T) {
@@ -478,6 +640,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
   TcGemmArgs g = lora::projection(GEMM_FWD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, y, ldy, err);
   g.ext_a = lora_b;
   g.ext_b = u;
+  if ((st = lora::shared_blocks<false>(g, T, S, ws, s, "moe_lora_linear (shared blocks)")) != MOE_OK) return st;
   const TcGemmOperands op = {w, x, K, int64_t(N) * K, ldx};
   return launch_gemm_tc(GEMM_FWD, g, op, s, who);
 }
@@ -511,21 +674,23 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
                     (st = lora::check_rows(who, "u", u, rank, rank)) != MOE_OK)))
     return st;
   int32_t *err = static_cast<int32_t *>(ws);
-  lora::ShrinkArgs h = {dy, lddy, lora_b, seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, du, err};
-  if ((st = lora::launch_shrink<true>(h, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
+  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, 0, du, err};
+  if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
   if (dx) {
     TcGemmArgs g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
     g.ext_a = lora_a;
     g.ext_b = du;
+    if ((st = lora::shared_blocks<true>(g, T, S, ws, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
     const TcGemmOperands op = {w, dy, K, int64_t(N) * K, lddy};
     if ((st = launch_gemm_tc(GEMM_DGRAD, g, op, s, who)) != MOE_OK) return st;
   }
   if (!d_lora_a) return MOE_OK;
-  lora::AdapterGradArgs q = {x, dy, u, du, ldx, lddy, seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank,
-                             (K + lora::AG_COLS - 1) / lora::AG_COLS, d_lora_a, d_lora_b};
+  const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, T, N, K, rank, (K + lora::AG_COLS - 1) / lora::AG_COLS,
+                                   0, d_lora_a, d_lora_b, err};
   const char *what = "moe_lora_linear_backward (adapters)";
-  return rank <= 16   ? lora::launch_adapter_grad_as<16>(q, s, what)
-         : rank <= 32 ? lora::launch_adapter_grad_as<32>(q, s, what)
-         : rank <= 64 ? lora::launch_adapter_grad_as<64>(q, s, what)
-                      : lora::launch_adapter_grad_as<128>(q, s, what);
+  const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
+  return rank <= 16   ? lora::launch_adapter_grad_as<16>(q, n_adapters, rx, rdy, ru, rdu, s, what)
+         : rank <= 32 ? lora::launch_adapter_grad_as<32>(q, n_adapters, rx, rdy, ru, rdu, s, what)
+         : rank <= 64 ? lora::launch_adapter_grad_as<64>(q, n_adapters, rx, rdy, ru, rdu, s, what)
+                      : lora::launch_adapter_grad_as<128>(q, n_adapters, rx, rdy, ru, rdu, s, what);
 }
