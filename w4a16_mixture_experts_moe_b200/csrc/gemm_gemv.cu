@@ -2,10 +2,10 @@
 // groups (decode): the weights are the only large operand, each read once, so
 // the kernel is bound by HBM and by how many loads are in flight.
 //
-// A CTA owns MT * 16 output columns (weight rows) of one group; its warps
-// take K in interleaved pieces of 128 / MT. Lane (g, t) = (lane / 4, lane % 4)
-// loads 16 bytes (8 weights) of rows g and g + 8 (of each 16) at each of a
-// piece's 32-wide chunks: eight independent loads, 4 KB per warp, are in
+// A CTA owns 16 output columns (weight rows) of one group; its warps take K in
+// interleaved pieces of 128. Lane (g, t) = (lane / 4, lane % 4) loads 16 bytes
+// (8 weights) of rows g and g + 8 at each of a piece's four 32-wide chunks:
+// eight independent loads, 4 KB per warp, are in
 // flight before the first MMA (mma.sync m16n8k16). A dot product does not depend on the order of its
 // terms, so a lane's fragment slots are bound to its own eight consecutive k,
 // for the rows of `in` (8 per MMA) as well. The warps' partial sums meet in
@@ -19,6 +19,10 @@
 
 namespace moe {
 namespace gv {
+
+constexpr int COLS = 16;     // output columns per CTA
+constexpr int LD = COLS + 1; // row stride of the partial sums
+constexpr int CH = 4;        // 32-wide chunks of a piece
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -38,26 +42,22 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
 }
 
 // This warp's partial sums for NT * 8 rows of `in` from row r0, into red[row][column].
-template <int MT, int NT, int WARPS>
+template <int NT, int WARPS>
 __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, int n0, int64_t r0, int rows, float *red) {
-  constexpr int LD = MT * 16 + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint16_t *wr = w + int64_t(n0 + g) * a.K + 8 * t;
   const uint16_t *xr = a.in + (r0 + g) * a.ldi + 8 * t;
-  constexpr int CH = 4 / MT;  // 32-wide chunks of a piece: eight weight loads in flight per lane
-  float acc[MT][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[j][i][q] = 0.f;
+    for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
 #pragma unroll 1
   for (int k0 = warp * CH * 32; k0 < a.K; k0 += WARPS * CH * 32) {
-    uint4 wv[2 * MT][CH];
+    uint4 wv[2][CH];
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         wv[i][c] = k0 + 32 * c + 8 * t < a.K && n0 + g + 8 * i < a.N ? ld_stream(wr + int64_t(8 * i) * a.K + k0 + 32 * c) : zero;
@@ -70,23 +70,19 @@ __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, 
                     ? __ldg(reinterpret_cast<const uint4 *>(xr + 8 * i * a.ldi + k0 + 32 * c))
                     : zero;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const uint4 &wa = wv[2 * j][c], &wb = wv[2 * j + 1][c];
-          mma_16816(acc[j][i], wa.x, wb.x, wa.y, wb.y, xv[c].x, xv[c].y);
-          mma_16816(acc[j][i], wa.z, wb.z, wa.w, wb.w, xv[c].z, xv[c].w);
-        }
+      for (int c = 0; c < CH; ++c) {
+        const uint4 &wa = wv[0][c], &wb = wv[1][c];
+        mma_16816(acc[i], wa.x, wb.x, wa.y, wb.y, xv[c].x, xv[c].y);
+        mma_16816(acc[i], wa.z, wb.z, wa.w, wb.w, xv[c].z, xv[c].w);
+      }
     }
   }
   // (c0, c1) = weight row g, rows 2t, 2t+1 of the 8-row tile; (c2, c3) = weight row g + 8
   float *o = red + warp * NT * 8 * LD;
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) o[(8 * i + 2 * t + (q & 1)) * LD + 16 * j + g + (q >> 1) * 8] = acc[j][i][q];
+    for (int q = 0; q < 4; ++q) o[(8 * i + 2 * t + (q & 1)) * LD + g + (q >> 1) * 8] = acc[i][q];
 }
 
 // The dot product of u[row] and row n of the adapter of row's segment.
@@ -109,16 +105,15 @@ __device__ __forceinline__ float adapter_dot(const GemvArgs &a, int row, int n) 
   return d;
 }
 
-template <int MT, int MAXNT, int WARPS>
+template <int MAXNT, int WARPS>
 struct Cfg {
-  static constexpr int SMEM = WARPS * MAXNT * 8 * (MT * 16 + 1) * 4;
+  static constexpr int SMEM = WARPS * MAXNT * 8 * LD * 4;
 };
 
-template <int MT, int MAXNT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, MT == 2 ? 1 : MAXNT == 2 ? 24 / WARPS : 16 / WARPS) gemv_kernel(const GemvArgs a) {
+template <int MAXNT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, MAXNT == 2 ? 24 / WARPS : 16 / WARPS) gemv_kernel(const GemvArgs a) {
   extern __shared__ float red[];
   __shared__ int found[32], which;
-  constexpr int COLS = MT * 16, LD = COLS + 1;
   const bool late = a.seg_adapter != nullptr;  // the previous launch only writes u
   if (!late) pdl_wait();
   pdl_trigger();  // behind the wait: a launch that starts early may count on what this one waited for
@@ -163,16 +158,16 @@ __global__ void __launch_bounds__(WARPS * 32, MT == 2 ? 1 : MAXNT == 2 ? 24 / WA
     int nt = 1;  // 8-row tiles of this pass, the stride of the partial sums
     if (!none) {
       if (rows <= 8) {
-        rows_pass<MT, 1, WARPS>(a, w, n0, lo + r0, rows, red);
+        rows_pass<1, WARPS>(a, w, n0, lo + r0, rows, red);
       } else if (MAXNT == 2 || rows <= 16) {
         nt = 2;
-        rows_pass<MT, 2, WARPS>(a, w, n0, lo + r0, rows, red);
+        rows_pass<2, WARPS>(a, w, n0, lo + r0, rows, red);
       } else if (MAXNT >= 4 && (MAXNT == 4 || rows <= 32)) {
         nt = 4;
-        rows_pass<MT, MAXNT >= 4 ? 4 : 1, WARPS>(a, w, n0, lo + r0, rows, red);
+        rows_pass<MAXNT >= 4 ? 4 : 1, WARPS>(a, w, n0, lo + r0, rows, red);
       } else {
         nt = MAXNT;
-        rows_pass<MT, MAXNT, WARPS>(a, w, n0, lo + r0, rows, red);
+        rows_pass<MAXNT, WARPS>(a, w, n0, lo + r0, rows, red);
       }
     }
     if (late && r0 == 0) pdl_wait();
@@ -199,15 +194,15 @@ __global__ void __launch_bounds__(WARPS * 32, MT == 2 ? 1 : MAXNT == 2 ? 24 / WA
   }
 }
 
-template <int MT, int MAXNT, int WARPS>
+template <int MAXNT, int WARPS>
 static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
-  constexpr size_t smem = Cfg<MT, MAXNT, WARPS>::SMEM;
+  constexpr size_t smem = Cfg<MAXNT, WARPS>::SMEM;
   if (smem > 48 * 1024) {
-    const int st = allow_dynamic_smem(reinterpret_cast<const void *>(gemv_kernel<MT, MAXNT, WARPS>), smem, what);
+    const int st = allow_dynamic_smem(reinterpret_cast<const void *>(gemv_kernel<MAXNT, WARPS>), smem, what);
     if (st != MOE_OK) return st;
   }
-  const dim3 grid(unsigned((a.N + MT * 16 - 1) / (MT * 16)), unsigned(grid_groups));
-  const cudaError_t e = launch_pdl(gemv_kernel<MT, MAXNT, WARPS>, grid, dim3(WARPS * 32), smem, s, a);
+  const dim3 grid(unsigned((a.N + COLS - 1) / COLS), unsigned(grid_groups));
+  const cudaError_t e = launch_pdl(gemv_kernel<MAXNT, WARPS>, grid, dim3(WARPS * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -216,14 +211,14 @@ static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const c
 
 int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
   if (a.seg_adapter) {  // one group of up to 64 rows
-    if (a.R <= 16) return gv::launch_as<1, 2, 8>(a, grid_groups, s, what);
-    if (a.R <= 32) return gv::launch_as<1, 4, 8>(a, grid_groups, s, what);
-    return gv::launch_as<2, 8, 8>(a, grid_groups, s, what);
+    if (a.R <= 16) return gv::launch_as<2, 8>(a, grid_groups, s, what);
+    if (a.R <= 32) return gv::launch_as<4, 8>(a, grid_groups, s, what);
+    return gv::launch_as<8, 8>(a, grid_groups, s, what);
   }
   // few CTAs: more warps share a CTA's reduction
   const int64_t ctas = int64_t(grid_groups) * ((a.N + 15) / 16);
-  if (ctas <= 2 * 148) return gv::launch_as<1, 2, 16>(a, grid_groups, s, what);
-  return gv::launch_as<1, 2, 4>(a, grid_groups, s, what);
+  if (ctas <= 2 * 148) return gv::launch_as<2, 16>(a, grid_groups, s, what);
+  return gv::launch_as<2, 4>(a, grid_groups, s, what);
 }
 
 }  // namespace moe

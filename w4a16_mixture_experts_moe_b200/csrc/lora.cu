@@ -88,14 +88,14 @@ struct ShrinkArgs {
 // warps that split each stage's CC reduction columns.
 template <int BJ, bool TRANS, int ROWS>
 struct ShrinkCfg {
-  static constexpr int RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 128 : 64;
+  static constexpr int RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
   static constexpr int Z = ROWS * CC * 2;              // bytes: boxes of 64 columns
   static constexpr int P = TRANS ? CC * 128 : BJ * CC * 2;  // TRANS: CC rows of 64 ranks
   static constexpr int STAGE = Z + P;
   static constexpr int RED = KW * ROWS * (BJ + 1) * 4;
-  static constexpr int STAGES = 120 * 1024 / STAGE < RING_MAX ? 120 * 1024 / STAGE : RING_MAX;
+  static constexpr int STAGES = 160 * 1024 / STAGE < RING_MAX ? 160 * 1024 / STAGE : RING_MAX;
   static constexpr int SMEM = 1024 + STAGES * STAGE + RED + int(sizeof(Ring));
-  static_assert(KW * 16 <= CC && CC % (KW * 16) == 0 && SMEM <= 200 * 1024, "tile shape");
+  static_assert(KW * 16 <= CC && CC % (KW * 16) == 0 && SMEM <= 227 * 1024, "tile shape");
 };
 
 // out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]), z = x and P = lora_a, or
@@ -298,30 +298,31 @@ struct AdapterGradArgs {
   int32_t *err;
 };
 
-constexpr int AG_COLS = 64, AG_ROWS = 64;
+constexpr int AG_COLS = 64;
 
-template <int RJ>
+template <int RJ, int AG_ROWS>
 struct AdapterGradCfg {
   static constexpr int Z = AG_ROWS * 128, P = AG_ROWS * (RJ == 128 ? 256 : 128);
   static constexpr int STAGE = Z + P;
   static constexpr int LD = AG_COLS + 2;                 // fp32 partial sums [RJ][LD]
   static constexpr int RED = RJ * LD * 4;
+  static constexpr int DEEP = 160 * 1024 / STAGE < RING_MAX ? 160 * 1024 / STAGE : RING_MAX, SHALLOW = 80 * 1024 / STAGE < 2 ? 2 : DEEP / 2;
   static constexpr int smem(int stages) { return 1024 + stages * STAGE + RED + int(sizeof(Ring)); }
 };
 
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
-// with p = du, z = x or p = u, z = dy. Rows pass 64 at a time through shared
+// with p = du, z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
 // memory, read transposed (ldmatrix.trans): M = columns (16 per warp), N =
 // ranks, K = rows (two warps share a chunk's rows). The rows behind a
 // segment's end are cleared in the fragments. The segments are taken in order
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
-template <int RJ>
+template <int RJ, int AG_ROWS>
 __global__ void __launch_bounds__(CONSUMERS + 32)
     adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_u,
                         const __grid_constant__ CUtensorMap tm_du) {
-  using Cfg = AdapterGradCfg<RJ>;
+  using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *red = reinterpret_cast<float *>(sm + a.stages * Cfg::STAGE);
@@ -380,8 +381,9 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
     if (rows == 0) break;
     const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int kk = kg * 2 + i;
+    for (int i = 0; i < AG_ROWS / 32; ++i) {
+      const int kk = kg * (AG_ROWS / 32) + i;
+      if (kk * 16 >= rows) break;
       uint32_t af[4];
       ldsm4<true>(af, sw128(z, kk * 16 + (lane & 7) + (lane >> 4) * 8, cg * 2 + ((lane >> 3) & 1)));
       uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
@@ -490,10 +492,10 @@ static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
   return check_launch(what);
 }
 
-template <int RJ>
+template <int RJ, int AG_ROWS>
 static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows &x, const Rows &dy, const Rows &u,
                                   const Rows &du, cudaStream_t s, const char *what) {
-  using Cfg = AdapterGradCfg<RJ>;
+  using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   CUtensorMap tx, tdy, tu, tdu;
   bool ok = true;
   const Rows *r[4] = {&x, &dy, &u, &du};
@@ -503,13 +505,22 @@ static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows 
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   const dim3 grid(unsigned(a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS), unsigned(n_adapters));
   // one CTA per SM: a deep ring; more: shallow rings, so that several CTAs share an SM
-  a.stages = int64_t(grid.x) * grid.y <= sm_count() ? 7 : 3;
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ>), Cfg::smem(7), what);
+  a.stages = int64_t(grid.x) * grid.y <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
   if (st != MOE_OK) return st;
-  const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
+  const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ, AG_ROWS>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
                                    tx, tdy, tu, tdu);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
+}
+
+template <int AG_ROWS>
+static int launch_adapter_grad(const AdapterGradArgs &a, int n_adapters, const Rows &x, const Rows &dy, const Rows &u,
+                               const Rows &du, cudaStream_t s, const char *what) {
+  return a.rank <= 16   ? launch_adapter_grad_as<16, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
+         : a.rank <= 32 ? launch_adapter_grad_as<32, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
+         : a.rank <= 64 ? launch_adapter_grad_as<64, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
+                        : launch_adapter_grad_as<128, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what);
 }
 
 // Rows of the fp32 sums for shared 16-row blocks: 16 per segment, or one per
@@ -689,8 +700,7 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
                                    0, d_lora_a, d_lora_b, err};
   const char *what = "moe_lora_linear_backward (adapters)";
   const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
-  return rank <= 16   ? lora::launch_adapter_grad_as<16>(q, n_adapters, rx, rdy, ru, rdu, s, what)
-         : rank <= 32 ? lora::launch_adapter_grad_as<32>(q, n_adapters, rx, rdy, ru, rdu, s, what)
-         : rank <= 64 ? lora::launch_adapter_grad_as<64>(q, n_adapters, rx, rdy, ru, rdu, s, what)
-                      : lora::launch_adapter_grad_as<128>(q, n_adapters, rx, rdy, ru, rdu, s, what);
+  // loads of 128 rows, or of 32 where segments are short on average
+  return T >= 64 * S ? lora::launch_adapter_grad<128>(q, n_adapters, rx, rdy, ru, rdu, s, what)
+                     : lora::launch_adapter_grad<32>(q, n_adapters, rx, rdy, ru, rdu, s, what);
 }
