@@ -63,7 +63,10 @@ constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
 constexpr int HAND_STOP = 31;
 constexpr int ROW_BOX = 32;        // rows per TMA box of a K-major B operand
 constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the output columns
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
+constexpr int OUT_ROWS = 32;       // output rows per staged store
+constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // one per half of the epilogue warps
+constexpr int SMEM = STAGES * STAGE_BYTES + 2 * OUT_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
+constexpr int OUT_BAR = 2;         // named barriers 2, 3: the four epilogue warps that share a staging buffer
 
 // One k-step, written by the first CTA's producer for its waiter.
 struct Step {
@@ -216,8 +219,43 @@ struct Maps {
   CUtensorMap b;   // fwd, dgrad: 32 rows. wgrad: 64 reduction rows x 64 columns
   CUtensorMap bw;  // the same for a full half tile: 128 rows; wgrad: 2 blocks of 64 columns (if b_wide)
   CUtensorMap ea, eb;  // adapters: like a and b
+  CUtensorMap out;     // BF16 output: 32 rows x 64 columns
   int a_wide, b_wide;
 };
+
+// 32 accumulator columns of lanes ta .. ta + 15, as 8-column fragments: thread
+// t holds, of columns 8 i .. 8 i + 7, a[4 i], a[4 i + 1] = lane t / 4, columns
+// 2 (t % 4) and the next, a[4 i + 2], a[4 i + 3] = the same of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t ta, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
+        "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+        "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+      : "r"(ta), "r"(ta + (16u << 16))
+      : "memory");
+}
+// Four 8 x 8 matrices, stored transposed: lane 8 m + r gives the address of row r of matrix m.
+__device__ __forceinline__ void stmatrix_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void store_2d(const CUtensorMap *tm, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+}
 
 struct Tile {
   int e;       // group
@@ -262,13 +300,20 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
   return x;
 }
 
+// Whether several segments share the n <= 16 rows from `row`; *first: the
+// segment of the first of them.
+__device__ __forceinline__ bool shared_block(const TcGemmArgs &a, int row, int n, int *first = nullptr) {
+  const int sg = first_segment(a.offsets, a.segs, (threadIdx.x & 1) ? row + n - 1 : row);
+  const int s0 = __shfl_sync(0xffffffffu, sg, 0);
+  if (first) *first = s0;
+  return s0 != __shfl_sync(0xffffffffu, sg, 1);
+}
+
 // The adapters' part of a 16-row block that several segments share (a block
 // of one segment has it in its sums already): n <= 16 rows from `row`.
 __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
-  const int last = row + n - 1;
-  const int sg = first_segment(a.offsets, a.segs, (threadIdx.x & 1) ? last : row);
-  const int s0 = __shfl_sync(0xffffffffu, sg, 0);
-  if (s0 == __shfl_sync(0xffffffffu, sg, 1)) return;
+  int s0;
+  if (!shared_block(a, row, n, &s0)) return;
   const int64_t r0 = a.delta_by_seg ? int64_t(min(s0 + 1, a.segs - 1)) * 16 : row;
   const float *d = a.delta + r0 * a.M + min(f, a.M - 1);
   float add[16];
@@ -276,6 +321,13 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
   for (int j = 0; j < 16; ++j) add[j] = j < n ? d[int64_t(j) * a.M] : 0.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + add[j]);
+}
+
+__device__ __forceinline__ void out_sync(int part) {
+  asm volatile("bar.sync %0, 128;" ::"r"(OUT_BAR + part) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_acc(uint32_t lo, uint32_t hi) {
+  return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 // Stores n <= 16 output rows of column f (rows a.ldo elements apart from
@@ -477,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gemm_kernel(const TcGemmArgs a, const __grid_constant__ Maps m) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES);
+  Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES + 2 * OUT_BYTES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
@@ -560,6 +612,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp < EPI_WARPS) {
     // ================================================================ epilogue
     const int q = warp & 3, part = warp >> 2;
+    const bool issuer = q == 0 && lane == 0;
+    const uint32_t out_buf = smem_u32(smem + STAGES * STAGE_BYTES + part * OUT_BYTES);
     if (MODE != GEMM_WGRAD && a.delta) pdl_wait();
     for (int i = 0;; ++i) {
       const int t = sched_pos(i);
@@ -572,7 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
       const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
       const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
-      for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) {
+      // accumulator columns j0 .. j0 + 15, row by row from registers
+      auto direct = [&](int j0) {
         uint32_t v[16];
         tmem_ld16(tb + j0, v);
         if (zero) {
@@ -582,11 +637,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int n = min(16, tl.nvalid - j0);
         if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
         store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, v);
+      };
+      if (a.out_f32)
+        for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
+      else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
+        const int rows = min(OUT_ROWS, tl.nvalid - j0);
+        if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
+            !(MODE != GEMM_WGRAD && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
+          // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
+          // warps write 128 columns of them to shared memory, one thread sends
+          // them off
+          uint32_t x[16], y[16];
+          tmem_ld_frag(tb + j0, x, y);
+          if (zero) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = y[j] = 0;
+          }
+          if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          out_sync(part);
+          const int piece = q * 4 + (lane >> 3);  // 8 columns
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane & 7);
+            stmatrix_trans(out_buf + (piece >> 3) * (OUT_ROWS * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                           pack_acc(x[4 * i], x[4 * i + 1]), pack_acc(x[4 * i + 2], x[4 * i + 3]),
+                           pack_acc(y[4 * i], y[4 * i + 1]), pack_acc(y[4 * i + 2], y[4 * i + 3]));
+          }
+          fence_proxy_async();
+          out_sync(part);
+          if (issuer) {
+            const int fc = tl.f0 + int(rank) * BMC;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (fc + 64 * h >= a.M) break;
+              if (MODE == GEMM_WGRAD) store_3d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0, tl.e);
+              else store_2d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0);
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          continue;
+        }
+        for (int j1 = j0; j1 < j0 + rows; j1 += 16) direct(j1);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader_read(&sh.tmem_empty[b]);
     }
+    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == A_WARP) {
     produce<MODE, true>(sh, a, m, smem, rank, total);
   } else if (warp == B_WARP) {
@@ -725,6 +822,10 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
     ok &= map_bf16(&m.bw, op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, gt::BN / 2, 1, 1});
   else if (m.b_wide)
     ok &= map_bf16(&m.bw, op.b, 3, {64, a.R, N / 64, 1}, {op.ldb, 64, 0}, {64, 64, 2, 1});
+  if (!a.out_f32)
+    ok &= MODE == GEMM_WGRAD
+              ? map_bf16(&m.out, a.out, 3, {K, N, a.groups, 1}, {a.ldo, a.out_gstride, 0}, {64, gt::OUT_ROWS, 1, 1})
+              : map_bf16(&m.out, a.out, 2, {a.M, a.R, 1, 1}, {a.ldo, 0, 0}, {64, gt::OUT_ROWS, 1, 1});
   if (a.adapter) {
     if (MODE == GEMM_FWD)
       ok &= map_bf16(&m.ea, a.ext_a, 3, {a.rank, N, a.n_adapters, 1}, {a.rank, int64_t(N) * a.rank, 0},
