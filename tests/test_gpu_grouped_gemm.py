@@ -115,6 +115,8 @@ SHAPES = [
     ([100] * 9, 128, 1024),
     ([2100, 3, 700], 384, 136),                    # more than one block of row tiles
     ([63, 64, 65, 127, 128, 129], 1000, 1032),
+    ([300, 257, 40, 512, 0, 511, 700, 1030], 1304, 1416),  # tiles of two MMAs beside tiles of one
+    ([513] * 3 + [272] * 40, 1024, 1024),
 ]
 
 

@@ -60,8 +60,10 @@ constexpr int EPI_WARPS = 8;
 constexpr int A_WARP = 8, FIX_WARP = 9, MMA_WARP = 10, WAIT_WARP = 11, B_WARP = 12;
 constexpr int THREADS = 416;
 constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
-constexpr int HAND_STOP = 31;
-constexpr int ROW_BOX = 32;        // rows per TMA box of a K-major B operand
+// A k-step's first handoff: its MMAs (0-4), bits below, or HAND_STOP. With
+// HAND_SET two more follow: the width / 16, then the first column / 16 or
+// HAND_FIRST (a tile's first k-step, which overwrites the accumulator).
+constexpr int HAND_KK = 7, HAND_LAST = 8, HAND_SET = 16, HAND_STOP = 31, HAND_FIRST = 31;
 constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the output columns
 constexpr int OUT_ROWS = 32;       // output rows per staged store
 constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // one per half of the epilogue warps
@@ -216,9 +218,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&a)[16]) {
 // loads a k-step instead of two took the wide product from 1.54 to 1.77 ms).
 struct Maps {
   CUtensorMap a;   // fwd: 128 rows of W. dgrad, wgrad: 64 reduction rows x 64 columns (x 2 blocks if a_wide)
-  CUtensorMap b;   // fwd, dgrad: 32 rows. wgrad: 64 reduction rows x 64 columns
-  CUtensorMap bw;  // the same for a full half tile: 128 rows; wgrad: 2 blocks of 64 columns (if b_wide)
-  CUtensorMap ea, eb;  // adapters: like a and b
+  CUtensorMap b[3];   // fwd, dgrad: 32, 64, 128 rows (the first that holds the tile's half: rows behind it are read
+                      // for nothing, which costs less than a second load). wgrad: 64 reduction rows x 64 columns,
+                      // x 2 blocks (if b_wide)
+  CUtensorMap ea, eb[3];  // adapters: like a and b
   CUtensorMap out;     // BF16 output: 32 rows x 64 columns
   int a_wide, b_wide;
 };
@@ -362,6 +365,9 @@ __device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int
   }
 }
 
+// The map of B for `half` rows per CTA: boxes of 32, 64, 128 rows.
+__device__ __forceinline__ int row_box(int half) { return half <= 32 ? 0 : half <= 64 ? 1 : 2; }
+
 // The pair's i-th tile, in a snake over the pairs.
 __device__ __forceinline__ int sched_pos(int i) {
   const int G = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1;
@@ -394,8 +400,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
     const int f = tl.f0 + int(rank) * BMC, r0 = tl.row + int(rank) * half;
     const int red = MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD;
     const int nsteps = MODE == GEMM_WGRAD && red == 0 ? 1 : (red + BK - 1) / BK;
-    const int nb = MODE == GEMM_WGRAD ? (half + 63) >> 6 : (half + ROW_BOX - 1) / ROW_BOX;  // loads of B
-    const int b_bytes = nb * (MODE == GEMM_WGRAD ? 8192 : ROW_BOX * BK * 2);
+    const int box = row_box(half), nb = (half + 63) >> 6;  // B's map; wgrad: 64-column blocks of B
+    const int b_bytes = MODE == GEMM_WGRAD ? nb * 8192 : (32 << box) * BK * 2;
     // adapters: the next segment that has one and covers whole 16-row blocks of
     // the tile; the lanes look at 32 segments at a time
     const int lane = threadIdx.x & 31, tile_end = tl.row + tl.nvalid;
@@ -453,9 +459,9 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
               pair_load_2d(sa + 8192, &m.a, f + 64, row, bar);
             }
           } else if (m.b_wide && half == BN / 2) {
-            pair_load_3d(sb, &m.bw, 0, row, r0 >> 6, bar);
+            pair_load_3d(sb, &m.b[1], 0, row, r0 >> 6, bar);
           } else {
-            for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * 8192, &m.b, r0 + j * 64, row, bar);
+            for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * 8192, &m.b[0], r0 + j * 64, row, bar);
           }
         } else if (A_SIDE) {
           if (MODE == GEMM_FWD) {
@@ -466,10 +472,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
             pair_load_3d(sa, &m.a, f, ks * BK, tl.e, bar);
             pair_load_3d(sa + 8192, &m.a, f + 64, ks * BK, tl.e, bar);
           }
-        } else if (nb * ROW_BOX == BN / 2) {
-          pair_load_2d(sb, &m.bw, ks * BK, r0, bar);
         } else {
-          for (int j = 0; j < nb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.b, ks * BK, r0 + j * ROW_BOX, bar);
+          pair_load_2d(sb, &m.b[box], ks * BK, r0, bar);
         }
       }
       __syncwarp();
@@ -480,7 +484,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       while (known && more && ok) {
         const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
         const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
-        const int enb = (whalf + ROW_BOX - 1) / ROW_BOX;
+        const int ebox = row_box(whalf);
         more = next_seg();
         for (int j0 = 0; j0 < a.rank && slot(); j0 += BK) {
           uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
@@ -489,7 +493,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
             if (A_SIDE) {
               sh.step[s] = Step{(min(BK, a.rank - j0) + 15) >> 4, STEP_EXT | (j0 + BK >= a.rank && !more ? STEP_LAST : 0),
                                 w16, col};
-              if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + enb * ROW_BOX * BK * 2));
+              if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * (A_BYTES + (32 << ebox) * BK * 2));
               if (MODE == GEMM_FWD) {
                 pair_load_3d(sa, &m.ea, j0, f, ad, bar);
               } else {
@@ -497,7 +501,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
                 pair_load_3d(sa + 8192, &m.ea, f + 64, j0, ad, bar);
               }
             } else {
-              for (int j = 0; j < enb; ++j) pair_load_2d(sb + j * ROW_BOX * BK * 2, &m.eb, j0, er0 + j * ROW_BOX, bar);
+              pair_load_2d(sb, &m.eb[ebox], j0, er0, bar);
             }
           }
           __syncwarp();
@@ -718,11 +722,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == WAIT_WARP && rank == 0) {
     // ================================================================ waiter
-    int tl = 0;
-    uint32_t phase = 0;  // of fixed[], one bit per slot
-    for (int it = 0;; ++it) {
-      const int s = it % STAGES;
-      bool ok = wait(sh, &sh.full[s], (it / STAGES) & 1, a.err);
+    int tl = 0, s = 0;
+    uint32_t round = 0, phase = 0;  // phase: of fixed[], one bit per slot
+    for (;;) {
+      bool ok = wait(sh, &sh.full[s], round, a.err);
       const Step st = sh.step[s];
       if (ok && !(st.flags & STEP_STOP)) {
         if (MODE == GEMM_WGRAD && (st.flags & STEP_FIX_TAIL)) {
@@ -733,39 +736,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       const bool stop = !ok || (st.flags & STEP_STOP);
-      const int kind = (st.flags & STEP_FIRST) ? 1 : (st.flags & STEP_EXT) ? 2 : 0, last = (st.flags & STEP_LAST) ? 1 : 0;
-      handoff(lane < (stop ? HAND_STOP : kind * 10 + last * 5 + st.kk));
+      const bool set = st.flags & (STEP_FIRST | STEP_EXT);
+      handoff(lane < (stop ? HAND_STOP : st.kk | (st.flags & STEP_LAST ? HAND_LAST : 0) | (set ? HAND_SET : 0)));
       if (stop) break;
-      if (kind) handoff(lane < st.n16);
-      if (kind == 2) handoff(lane < st.col >> 4);
-      tl += last;
+      if (set) {
+        handoff(lane < st.n16);
+        handoff(lane < (st.flags & STEP_FIRST ? HAND_FIRST : st.col >> 4));
+      }
+      if (st.flags & STEP_LAST) ++tl;
+      if (++s == STAGES) { s = 0; round ^= 1; }
     }
   } else if (warp == MMA_WARP && rank == 0) {
     // ================================================================ MMA issuer
     constexpr bool A_MN = MODE != GEMM_FWD, B_MN = MODE == GEMM_WGRAD;
     constexpr uint32_t KA = A_MN ? 2048 >> 4 : 32 >> 4, KB = B_MN ? 2048 >> 4 : 32 >> 4;  // 16 reduction indices on
+    constexpr uint32_t idesc = idesc_bf16(A_MN, B_MN);
+    const uint64_t ring = sw128_desc(smem_u32(smem), 8192);  // the start address is the descriptor's low field
     int tl = 0, n16 = 0, s = 0;
     for (;;) {
       const int v = handoff(0);
       if (v >= HAND_STOP) break;
-      const int kind = v / 10, last = v % 10 / 5, kk = v % 5;
       int col = 0;
-      if (kind) n16 = handoff(0);
-      if (kind == 2) col = handoff(0) * 16;
+      bool first = false;
+      if (v & HAND_SET) {
+        n16 = handoff(0);
+        const int aux = handoff(0);
+        first = aux == HAND_FIRST;
+        if (!first) col = aux * 16;
+      }
       tc_fence_after();
-      const uint32_t sa = smem_u32(smem) + s * STAGE_BYTES;
-      const uint64_t da = sw128_desc(sa, 8192), db = sw128_desc(sa + A_BYTES, 8192);
-      const uint32_t idesc = idesc_bf16(A_MN, B_MN) | (uint32_t(n16 * 2) << 17);
-      const uint32_t d = tmem + (tl & 1) * BN + col;
+      const uint64_t da = ring + uint64_t(s) * (STAGE_BYTES >> 4), db = da + (A_BYTES >> 4);
+      const uint32_t id = idesc | uint32_t(n16 * 2) << 17, d = tmem + (tl & 1) * BN + col;
       if (elect_one()) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q < kk) mma_pair(d, da + q * KA, db + q * KB, idesc, kind != 1 || q > 0);
+          if (q < (v & HAND_KK)) mma_pair(d, da + q * KA, db + q * KB, id, !first || q > 0);
         commit_pair(&sh.empty[s]);
-        if (last) commit_pair(&sh.tmem_full[tl & 1]);
+        if (v & HAND_LAST) commit_pair(&sh.tmem_full[tl & 1]);
       }
       __syncwarp();
-      tl += last;
+      if (v & HAND_LAST) ++tl;
       if (++s == STAGES) s = 0;
     }
   }
@@ -816,12 +826,12 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
     ok &= m.a_wide ? map_bf16(&m.a, op.a, 3, {64, a.R, K / 64, 1}, {op.lda, 64, 0}, {64, 64, 2, 1})
                    : map_bf16(&m.a, op.a, 2, {K, a.R, 1, 1}, {op.lda, 0, 0}, {64, 64, 1, 1});
   const int64_t width = MODE == GEMM_FWD ? K : N;
-  const int rows = MODE == GEMM_WGRAD ? 64 : gt::ROW_BOX;
-  ok &= map_bf16(&m.b, op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, rows, 1, 1});
-  if (MODE != GEMM_WGRAD)
-    ok &= map_bf16(&m.bw, op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, gt::BN / 2, 1, 1});
-  else if (m.b_wide)
-    ok &= map_bf16(&m.bw, op.b, 3, {64, a.R, N / 64, 1}, {op.ldb, 64, 0}, {64, 64, 2, 1});
+  if (MODE == GEMM_WGRAD) {
+    ok &= map_bf16(&m.b[0], op.b, 2, {N, a.R, 1, 1}, {op.ldb, 0, 0}, {64, 64, 1, 1});
+    if (m.b_wide) ok &= map_bf16(&m.b[1], op.b, 3, {64, a.R, N / 64, 1}, {op.ldb, 64, 0}, {64, 64, 2, 1});
+  } else {
+    for (int i = 0; i < 3; ++i) ok &= map_bf16(&m.b[i], op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, 32 << i, 1, 1});
+  }
   if (!a.out_f32)
     ok &= MODE == GEMM_WGRAD
               ? map_bf16(&m.out, a.out, 3, {K, N, a.groups, 1}, {a.ldo, a.out_gstride, 0}, {64, gt::OUT_ROWS, 1, 1})
@@ -832,7 +842,8 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
                      {64, gt::BMC, 1, 1});
     else
       ok &= map_bf16(&m.ea, a.ext_a, 3, {K, a.rank, a.n_adapters, 1}, {K, int64_t(K) * a.rank, 0}, {64, 64, 1, 1});
-    ok &= map_bf16(&m.eb, a.ext_b, 2, {a.rank, a.R, 1, 1}, {a.rank, 0, 0}, {64, gt::ROW_BOX, 1, 1});
+    for (int i = 0; i < 3; ++i)
+      ok &= map_bf16(&m.eb[i], a.ext_b, 2, {a.rank, a.R, 1, 1}, {a.rank, 0, 0}, {64, 32 << i, 1, 1});
   }
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE>), gt::SMEM, what);
