@@ -210,11 +210,7 @@ static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const c
 }  // namespace gv
 
 int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
-  if (a.seg_adapter) {  // one group of up to 64 rows
-    if (a.R <= 16) return gv::launch_as<2, 8>(a, grid_groups, s, what);
-    if (a.R <= 32) return gv::launch_as<4, 8>(a, grid_groups, s, what);
-    return gv::launch_as<8, 8>(a, grid_groups, s, what);
-  }
+  if (a.seg_adapter) return gv::launch_as<2, 8>(a, grid_groups, s, what);  // one group of few rows
   // few CTAs: more warps share a CTA's reduction
   const int64_t ctas = int64_t(grid_groups) * ((a.N + 15) / 16);
   if (ctas <= 2 * 148) return gv::launch_as<2, 16>(a, grid_groups, s, what);

@@ -16,7 +16,11 @@
 // tensor cores' balance point, so they are bound by memory: mma.sync from
 // shared memory that TMA fills, a ring of stages deep enough to keep the loads
 // in flight.
+#include <cooperative_groups.h>
+
 #include "gemm.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 namespace lora {
@@ -40,6 +44,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float d) {
+  d = fmaf(bf16_lo(a.x), bf16_lo(b.x), d); d = fmaf(bf16_hi(a.x), bf16_hi(b.x), d);
+  d = fmaf(bf16_lo(a.y), bf16_lo(b.y), d); d = fmaf(bf16_hi(a.y), bf16_hi(b.y), d);
+  d = fmaf(bf16_lo(a.z), bf16_lo(b.z), d); d = fmaf(bf16_hi(a.z), bf16_hi(b.z), d);
+  d = fmaf(bf16_lo(a.w), bf16_lo(b.w), d); d = fmaf(bf16_hi(a.w), bf16_hi(b.w), d);
+  return d;
 }
 
 // 16-byte piece c of row r in a 128-byte-swizzled tile.
@@ -223,26 +235,38 @@ struct DeltaArgs {
 
 // The adapters' part of the 16-row blocks that several segments share, as fp32
 // rows for the projection's epilogue: delta[j][f] = u[row j] . w_a[f], row j's
-// own adapter a. One CTA per 128 columns and segment; the block's owner does
-// the block, the others leave. A thread keeps its column of the adapter in
-// registers while rows share it.
+// own adapter a. A CTA does 128 columns of four rows of a block (a row's loads
+// wait on nothing but its adapter's index, but follow the row before): blocks
+// by their owning segment, or all blocks where segments are many. A thread
+// keeps its column of the adapter in registers while rows share it.
+constexpr int DELTA_ROWS = 4;
+
 template <bool COLS>
 __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
-  __shared__ __align__(16) uint16_t us[16][MAX_RANK];
-  __shared__ int ads[16];
+  __shared__ __align__(16) uint16_t us[DELTA_ROWS][MAX_RANK];
+  __shared__ int ads[DELTA_ROWS];
   pdl_wait();
   pdl_trigger();  // behind the wait, as in shrink_kernel
-  const int s = blockIdx.y, o = a.seg_offsets[s], end = min(a.seg_offsets[a.segs], a.T);
-  const int row = o & ~15;
-  if (o <= 0 || o == row || o >= end || (s > 0 && a.seg_offsets[s - 1] > row)) return;
-  const int n = min(16, end - row), tid = threadIdx.x;
-  if (tid < 16) {
-    int ad = -1;
-    if (tid < n) {
-      const int sg = first_segment(a.seg_offsets, a.segs, row + tid);
-      if (sg < a.segs && a.seg_offsets[sg] <= row + tid) ad = a.seg_adapter[sg];
-      if (ad >= a.n_adapters) ad = -1;
-    }
+  const int end = min(a.seg_offsets[a.segs], a.T), tid = threadIdx.x;
+  int row;  // the block's first row
+  if (a.by_seg) {
+    const int s = blockIdx.y, o = a.seg_offsets[s];
+    row = o & ~15;
+    if (o <= 0 || o == row || o >= end || (s > 0 && a.seg_offsets[s - 1] > row)) return;
+  } else {
+    row = blockIdx.y * 16;
+    if (row >= end || first_segment(a.seg_offsets, a.segs, row) ==
+                          first_segment(a.seg_offsets, a.segs, min(row + 15, end - 1)))
+      return;
+  }
+  const int j0 = blockIdx.z * DELTA_ROWS, n = min(DELTA_ROWS, end - row - j0);  // this CTA's rows: row + j0 ...
+  if (n <= 0) return;
+  float *out = a.delta + (a.by_seg ? int64_t(blockIdx.y) * 16 : int64_t(row)) * a.M + int64_t(j0) * a.M;
+  row += j0;
+  if (tid < n) {
+    const int sg = first_segment(a.seg_offsets, a.segs, row + tid);
+    int ad = sg < a.segs && a.seg_offsets[sg] <= row + tid ? a.seg_adapter[sg] : -1;
+    if (ad >= a.n_adapters) ad = -1;
     ads[tid] = ad;
   }
   const int pieces = a.rank / 8;
@@ -252,7 +276,7 @@ __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
   __syncthreads();
   const int f = blockIdx.x * 128 + tid;
   if (f >= a.M) return;
-  float *out = a.delta + (a.by_seg ? int64_t(s) * 16 : int64_t(row)) * a.M + f;
+  out += f;
   uint4 w[MAX_RANK / 8];
   int prev = -1;
   for (int j = 0; j < n; ++j) {
@@ -279,19 +303,187 @@ __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
       for (int i = 0; i < MAX_RANK / 8; ++i) {
         if (i * 8 >= a.rank) break;
         const uint4 y = *reinterpret_cast<const uint4 *>(&us[j][i * 8]);
-        d = fmaf(bf16_lo(w[i].x), bf16_lo(y.x), d); d = fmaf(bf16_hi(w[i].x), bf16_hi(y.x), d);
-        d = fmaf(bf16_lo(w[i].y), bf16_lo(y.y), d); d = fmaf(bf16_hi(w[i].y), bf16_hi(y.y), d);
-        d = fmaf(bf16_lo(w[i].z), bf16_lo(y.z), d); d = fmaf(bf16_hi(w[i].z), bf16_hi(y.z), d);
-        d = fmaf(bf16_lo(w[i].w), bf16_lo(y.w), d); d = fmaf(bf16_hi(w[i].w), bf16_hi(y.w), d);
+        d = dot8(w[i], y, d);
       }
     }
     out[int64_t(j) * a.M] = d;
   }
 }
 
+struct ProjArgs {
+  const int32_t *seg_offsets, *seg_adapter;
+  int segs, n_adapters, T, C, M, rank;  // C: reduction, M: output columns
+  const uint16_t *u, *ext;              // u / du [T][rank]; lora_b [n][M][rank], or lora_a [n][rank][M] (TRANS)
+  uint16_t *out;
+  int64_t ldo;
+  int32_t *err;
+};
+
+template <bool TRANS, int ROWS>
+struct ProjCfg {
+  static constexpr int BJ = 64, RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
+  static constexpr int Z = ROWS * CC * 2, P = BJ * CC * 2;  // bytes; TRANS: CC rows of 64 columns
+  static constexpr int STAGE = Z + P, LD = BJ + 1;
+  static constexpr int RED = KW * ROWS * LD * 4;
+  static constexpr int STAGES = 120 * 1024 / STAGE < RING_MAX ? 120 * 1024 / STAGE : RING_MAX;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + RED + int(sizeof(Ring));
+  static_assert(SMEM <= 200 * 1024, "shared memory budget");
+};
+
+// The projection of a decode-sized batch with its adapters: out = z W^T + u B_a^T
+// (z = x), or z W + du A_a (z = dy, TRANS). W is read once per ROWS rows, so W's
+// bytes bound it and the SMs have to share them: a cluster of CTAs takes the
+// same ROWS x 64 outputs and splits the reduction; the partial sums meet through
+// distributed shared memory, each CTA adding and finishing its share of the
+// rows in a fixed order. W and the rows stream before u is there (the launch
+// before computes it); the epilogue waits for it.
+template <bool TRANS, int ROWS>
+__global__ void __launch_bounds__(CONSUMERS + 32)
+    proj_kernel(const ProjArgs a, const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_w) {
+  using Cfg = ProjCfg<TRANS, ROWS>;
+  constexpr int BJ = Cfg::BJ, LD = Cfg::LD;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int ads[ROWS];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *red = reinterpret_cast<float *>(sm + Cfg::STAGES * Cfg::STAGE);
+  Ring &ring = *reinterpret_cast<Ring *>(sm + Cfg::STAGES * Cfg::STAGE + Cfg::RED);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int parts = int(cluster.num_blocks()), part = int(cluster.block_rank());
+  ring_init(ring, Cfg::STAGES);
+  pdl_trigger();
+  const int row0 = blockIdx.y * ROWS, j0 = int(blockIdx.x) / parts * BJ;
+  const int end = min(max(a.seg_offsets[a.segs], 0), a.T);
+  const int nc = (a.C + Cfg::CC - 1) / Cfg::CC, c_lo = nc * part / parts, c_hi = nc * (part + 1) / parts;
+  int slot = 0, round = 0;
+  bool ok = true;
+  if (warp == 8) {
+    for (int c = c_lo; c < c_hi && ok; ++c) {
+      ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
+      if (!ok) break;
+      if (tma::elect_one()) {
+        uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+        tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
+        if (TRANS) tma::tma_load_2d(p, &tm_w, j0, c * Cfg::CC, &ring.full[slot]);
+#pragma unroll
+        for (int b = 0; b < Cfg::CC / 64; ++b) {
+          if (!TRANS) tma::tma_load_2d(p + b * BJ * 128, &tm_w, c * Cfg::CC + b * 64, j0, &ring.full[slot]);
+          tma::tma_load_2d(z + b * ROWS * 128, &tm_z, c * Cfg::CC + b * 64, row0, &ring.full[slot]);
+        }
+      }
+      __syncwarp();
+      if (++slot == Cfg::STAGES) { slot = 0; ++round; }
+    }
+  } else {
+    if (tid < ROWS) {  // the rows' adapters
+      const int row = row0 + tid;
+      int ad = -1;
+      if (row < end) {
+        const int sg = first_segment(a.seg_offsets, a.segs, row);
+        if (sg < a.segs && a.seg_offsets[sg] <= row) ad = a.seg_adapter[sg];
+        if (ad >= a.n_adapters) ad = -1;
+      }
+      ads[tid] = ad;
+    }
+    const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
+    float acc[BJ / 8][4];
+#pragma unroll
+    for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+    for (int c = c_lo; c < c_hi; ++c) {
+      ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
+      if (!ok) break;
+      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+#pragma unroll
+      for (int i = 0; i < Cfg::CC / (16 * Cfg::KW); ++i) {
+        const int kk = kw * (Cfg::CC / (16 * Cfg::KW)) + i;
+        uint32_t af[4];
+        ldsm4<false>(af, sw128(z + (kk >> 2) * ROWS * 128, rw * 16 + (lane & 15), (kk & 3) * 2 + (lane >> 4)));
+#pragma unroll
+        for (int jp = 0; jp < BJ / 16; ++jp) {
+          uint32_t bf[4];
+          if (TRANS)
+            ldsm4<true>(bf, sw128(p, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, jp * 2 + (lane >> 4)));
+          else
+            ldsm4<false>(bf, sw128(p + (kk >> 2) * BJ * 128, jp * 16 + (lane & 7) + (lane >> 4) * 8,
+                                   (kk & 3) * 2 + ((lane >> 3) & 1)));
+          mma_16816(acc[2 * jp], af, bf[0], bf[1]);
+          mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+      if (++slot == Cfg::STAGES) { slot = 0; ++round; }
+    }
+#pragma unroll
+    for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[(kw * ROWS + rw * 16 + g + (q >> 1) * 8) * LD + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
+    consumer_sync();
+    if (Cfg::KW > 1) {  // this CTA's sums, into the first warp's place
+      for (int p = tid; p < ROWS * BJ; p += CONSUMERS) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < Cfg::KW; ++k) v += red[(k * ROWS + p / BJ) * LD + p % BJ];
+        red[p / BJ * LD + p % BJ] = v;
+      }
+    }
+  }
+  cluster.sync();  // every CTA's sums are in its shared memory
+  if (warp < 8) {
+    pdl_wait();
+    const int r_lo = ROWS * part / parts, r_hi = ROWS * (part + 1) / parts;
+    for (int p = tid; p < (r_hi - r_lo) * (BJ / 2); p += CONSUMERS) {
+      const int r = r_lo + p / (BJ / 2), j = p % (BJ / 2) * 2, row = row0 + r, n = j0 + j;
+      if (row >= end || n >= a.M) continue;
+      float v0 = 0.f, v1 = 0.f;
+      for (int q = 0; q < parts; ++q) {
+        const float *o = cluster.map_shared_rank(red, q) + r * LD + j;
+        v0 += o[0];
+        v1 += o[1];
+      }
+      const int ad = ads[r];
+      if (ad >= 0) {
+        float d0 = 0.f, d1 = 0.f;
+        const uint4 *u = reinterpret_cast<const uint4 *>(a.u + int64_t(row) * a.rank);
+        if (TRANS) {
+          const uint16_t *w = a.ext + int64_t(ad) * a.rank * a.M + n;
+#pragma unroll 2
+          for (int i = 0; i < a.rank / 8; ++i) {
+            const uint4 y = u[i];
+            const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t w2 = *reinterpret_cast<const uint32_t *>(w + int64_t(8 * i + k) * a.M);
+              const float f = (k & 1) ? bf16_hi(yw[k >> 1]) : bf16_lo(yw[k >> 1]);
+              d0 = fmaf(bf16_lo(w2), f, d0);
+              d1 = fmaf(bf16_hi(w2), f, d1);
+            }
+          }
+        } else {
+          const uint4 *w0 = reinterpret_cast<const uint4 *>(a.ext + (int64_t(ad) * a.M + n) * a.rank);
+          const uint4 *w1 = w0 + a.rank / 8;
+#pragma unroll 2
+          for (int i = 0; i < a.rank / 8; ++i) {
+            const uint4 y = u[i], x0 = w0[i], x1 = w1[i];
+            d0 = dot8(x0, y, d0);
+            d1 = dot8(x1, y, d1);
+          }
+        }
+        v0 += d0;
+        v1 += d1;
+      }
+      *reinterpret_cast<uint32_t *>(a.out + int64_t(row) * a.ldo + n) = pack_bf16x2(v0, v1);
+    }
+  }
+  cluster.sync();  // no CTA leaves while its sums are read
+}
+
 struct AdapterGradArgs {
   const int32_t *seg_offsets, *seg_adapter;
-  int segs, T, N, K, rank;
+  int segs, n_adapters, T, N, K, rank;
   int slabs_a;        // 64-column slabs of x; the others are dy's
   int stages;
   uint16_t *da, *db;  // [n][rank][K], [n][N][rank]
@@ -331,54 +523,67 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   ring_init(ring, a.stages);
   pdl_trigger();
   pdl_wait();
-  const int ad = blockIdx.y;
   const bool is_a = int(blockIdx.x) < a.slabs_a;
   const int c0 = (is_a ? blockIdx.x : blockIdx.x - a.slabs_a) * AG_COLS, C = is_a ? a.K : a.N;
   int slot = 0, round = 0;
   bool ok = true;
   if (warp == 8) {
     const CUtensorMap *tz = is_a ? &tm_x : &tm_dy, *tp = is_a ? &tm_du : &tm_u;
-    for (int s0 = 0; s0 < a.segs && ok; s0 += 32) {  // the lanes look at 32 segments
-      const int s = s0 + lane;
-      int lo = 0, hi = 0;
-      if (s < a.segs && a.seg_adapter[s] == ad) {
-        lo = max(a.seg_offsets[s], 0);
-        hi = min(a.seg_offsets[s + 1], a.T);
-      }
-      for (uint32_t m = __ballot_sync(0xffffffffu, hi > lo); m && ok; m &= m - 1) {
-        const int l = __ffs(m) - 1, e = __shfl_sync(0xffffffffu, hi, l);
-        for (int r = __shfl_sync(0xffffffffu, lo, l); r < e && ok; r += AG_ROWS) {
-          ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
-          if (ok && tma::elect_one()) {
-            uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
-            ring.rows[slot] = min(AG_ROWS, e - r);
-            tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
-            tma::tma_load_2d(z, tz, c0, r, &ring.full[slot]);
-            tma::tma_load_2d(p, tp, 0, r, &ring.full[slot]);
-            if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp, 64, r, &ring.full[slot]);
+    for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
+      for (int s0 = 0; s0 < a.segs && ok; s0 += 32) {  // the lanes look at 32 segments
+        const int s = s0 + lane;
+        int lo = 0, hi = 0;
+        if (s < a.segs && a.seg_adapter[s] == ad) {
+          lo = max(a.seg_offsets[s], 0);
+          hi = min(a.seg_offsets[s + 1], a.T);
+        }
+        for (uint32_t m = __ballot_sync(0xffffffffu, hi > lo); m && ok; m &= m - 1) {
+          const int l = __ffs(m) - 1, e = __shfl_sync(0xffffffffu, hi, l);
+          for (int r = __shfl_sync(0xffffffffu, lo, l); r < e && ok; r += AG_ROWS) {
+            ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
+            if (ok && tma::elect_one()) {
+              uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+              ring.rows[slot] = min(AG_ROWS, e - r);
+              tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
+              tma::tma_load_2d(z, tz, c0, r, &ring.full[slot]);
+              tma::tma_load_2d(p, tp, 0, r, &ring.full[slot]);
+              if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp, 64, r, &ring.full[slot]);
+            }
+            __syncwarp();
+            if (++slot == a.stages) { slot = 0; ++round; }
           }
-          __syncwarp();
-          if (++slot == a.stages) { slot = 0; ++round; }
         }
       }
+      if (!ok) break;
+      ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);  // the adapter's end: a stage without rows
+      if (ok && tma::elect_one()) {
+        ring.rows[slot] = 0;
+        tma::mbar_arrive(&ring.full[slot]);
+      }
+      __syncwarp();
+      if (++slot == a.stages) { slot = 0; ++round; }
     }
-    if (ok && ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err) && tma::elect_one()) {
-      ring.rows[slot] = 0;
-      tma::mbar_arrive(&ring.full[slot]);
-    }
-    __syncwarp();
     return;
   }
   const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;
+  for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
   float acc[RJ / 8][4];
 #pragma unroll
   for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+  bool any = false;
   for (;;) {
-    if (!ring_wait(ring, &ring.full[slot], round & 1, a.err)) break;
+    ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
+    if (!ok) break;
     const int rows = ring.rows[slot];
-    if (rows == 0) break;
+    if (rows == 0) {
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+      if (++slot == a.stages) { slot = 0; ++round; }
+      break;
+    }
+    any = true;
     const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
 #pragma unroll
     for (int i = 0; i < AG_ROWS / 32; ++i) {
@@ -408,18 +613,18 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   }
   // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
   auto at = [&](int j, int q) -> float & { return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8]; };
-  if (kg == 1) {
+  if (any && kg == 1) {
 #pragma unroll
     for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
   }
   consumer_sync();
-  if (kg == 0) {
+  if (kg == 0) {  // (without rows: the zeros of acc)
 #pragma unroll
     for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+      for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q] + (any ? at(j, q) : 0.f);
   }
   consumer_sync();
   if (is_a) {  // [rank][K]: 64 columns of each row
@@ -436,6 +641,8 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
         *reinterpret_cast<uint32_t *>(a.db + (int64_t(ad) * a.N + c0 + c) * a.rank + j) =
             pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
     }
+  }
+  consumer_sync();  // the sums are read
   }
 }
 
@@ -484,16 +691,59 @@ static int launch_shrink(const ShrinkArgs &a, const Rows &z, const uint16_t *p, 
                         : launch_shrink_as<64, TRANS, 64>(a, z, p, s, what);
 }
 
+template <bool TRANS, int ROWS>
+static int launch_proj_as(const ProjArgs &a, const Rows &z, const uint16_t *w, cudaStream_t s, const char *what) {
+  using Cfg = ProjCfg<TRANS, ROWS>;
+  CUtensorMap tz, tw;
+  bool ok = map_bf16(&tz, z.p, 2, {z.width, a.T, 1, 1}, {z.ld, 0, 0}, {64, ROWS, 1, 1});
+  if (TRANS)
+    ok &= map_bf16(&tw, w, 2, {a.M, a.C, 1, 1}, {a.M, 0, 0}, {64, Cfg::CC, 1, 1});
+  else
+    ok &= map_bf16(&tw, w, 2, {a.C, a.M, 1, 1}, {a.C, 0, 0}, {64, Cfg::BJ, 1, 1});
+  if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
+  auto *kernel = proj_kernel<TRANS, ROWS>;
+  const int st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg::SMEM, what);
+  if (st != MOE_OK) return st;
+  const int tiles = (a.M + Cfg::BJ - 1) / Cfg::BJ, row_tiles = (a.T + ROWS - 1) / ROWS;
+  const int nc = (a.C + Cfg::CC - 1) / Cfg::CC;
+  int parts = 1;  // until the CTAs cover the SMs, each with two stages of work at least
+  while (parts < 8 && tiles * row_tiles * parts * 2 <= sm_count() && nc >= parts * 4) parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles * parts), unsigned(row_tiles));
+  cfg.blockDim = dim3(CONSUMERS + 32);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(parts);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, tz, tw);
+  if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+template <bool TRANS>
+static int launch_proj(const ProjArgs &a, const Rows &z, const uint16_t *w, cudaStream_t s, const char *what) {
+  return a.T <= 16   ? launch_proj_as<TRANS, 16>(a, z, w, s, what)
+         : a.T <= 32 ? launch_proj_as<TRANS, 32>(a, z, w, s, what)
+                     : launch_proj_as<TRANS, 64>(a, z, w, s, what);
+}
+
 template <bool COLS>
 static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
-  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.segs));
+  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.by_seg ? a.segs : (a.T + 15) / 16), 16 / DELTA_ROWS);
   const cudaError_t e = launch_pdl(delta_kernel<COLS>, grid, dim3(128), 0, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
 
 template <int RJ, int AG_ROWS>
-static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows &x, const Rows &dy, const Rows &u,
+static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &dy, const Rows &u,
                                   const Rows &du, cudaStream_t s, const char *what) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   CUtensorMap tx, tdy, tu, tdu;
@@ -503,8 +753,12 @@ static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows 
   for (int i = 0; i < 4; ++i)
     ok &= map_bf16(m[i], r[i]->p, 2, {r[i]->width, a.T, 1, 1}, {r[i]->ld, 0, 0}, {64, AG_ROWS, 1, 1});
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
-  const dim3 grid(unsigned(a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS), unsigned(n_adapters));
-  // one CTA per SM: a deep ring; more: shallow rings, so that several CTAs share an SM
+  // One CTA per SM: a deep ring; more: shallow rings, so that several CTAs share
+  // an SM, each going through every grid.y-th adapter (about four CTAs an SM).
+  const int slabs = a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS;
+  int ny = (4 * sm_count() + slabs - 1) / slabs;
+  if (ny > a.n_adapters) ny = a.n_adapters;
+  const dim3 grid{unsigned(slabs), unsigned(ny)};
   a.stages = int64_t(grid.x) * grid.y <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
   if (st != MOE_OK) return st;
@@ -515,12 +769,12 @@ static int launch_adapter_grad_as(AdapterGradArgs a, int n_adapters, const Rows 
 }
 
 template <int AG_ROWS>
-static int launch_adapter_grad(const AdapterGradArgs &a, int n_adapters, const Rows &x, const Rows &dy, const Rows &u,
+static int launch_adapter_grad(const AdapterGradArgs &a, const Rows &x, const Rows &dy, const Rows &u,
                                const Rows &du, cudaStream_t s, const char *what) {
-  return a.rank <= 16   ? launch_adapter_grad_as<16, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
-         : a.rank <= 32 ? launch_adapter_grad_as<32, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
-         : a.rank <= 64 ? launch_adapter_grad_as<64, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what)
-                        : launch_adapter_grad_as<128, AG_ROWS>(a, n_adapters, x, dy, u, du, s, what);
+  return a.rank <= 16   ? launch_adapter_grad_as<16, AG_ROWS>(a, x, dy, u, du, s, what)
+         : a.rank <= 32 ? launch_adapter_grad_as<32, AG_ROWS>(a, x, dy, u, du, s, what)
+         : a.rank <= 64 ? launch_adapter_grad_as<64, AG_ROWS>(a, x, dy, u, du, s, what)
+                        : launch_adapter_grad_as<128, AG_ROWS>(a, x, dy, u, du, s, what);
 }
 
 // Rows of the fp32 sums for shared 16-row blocks: 16 per segment, or one per
@@ -558,9 +812,10 @@ static int check_rows(const char *who, const char *name, const void *p, int64_t 
   return MOE_OK;
 }
 
-// Up to this many rows the projection runs as a weight stream, all rows in one
-// pass over W.
-constexpr int GEMV_MAX_T = 64;
+// Up to this many rows the projection is a weight stream (proj_kernel), one
+// pass over W; the forward pass of the fewest rows runs in gemm_gemv.cu.
+constexpr int PROJ_MAX_T = 64;
+constexpr int GEMV_MAX_T = 8;
 
 static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const int32_t *seg_adapter, int T, int S,
                              int n_adapters, int rank, int N, int K, void *out, int64_t ldo, int32_t *err) {
@@ -627,7 +882,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
   cudaStream_t s = as_stream(stream);
   int32_t *err = static_cast<int32_t *>(ws);
 
-  if (T <= lora::GEMV_MAX_T || T < 16 * S) {
+  if (T <= lora::GEMV_MAX_T || T < 16 * int64_t(S)) {
     // short segments: each streams its adapter's A
     GemvArgs v = {};
     v.in = x; v.ldi = ldx; v.offsets = seg_offsets; v.index = seg_adapter;
@@ -647,6 +902,10 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.seg_offsets = seg_offsets; v.seg_adapter = seg_adapter; v.segs = S; v.n_adapters = n_adapters; v.rank = rank;
     v.u = u; v.lora_b = lora_b;
     return launch_gemm_gemv(v, 1, s, who);
+  }
+  if (T <= lora::PROJ_MAX_T) {
+    const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, K, N, rank, u, lora_b, y, ldy, err};
+    return lora::launch_proj<false>(v, {x, ldx, K}, w, s, who);
   }
   TcGemmArgs g = lora::projection(GEMM_FWD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, y, ldy, err);
   g.ext_a = lora_b;
@@ -687,7 +946,10 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
   int32_t *err = static_cast<int32_t *>(ws);
   const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, 0, du, err};
   if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
-  if (dx) {
+  if (dx && T <= lora::PROJ_MAX_T) {
+    const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, du, lora_a, dx, lddx, err};
+    if ((st = lora::launch_proj<true>(v, {dy, lddy, N}, w, s, who)) != MOE_OK) return st;
+  } else if (dx) {
     TcGemmArgs g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
     g.ext_a = lora_a;
     g.ext_b = du;
@@ -696,11 +958,11 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
     if ((st = launch_gemm_tc(GEMM_DGRAD, g, op, s, who)) != MOE_OK) return st;
   }
   if (!d_lora_a) return MOE_OK;
-  const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, T, N, K, rank, (K + lora::AG_COLS - 1) / lora::AG_COLS,
+  const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, (K + lora::AG_COLS - 1) / lora::AG_COLS,
                                    0, d_lora_a, d_lora_b, err};
   const char *what = "moe_lora_linear_backward (adapters)";
   const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
   // loads of 128 rows, or of 32 where segments are short on average
-  return T >= 64 * S ? lora::launch_adapter_grad<128>(q, n_adapters, rx, rdy, ru, rdu, s, what)
-                     : lora::launch_adapter_grad<32>(q, n_adapters, rx, rdy, ru, rdu, s, what);
+  return T >= 64 * S ? lora::launch_adapter_grad<128>(q, rx, rdy, ru, rdu, s, what)
+                     : lora::launch_adapter_grad<32>(q, rx, rdy, ru, rdu, s, what);
 }
