@@ -23,6 +23,7 @@ namespace gv {
 constexpr int COLS = 16;     // output columns per CTA
 constexpr int LD = COLS + 1; // row stride of the partial sums
 constexpr int CH = 4;        // 32-wide chunks of a piece
+constexpr int MAXNT = 2;     // 8-row tiles of `in` per pass
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -105,13 +106,13 @@ __device__ __forceinline__ float adapter_dot(const GemvArgs &a, int row, int n) 
   return d;
 }
 
-template <int MAXNT, int WARPS>
+template <int WARPS>
 struct Cfg {
   static constexpr int SMEM = WARPS * MAXNT * 8 * LD * 4;
 };
 
-template <int MAXNT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, MAXNT == 2 ? 24 / WARPS : 16 / WARPS) gemv_kernel(const GemvArgs a) {
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const GemvArgs a) {
   extern __shared__ float red[];
   __shared__ int found[32], which;
   const bool late = a.seg_adapter != nullptr;  // the previous launch only writes u
@@ -159,15 +160,9 @@ __global__ void __launch_bounds__(WARPS * 32, MAXNT == 2 ? 24 / WARPS : 16 / WAR
     if (!none) {
       if (rows <= 8) {
         rows_pass<1, WARPS>(a, w, n0, lo + r0, rows, red);
-      } else if (MAXNT == 2 || rows <= 16) {
+      } else {
         nt = 2;
         rows_pass<2, WARPS>(a, w, n0, lo + r0, rows, red);
-      } else if (MAXNT >= 4 && (MAXNT == 4 || rows <= 32)) {
-        nt = 4;
-        rows_pass<MAXNT >= 4 ? 4 : 1, WARPS>(a, w, n0, lo + r0, rows, red);
-      } else {
-        nt = MAXNT;
-        rows_pass<MAXNT, WARPS>(a, w, n0, lo + r0, rows, red);
       }
     }
     if (late && r0 == 0) pdl_wait();
@@ -194,15 +189,15 @@ __global__ void __launch_bounds__(WARPS * 32, MAXNT == 2 ? 24 / WARPS : 16 / WAR
   }
 }
 
-template <int MAXNT, int WARPS>
+template <int WARPS>
 static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
-  constexpr size_t smem = Cfg<MAXNT, WARPS>::SMEM;
+  constexpr size_t smem = Cfg<WARPS>::SMEM;
   if (smem > 48 * 1024) {
-    const int st = allow_dynamic_smem(reinterpret_cast<const void *>(gemv_kernel<MAXNT, WARPS>), smem, what);
+    const int st = allow_dynamic_smem(reinterpret_cast<const void *>(gemv_kernel<WARPS>), smem, what);
     if (st != MOE_OK) return st;
   }
   const dim3 grid(unsigned((a.N + COLS - 1) / COLS), unsigned(grid_groups));
-  const cudaError_t e = launch_pdl(gemv_kernel<MAXNT, WARPS>, grid, dim3(WARPS * 32), smem, s, a);
+  const cudaError_t e = launch_pdl(gemv_kernel<WARPS>, grid, dim3(WARPS * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -210,11 +205,11 @@ static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const c
 }  // namespace gv
 
 int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
-  if (a.seg_adapter) return gv::launch_as<2, 8>(a, grid_groups, s, what);  // one group of few rows
+  if (a.seg_adapter) return gv::launch_as<8>(a, grid_groups, s, what);  // one group of few rows
   // few CTAs: more warps share a CTA's reduction
   const int64_t ctas = int64_t(grid_groups) * ((a.N + 15) / 16);
-  if (ctas <= 2 * 148) return gv::launch_as<2, 16>(a, grid_groups, s, what);
-  return gv::launch_as<2, 4>(a, grid_groups, s, what);
+  if (ctas <= 2 * 148) return gv::launch_as<16>(a, grid_groups, s, what);
+  return gv::launch_as<4>(a, grid_groups, s, what);
 }
 
 }  // namespace moe

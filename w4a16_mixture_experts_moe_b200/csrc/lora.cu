@@ -567,82 +567,91 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   }
   const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;
   for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
-  float acc[RJ / 8][4];
+    float acc[RJ / 8][4];
 #pragma unroll
-  for (int j = 0; j < RJ / 8; ++j)
+    for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-  bool any = false;
-  for (;;) {
-    ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
-    if (!ok) break;
-    const int rows = ring.rows[slot];
-    if (rows == 0) {
+      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+    bool any = false, more = true;
+    while (more) {
+      ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
+      if (!ok) break;
+      const int rows = ring.rows[slot];
+      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+      more = rows > 0;
+      any |= more;
+#pragma unroll
+      for (int i = 0; i < AG_ROWS / 32; ++i) {
+        const int kk = kg * (AG_ROWS / 32) + i;
+        if (kk * 16 >= rows) break;
+        uint32_t af[4];
+        ldsm4<true>(af, sw128(z, kk * 16 + (lane & 7) + (lane >> 4) * 8, cg * 2 + ((lane >> 3) & 1)));
+        uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
+        if (rows < kk * 16 + 16) {
+          const int left = rows - kk * 16 - 2 * t4;
+          m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+          m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
+          af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1;
+        }
+#pragma unroll
+        for (int jp = 0; jp < RJ / 16; ++jp) {
+          uint32_t bf[4];
+          ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8,
+                                (jp & 3) * 2 + (lane >> 4)));
+          mma_16816(acc[2 * jp], af, bf[0] & m0, bf[1] & m1);
+          mma_16816(acc[2 * jp + 1], af, bf[2] & m0, bf[3] & m1);
+        }
+      }
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
       if (++slot == a.stages) { slot = 0; ++round; }
-      break;
     }
-    any = true;
-    const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
-#pragma unroll
-    for (int i = 0; i < AG_ROWS / 32; ++i) {
-      const int kk = kg * (AG_ROWS / 32) + i;
-      if (kk * 16 >= rows) break;
-      uint32_t af[4];
-      ldsm4<true>(af, sw128(z, kk * 16 + (lane & 7) + (lane >> 4) * 8, cg * 2 + ((lane >> 3) & 1)));
-      uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
-      if (rows < kk * 16 + 16) {
-        const int left = rows - kk * 16 - 2 * t4;
-        m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-        m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
-        af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1;
+    if (!any) {  // no rows: zeros
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      for (int p = tid; p < AG_COLS * a.rank / 8; p += CONSUMERS) {
+        if (is_a) {
+          const int j = p / (AG_COLS / 8), c = c0 + p % (AG_COLS / 8) * 8;
+          if (c < C) *reinterpret_cast<uint4 *>(a.da + (int64_t(ad) * a.rank + j) * a.K + c) = zero;
+        } else if (c0 + p / (a.rank / 8) < C) {
+          *reinterpret_cast<uint4 *>(a.db + (int64_t(ad) * a.N + c0) * a.rank + p * 8) = zero;
+        }
       }
+      continue;
+    }
+    // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
+    auto at = [&](int j, int q) -> float & {
+      return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8];
+    };
+    if (kg == 1) {
 #pragma unroll
-      for (int jp = 0; jp < RJ / 16; ++jp) {
-        uint32_t bf[4];
-        ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8,
-                              (jp & 3) * 2 + (lane >> 4)));
-        mma_16816(acc[2 * jp], af, bf[0] & m0, bf[1] & m1);
-        mma_16816(acc[2 * jp + 1], af, bf[2] & m0, bf[3] & m1);
+      for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
+    }
+    consumer_sync();
+    if (kg == 0) {
+#pragma unroll
+      for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+    }
+    consumer_sync();
+    if (is_a) {  // [rank][K]: 64 columns of each row
+      for (int p = tid; p < a.rank * (AG_COLS / 2); p += CONSUMERS) {
+        const int j = p / (AG_COLS / 2), c = p % (AG_COLS / 2) * 2;
+        if (c0 + c < C)
+          *reinterpret_cast<uint32_t *>(a.da + (int64_t(ad) * a.rank + j) * a.K + c0 + c) =
+              pack_bf16x2(red[j * Cfg::LD + c], red[j * Cfg::LD + c + 1]);
+      }
+    } else {     // [N][rank]: 64 whole rows
+      for (int p = tid; p < AG_COLS * (a.rank / 2); p += CONSUMERS) {
+        const int c = p / (a.rank / 2), j = p % (a.rank / 2) * 2;
+        if (c0 + c < C)
+          *reinterpret_cast<uint32_t *>(a.db + (int64_t(ad) * a.N + c0 + c) * a.rank + j) =
+              pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
       }
     }
-    __syncwarp();
-    if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
-    if (++slot == a.stages) { slot = 0; ++round; }
-  }
-  // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
-  auto at = [&](int j, int q) -> float & { return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8]; };
-  if (any && kg == 1) {
-#pragma unroll
-    for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
-  }
-  consumer_sync();
-  if (kg == 0) {  // (without rows: the zeros of acc)
-#pragma unroll
-    for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q] + (any ? at(j, q) : 0.f);
-  }
-  consumer_sync();
-  if (is_a) {  // [rank][K]: 64 columns of each row
-    for (int p = tid; p < a.rank * (AG_COLS / 2); p += CONSUMERS) {
-      const int j = p / (AG_COLS / 2), c = p % (AG_COLS / 2) * 2;
-      if (c0 + c < C)
-        *reinterpret_cast<uint32_t *>(a.da + (int64_t(ad) * a.rank + j) * a.K + c0 + c) =
-            pack_bf16x2(red[j * Cfg::LD + c], red[j * Cfg::LD + c + 1]);
-    }
-  } else {     // [N][rank]: 64 whole rows
-    for (int p = tid; p < AG_COLS * (a.rank / 2); p += CONSUMERS) {
-      const int c = p / (a.rank / 2), j = p % (a.rank / 2) * 2;
-      if (c0 + c < C)
-        *reinterpret_cast<uint32_t *>(a.db + (int64_t(ad) * a.N + c0 + c) * a.rank + j) =
-            pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
-    }
-  }
-  consumer_sync();  // the sums are read
+    consumer_sync();  // the sums are read
   }
 }
 
@@ -812,9 +821,11 @@ static int check_rows(const char *who, const char *name, const void *p, int64_t 
   return MOE_OK;
 }
 
-// Up to this many rows the projection is a weight stream (proj_kernel), one
-// pass over W; the forward pass of the fewest rows runs in gemm_gemv.cu.
-constexpr int PROJ_MAX_T = 64;
+// Up to this many rows the projection is a weight stream (proj_kernel: N = 4096,
+// K = 2048, four requests of rank 16: 18 us at 128 rows and 35 us at 192,
+// where the tensor-core engine takes 22 us at both); the forward pass of the
+// fewest rows runs in gemm_gemv.cu, with one launch's prologue less to wait for.
+constexpr int PROJ_MAX_T = 128;
 constexpr int GEMV_MAX_T = 8;
 
 static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const int32_t *seg_adapter, int T, int S,
