@@ -537,12 +537,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
-  pdl_trigger();
-  // Only the epilogue needs the launch before this one when that launch
-  // computes the shared blocks: it waits for what this kernel otherwise reads
-  // before it lets this kernel start.
-  if (MODE == GEMM_WGRAD || !a.delta) pdl_wait();
-
   // ---- prologue: barriers, tensor memory, tile table
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -563,6 +557,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  pdl_trigger();
+  // Only the epilogue needs the launch before this one when that launch
+  // computes the shared blocks: it waits for what this kernel otherwise reads
+  // before it lets this kernel start.
+  if (MODE == GEMM_WGRAD || !a.delta) pdl_wait();
   if (warp == 0) {
     int v[8], local = 0;
     bool bad = false;

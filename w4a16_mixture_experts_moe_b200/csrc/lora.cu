@@ -18,6 +18,8 @@
 // in flight.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "gemm.cuh"
 
 namespace cg = cooperative_groups;
@@ -29,15 +31,15 @@ constexpr int MAX_RANK = 128;
 constexpr int MAX_SEGS = 65535;  // a grid dimension of the decode form
 
 template <bool TRANS>
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *p) {
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   if (TRANS)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+                 : "r"(at));
   else
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+                 : "r"(at));
 }
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -55,7 +57,7 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float d) {
 }
 
 // 16-byte piece c of row r in a 128-byte-swizzled tile.
-__device__ __forceinline__ const uint8_t *sw128(const uint8_t *tile, int r, int c) {
+__device__ __forceinline__ uint32_t sw128(uint32_t tile, int r, int c) {
   return tile + r * 128 + ((c ^ (r & 7)) << 4);
 }
 
@@ -91,24 +93,54 @@ struct ShrinkArgs {
   const float *scale;
   int segs, n_adapters, T, C, rank;
   int split;          // CTAs that share a row tile's segments
-  int stages;
   uint16_t *out;      // [T][rank]
   int32_t *err;
 };
 
-// A tile of ROWS rows and BJ ranks; RW x KW = 8 warps: RW 16-row tiles, KW
-// warps that split each stage's CC reduction columns.
+// A tile of ROWS rows and BJ ranks; RW x KW = 8 warps: RW of MT 16-row tiles
+// each, and KW that split each stage's CC reduction columns. (Two row tiles a
+// warp halve the reads of P from shared memory, which bound the wide tile.)
 template <int BJ, bool TRANS, int ROWS>
 struct ShrinkCfg {
-  static constexpr int RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
+  static constexpr int MT = ROWS == 64 ? 2 : 1, RW = ROWS / 16 / MT, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
   static constexpr int Z = ROWS * CC * 2;              // bytes: boxes of 64 columns
   static constexpr int P = TRANS ? CC * 128 : BJ * CC * 2;  // TRANS: CC rows of 64 ranks
   static constexpr int STAGE = Z + P;
   static constexpr int RED = KW * ROWS * (BJ + 1) * 4;
-  static constexpr int STAGES = 160 * 1024 / STAGE < RING_MAX ? 160 * 1024 / STAGE : RING_MAX;
+  static constexpr int STAGES = 128 * 1024 / STAGE < RING_MAX ? 128 * 1024 / STAGE : RING_MAX;
   static constexpr int SMEM = 1024 + STAGES * STAGE + RED + int(sizeof(Ring));
   static_assert(KW * 16 <= CC && CC % (KW * 16) == 0 && SMEM <= 227 * 1024, "tile shape");
 };
+
+// One stage's products for a warp: acc += z [16 MT rows][CC / KW] P^T. z: boxes of
+// ROWS rows x 64 columns; P behind it: boxes of BJ rows (ranks, or columns of W)
+// x 64, or CC rows of 64 (TRANS).
+template <class Cfg, int BJ, bool TRANS, int ROWS>
+__device__ __forceinline__ void stage_mma(float (&acc)[Cfg::MT][BJ / 8][4], uint32_t z, int rw, int kw) {
+  const uint32_t p = z + Cfg::Z;
+  const int lane = threadIdx.x & 31, lo = lane & 7, m8 = (lane >> 3) & 1, hi = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < Cfg::CC / (16 * Cfg::KW); ++i) {
+    const int kk = kw * (Cfg::CC / (16 * Cfg::KW)) + i;  // 16 columns of the stage
+    uint32_t af[Cfg::MT][4];
+#pragma unroll
+    for (int m = 0; m < Cfg::MT; ++m)
+      ldsm4<false>(af[m], sw128(z + (kk >> 2) * ROWS * 128, (rw * Cfg::MT + m) * 16 + lo + m8 * 8, (kk & 3) * 2 + hi));
+#pragma unroll
+    for (int jp = 0; jp < BJ / 16; ++jp) {
+      uint32_t bf[4];
+      if (TRANS)
+        ldsm4<true>(bf, sw128(p, kk * 16 + lo + m8 * 8, jp * 2 + hi));
+      else
+        ldsm4<false>(bf, sw128(p + (kk >> 2) * BJ * 128, jp * 16 + lo + hi * 8, (kk & 3) * 2 + m8));
+#pragma unroll
+      for (int m = 0; m < Cfg::MT; ++m) {
+        mma_16816(acc[m][2 * jp], af[m], bf[0], bf[1]);
+        mma_16816(acc[m][2 * jp + 1], af[m], bf[2], bf[3]);
+      }
+    }
+  }
+}
 
 // out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]), z = x and P = lora_a, or
 // z = dy and P_a[j][c] = lora_b[a][c][j] (TRANS). A tile may hold several
@@ -124,6 +156,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   float *red = reinterpret_cast<float *>(sm + Cfg::STAGES * Cfg::STAGE);
   Ring &ring = *reinterpret_cast<Ring *>(sm + Cfg::STAGES * Cfg::STAGE + Cfg::RED);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring0 = tma::smem_u32(sm);
   ring_init(ring, Cfg::STAGES);
   pdl_wait();     // in this order: the launches behind this one may start before u is there, but
   pdl_trigger();  // not before what this launch itself waits for
@@ -173,42 +206,29 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       continue;
     }
     const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
-    float acc[BJ / 8][4];
+    float acc[Cfg::MT][BJ / 8][4];
 #pragma unroll
-    for (int j = 0; j < BJ / 8; ++j)
+    for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+      for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
     for (int c = 0; c < nc; ++c) {
       ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
       if (!ok) break;
-      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
-#pragma unroll
-      for (int i = 0; i < Cfg::CC / (16 * Cfg::KW); ++i) {
-        const int kk = kw * (Cfg::CC / (16 * Cfg::KW)) + i;  // 16 columns of the stage
-        uint32_t af[4];
-        ldsm4<false>(af, sw128(z + (kk >> 2) * ROWS * 128, rw * 16 + (lane & 15), (kk & 3) * 2 + (lane >> 4)));
-#pragma unroll
-        for (int jp = 0; jp < BJ / 16; ++jp) {
-          uint32_t bf[4];
-          if (TRANS)  // stored [c][j]
-            ldsm4<true>(bf, sw128(p, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, jp * 2 + (lane >> 4)));
-          else        // stored [j][c]
-            ldsm4<false>(bf, sw128(p + (kk >> 2) * BJ * 128, jp * 16 + (lane & 7) + (lane >> 4) * 8,
-                                   (kk & 3) * 2 + ((lane >> 3) & 1)));
-          mma_16816(acc[2 * jp], af, bf[0], bf[1]);
-          mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
-        }
-      }
+      stage_mma<Cfg, BJ, TRANS, ROWS>(acc, ring0 + slot * Cfg::STAGE, rw, kw);
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
       if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
     // the KW partial sums, added in a fixed order
 #pragma unroll
-    for (int j = 0; j < BJ / 8; ++j)
+    for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        red[(kw * ROWS + rw * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
+      for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          red[(kw * ROWS + (rw * Cfg::MT + i) * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[i][j][q];
     consumer_sync();
     const float sc = a.scale ? a.scale[ad] : 1.f;
     for (int p = tid; p < (hi - lo) * (BJ / 2); p += CONSUMERS) {
@@ -321,7 +341,7 @@ struct ProjArgs {
 
 template <bool TRANS, int ROWS>
 struct ProjCfg {
-  static constexpr int BJ = 64, RW = ROWS / 16, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
+  static constexpr int BJ = 64, MT = ROWS == 64 ? 2 : 1, RW = ROWS / 16 / MT, KW = 8 / RW, CC = ROWS == 16 ? 256 : 128;
   static constexpr int Z = ROWS * CC * 2, P = BJ * CC * 2;  // bytes; TRANS: CC rows of 64 columns
   static constexpr int STAGE = Z + P, LD = BJ + 1;
   static constexpr int RED = KW * ROWS * LD * 4;
@@ -350,6 +370,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = int(cluster.num_blocks()), part = int(cluster.block_rank());
+  const uint32_t ring0 = tma::smem_u32(sm);
   ring_init(ring, Cfg::STAGES);
   pdl_trigger();
   const int row0 = blockIdx.y * ROWS, j0 = int(blockIdx.x) / parts * BJ;
@@ -386,41 +407,28 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       ads[tid] = ad;
     }
     const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
-    float acc[BJ / 8][4];
+    float acc[Cfg::MT][BJ / 8][4];
 #pragma unroll
-    for (int j = 0; j < BJ / 8; ++j)
+    for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+      for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
     for (int c = c_lo; c < c_hi; ++c) {
       ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
       if (!ok) break;
-      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
-#pragma unroll
-      for (int i = 0; i < Cfg::CC / (16 * Cfg::KW); ++i) {
-        const int kk = kw * (Cfg::CC / (16 * Cfg::KW)) + i;
-        uint32_t af[4];
-        ldsm4<false>(af, sw128(z + (kk >> 2) * ROWS * 128, rw * 16 + (lane & 15), (kk & 3) * 2 + (lane >> 4)));
-#pragma unroll
-        for (int jp = 0; jp < BJ / 16; ++jp) {
-          uint32_t bf[4];
-          if (TRANS)
-            ldsm4<true>(bf, sw128(p, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, jp * 2 + (lane >> 4)));
-          else
-            ldsm4<false>(bf, sw128(p + (kk >> 2) * BJ * 128, jp * 16 + (lane & 7) + (lane >> 4) * 8,
-                                   (kk & 3) * 2 + ((lane >> 3) & 1)));
-          mma_16816(acc[2 * jp], af, bf[0], bf[1]);
-          mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
-        }
-      }
+      stage_mma<Cfg, BJ, TRANS, ROWS>(acc, ring0 + slot * Cfg::STAGE, rw, kw);
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
       if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
 #pragma unroll
-    for (int j = 0; j < BJ / 8; ++j)
+    for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        red[(kw * ROWS + rw * 16 + g + (q >> 1) * 8) * LD + j * 8 + 2 * t4 + (q & 1)] = acc[j][q];
+      for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          red[(kw * ROWS + (rw * Cfg::MT + i) * 16 + g + (q >> 1) * 8) * LD + j * 8 + 2 * t4 + (q & 1)] = acc[i][j][q];
     consumer_sync();
     if (Cfg::KW > 1) {  // this CTA's sums, into the first warp's place
       for (int p = tid; p < ROWS * BJ; p += CONSUMERS) {
@@ -498,7 +506,8 @@ struct AdapterGradCfg {
   static constexpr int STAGE = Z + P;
   static constexpr int LD = AG_COLS + 2;                 // fp32 partial sums [RJ][LD]
   static constexpr int RED = RJ * LD * 4;
-  static constexpr int DEEP = 160 * 1024 / STAGE < RING_MAX ? 160 * 1024 / STAGE : RING_MAX, SHALLOW = 80 * 1024 / STAGE < 2 ? 2 : DEEP / 2;
+  static constexpr int DEEP = 160 * 1024 / STAGE < RING_MAX ? 160 * 1024 / STAGE : RING_MAX;
+  static constexpr int SHALLOW = DEEP / 2 < 2 ? 2 : DEEP / 2;
   static constexpr int smem(int stages) { return 1024 + stages * STAGE + RED + int(sizeof(Ring)); }
 };
 
@@ -506,7 +515,7 @@ struct AdapterGradCfg {
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
 // with p = du, z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
 // memory, read transposed (ldmatrix.trans): M = columns (16 per warp), N =
-// ranks, K = rows (two warps share a chunk's rows). The rows behind a
+// ranks, K = rows (two warps share a chunk's). The rows behind a
 // segment's end are cleared in the fragments. The segments are taken in order
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
 template <int RJ, int AG_ROWS>
@@ -520,6 +529,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   float *red = reinterpret_cast<float *>(sm + a.stages * Cfg::STAGE);
   Ring &ring = *reinterpret_cast<Ring *>(sm + a.stages * Cfg::STAGE + Cfg::RED);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring0 = tma::smem_u32(sm);
   ring_init(ring, a.stages);
   pdl_trigger();
   pdl_wait();
@@ -566,6 +576,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
     return;
   }
   const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;
+  const int lo = lane & 7, m8 = (lane >> 3) & 1, hi = lane >> 4;
   for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
     float acc[RJ / 8][4];
 #pragma unroll
@@ -577,31 +588,35 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
       if (!ok) break;
       const int rows = ring.rows[slot];
-      const uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+      const uint32_t z = ring0 + slot * Cfg::STAGE, p = z + Cfg::Z;
       more = rows > 0;
       any |= more;
+      auto products = [&](auto cut) {  // cut: the stage ends inside this warp's rows
 #pragma unroll
-      for (int i = 0; i < AG_ROWS / 32; ++i) {
-        const int kk = kg * (AG_ROWS / 32) + i;
-        if (kk * 16 >= rows) break;
-        uint32_t af[4];
-        ldsm4<true>(af, sw128(z, kk * 16 + (lane & 7) + (lane >> 4) * 8, cg * 2 + ((lane >> 3) & 1)));
-        uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
-        if (rows < kk * 16 + 16) {
-          const int left = rows - kk * 16 - 2 * t4;
-          m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-          m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
-          af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1;
-        }
+        for (int i = 0; i < AG_ROWS / 32; ++i) {
+          const int kk = kg * (AG_ROWS / 32) + i;
+          uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // this lane's reduction rows 2t, 2t+1 and 2t+8, 2t+9
+          if (cut) {
+            const int left = rows - kk * 16 - 2 * t4;
+            if (left + 2 * t4 <= 0) break;
+            m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+            m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
+          }
+          uint32_t af[4];
+          ldsm4<true>(af, sw128(z, kk * 16 + lo + hi * 8, cg * 2 + m8));
+          if (cut) { af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1; }
 #pragma unroll
-        for (int jp = 0; jp < RJ / 16; ++jp) {
-          uint32_t bf[4];
-          ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8,
-                                (jp & 3) * 2 + (lane >> 4)));
-          mma_16816(acc[2 * jp], af, bf[0] & m0, bf[1] & m1);
-          mma_16816(acc[2 * jp + 1], af, bf[2] & m0, bf[3] & m1);
+          for (int jp = 0; jp < RJ / 16; ++jp) {
+            uint32_t bf[4];
+            ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + lo + m8 * 8, (jp & 3) * 2 + hi));
+            if (cut) { bf[0] &= m0; bf[1] &= m1; bf[2] &= m0; bf[3] &= m1; }
+            mma_16816(acc[2 * jp], af, bf[0], bf[1]);
+            mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
+          }
         }
-      }
+      };
+      if (rows >= (kg + 1) * (AG_ROWS / 2)) products(std::false_type{});
+      else if (rows > kg * (AG_ROWS / 2)) products(std::true_type{});
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
       if (++slot == a.stages) { slot = 0; ++round; }
@@ -762,13 +777,14 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   for (int i = 0; i < 4; ++i)
     ok &= map_bf16(m[i], r[i]->p, 2, {r[i]->width, a.T, 1, 1}, {r[i]->ld, 0, 0}, {64, AG_ROWS, 1, 1});
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
-  // One CTA per SM: a deep ring; more: shallow rings, so that several CTAs share
-  // an SM, each going through every grid.y-th adapter (about four CTAs an SM).
+  // Up to four CTAs per SM, each going through every grid.y-th adapter: an
+  // adapter's end (sums joined and stored) hides behind the other CTAs. A grid
+  // of less than one CTA per SM gets deep rings instead.
   const int slabs = a.slabs_a + (a.N + AG_COLS - 1) / AG_COLS;
   int ny = (4 * sm_count() + slabs - 1) / slabs;
-  if (ny > a.n_adapters) ny = a.n_adapters;
+  ny = ny > a.n_adapters ? a.n_adapters : ny;
+  a.stages = slabs * ny <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
   const dim3 grid{unsigned(slabs), unsigned(ny)};
-  a.stages = int64_t(grid.x) * grid.y <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
   if (st != MOE_OK) return st;
   const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ, AG_ROWS>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
@@ -902,7 +918,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.scale = scale; v.out = u; v.ldo = rank; v.err = err;
     st = launch_gemm_gemv(v, S, s, "moe_lora_linear (adapters)");
   } else {
-    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, 0, u, err};
+    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, u, err};
     st = lora::launch_shrink<false>(h, {x, ldx, K}, lora_a, s, "moe_lora_linear (adapters)");
   }
   if (st != MOE_OK) return st;
@@ -955,7 +971,7 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
                     (st = lora::check_rows(who, "u", u, rank, rank)) != MOE_OK)))
     return st;
   int32_t *err = static_cast<int32_t *>(ws);
-  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, 0, du, err};
+  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, du, err};
   if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
   if (dx && T <= lora::PROJ_MAX_T) {
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, du, lora_a, dx, lddx, err};
