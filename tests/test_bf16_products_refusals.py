@@ -121,3 +121,21 @@ def test_names_are_public(N):
                  "moe_lora_linear_backward", "moe_grouped_gemm_workspace_size", "moe_lora_workspace_size"):
         assert getattr(moe, name) is getattr(N, name)
     assert (moe.MOE_GEMM_OUT_F32, moe.MOE_GEMM_ACCUMULATE, moe.MOE_DEVERR_OFFSETS) == (1, 2, 5)
+
+
+def test_host_tensors_are_refused(N):
+    """A tensor outside the current device is refused by the binding, before the
+    library sees its address."""
+    import torch
+    t = torch.zeros(64, 64, dtype=torch.bfloat16)
+    with pytest.raises(N.MoeError) as ei:
+        N.moe_grouped_gemm(t, 64, P, P, 64 * 32, 4, 2, 32, 64, 0, P, 32, P, BIG, 0)
+    assert ei.value.status == N.MOE_ERR_INVALID_ARG and "current device" in str(ei.value)
+    with pytest.raises(N.MoeError):
+        N.moe_lora_linear(P, 64, P, t, P, P, P, None, 4, 2, 3, 16, 32, 64, P, P, 32, P, BIG, 0)
+
+
+def test_too_many_tiles_are_refused(N):
+    # 2^30 rows by 2^24 columns: more tiles than the engine counts (refused before or for want of a GPU)
+    st = _fwd(N, R=1 << 30, E=1, n=1 << 24, ldy=1 << 24, ws_=(1 << 24) * 64)
+    assert st in (N.MOE_ERR_SHAPE, N.MOE_ERR_UNSUPPORTED)

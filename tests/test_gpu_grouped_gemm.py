@@ -305,3 +305,74 @@ def test_weights_of_a_bf16_bank(M):
     e = torch.repeat_interleave(torch.arange(E, device="cuda"), counts.long())
     mag = torch.einsum("ri,rhi->rh", h.double().abs(), down.double().abs()[e])
     assert ((y - ref).abs().double() <= (2.0 ** -7 + I * 2.0 ** -22) * mag).all()
+
+
+def test_training_step_of_a_moe_layer(M):
+    """The operators as a training step of one MoE layer uses them, behind a
+    projection with adapters: every stage against 64 bits on that stage's own
+    inputs, forward and backward."""
+    from tests.test_gpu_lora import Problem
+    E, H, I, k = 8, 256, 192, 2
+    p = Problem([70, 0, 41, 52], [1, 0, -1, 0], 2, 16, H, 264, seed=40)
+    p.strided()
+    T = p.T
+    lws = p.workspace(M)
+    p.forward(M, lws)                                               # x = projection(tokens), adapters per request
+    p.check_forward()
+    x = p.y
+    wr = _rand((E, H), 41, 0.1)
+    up, down = _rand((E, I, H), 42, 0.1), _rand((E, H, I), 43, 0.1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    logits = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    ids, tw = torch.empty(T, k, **i32), torch.empty(T, k, device="cuda")
+    M.moe_route_topk(x, wr, T, H, E, k, None, M.MOE_RENORM, logits, ids, tw)
+    P = T * k
+    counts, off, sp, pp = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(P, **i32), torch.empty(P, **i32)
+    gws = torch.zeros(M.moe_group_workspace_size(T, k, E), dtype=torch.uint8, device="cuda")
+    M.moe_group_tokens(ids, T, k, E, counts, off, sp, pp, gws, gws.numel())
+    tok = (sp // k).long()
+    xs = x[tok].contiguous()
+    ws = torch.zeros(M.moe_grouped_gemm_workspace_size(P, E, I, H), dtype=torch.uint8, device="cuda")
+    f = M.MOE_GEMM_OUT_F32
+    a = torch.empty(P, I, device="cuda")
+    M.moe_grouped_gemm(xs, H, off, up, I * H, P, E, I, H, f, a, I, ws, ws.numel())
+    h = torch.relu(a).to(torch.bfloat16)
+    y = torch.empty(P, H, device="cuda")
+    M.moe_grouped_gemm(h, I, off, down, H * I, P, E, H, I, f, y, H, ws, ws.numel())
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    M.moe_combine(y, tw, pp, x, T, k, H, out)
+
+    dout = _rand((T, H), 44)
+    dys = (dout.float()[tok] * tw.flatten()[sp.long()][:, None]).to(torch.bfloat16)
+    d_down, d_up = torch.empty(E, H, I, device="cuda"), torch.zeros(E, I, H, device="cuda")
+    dh, dxs = torch.empty(P, I, device="cuda"), torch.empty(P, H, device="cuda")
+    M.moe_grouped_gemm_wgrad(dys, H, h, I, off, P, E, H, I, f, d_down, H * I, ws, ws.numel())
+    M.moe_grouped_gemm_dgrad(dys, H, off, down, H * I, P, E, H, I, f, dh, I, ws, ws.numel())
+    da = (dh * (a > 0)).to(torch.bfloat16)
+    M.moe_grouped_gemm_wgrad(da, I, xs, H, off, P, E, I, H, f | M.MOE_GEMM_ACCUMULATE, d_up, I * H, ws, ws.numel())
+    M.moe_grouped_gemm_dgrad(da, I, off, up, I * H, P, E, I, H, f, dxs, H, ws, ws.numel())
+    ones = torch.ones(T, k, device="cuda")
+    p.dy = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")   # a token's experts summed, and the residual
+    M.moe_combine(dxs, ones, pp, dout, T, k, H, p.dy)
+    p.strided()
+    p.backward(M, lws)
+    torch.cuda.synchronize()
+    p.check_backward()
+    assert M.moe_read_device_error(ws) == 0 and M.moe_read_device_error(lws) == 0
+
+    o = off.tolist()
+    assert o[-1] == P
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        n = o[e + 1] - o[e]
+        for got, l, m, terms, what in ((a[r], xs[r], up[e].T, H, "a"), (y[r], h[r], down[e].T, I, "y"),
+                                       (dh[r], dys[r], down[e], H, "dh"), (dxs[r], da[r], up[e], I, "dxs"),
+                                       (d_down[e], dys[r].T, h[r], n, "d_down"), (d_up[e], da[r].T, xs[r], n + 1, "d_up")):
+            l, m = l.double(), m.double()
+            _check(got, l @ m, l.abs() @ m.abs(), terms, False, f"{what}[{e}]")
+    ref = x.double()
+    mag = ref.abs()
+    for j in range(k):
+        v = y.double()[pp.view(T, k)[:, j].long()] * tw.double()[:, j:j + 1]
+        ref, mag = ref + v, mag + v.abs()
+    _check(out, ref, mag, k + 1, True, "out")

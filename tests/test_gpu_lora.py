@@ -161,7 +161,12 @@ CASES = [
     ([1] * 7, [2, 0, -1, 2, 1, 1, 0], 3, 16, 136, 200, 2),        # a decode batch, padded
     ([1] * 32, list(range(16)) * 2, 16, 24, 264, 328, 0),
     ([1] * 33, [i % 5 - 1 for i in range(33)], 4, 64, 512, 256, 0),
-    ([1] * 130, [i % 9 - 1 for i in range(130)], 9, 16, 520, 136, 3),
+    ([1] * 127, [i % 9 - 1 for i in range(127)], 9, 16, 520, 136, 3),
+    ([1] * 130, [i % 9 - 1 for i in range(130)], 9, 128, 520, 136, 3),
+    ([60, 7, 61], [2, 0, 1], 3, 48, 2056, 1032, 0),               # the decode form's largest batch, split reductions
+    ([5] * 3, [1, -1, 1], 2, 8, 2048, 2048, 0),
+    ([2500, 1700], [0, 1], 2, 16, 136, 264, 0),                   # the wide tile of the inner products
+    ([3000, 1300, 8], [1, 2, 0], 3, 128, 264, 136, 0),
     ([40, 0, 3, 90, 1], [1, 0, 1, -1, 0], 2, 16, 256, 192, 0),
     ([300, 0, 45, 0, 171], [0, 3, 2, 1, 0], 5, 32, 384, 520, 9),  # adapters without rows, one with two segments
     ([64, 64, 128, 256], [0, 1, 2, 3], 4, 128, 264, 136, 0),
@@ -196,7 +201,7 @@ def test_strides(M, lens):
     p.check_backward()
 
 
-@pytest.mark.parametrize("lens", [[1] * 6, [70, 33, 61]])
+@pytest.mark.parametrize("lens", [[1] * 6, [20, 9, 40], [70, 33, 61]])
 def test_other_segments_values_do_not_enter(M, lens):
     """An infinity in one request's row stays out of the other requests' rows
     and gradients, though they share tiles."""
@@ -218,8 +223,11 @@ def test_other_segments_values_do_not_enter(M, lens):
         assert torch.isfinite(b).all() and torch.equal(a, b)
 
 
-def test_adapters_that_hold_nan_are_not_read_for_other_rows(M):
-    p = Problem([40, 60, 30], [0, 1, -1], 2, 16, 136, 72, seed=9)
+@pytest.mark.parametrize("scale", [1, 2, 10])
+def test_adapters_that_hold_nan_are_not_read_for_other_rows(M, scale):
+    # the decode and the batch form, with shared 16-row blocks
+    lens = [4 * scale, 6 * scale, 3 * scale]
+    p = Problem(lens, [0, 1, -1], 2, 16, 136, 72, seed=9)
     p.strided()
     ws = p.workspace(M)
     p.forward(M, ws)
@@ -228,12 +236,12 @@ def test_adapters_that_hold_nan_are_not_read_for_other_rows(M):
     p.a[1], p.b[1] = NAN, NAN
     p.forward(M, ws)
     p.backward(M, ws)
-    for lo, hi in ((0, 40), (100, 130)):
+    for lo, hi in ((0, p.off[1]), (p.off[2], p.off[3])):
         assert torch.equal(p.y[lo:hi], y[lo:hi]) and torch.equal(p.dx[lo:hi], dx[lo:hi])
     assert torch.equal(p.da[0], da[0])
 
 
-@pytest.mark.parametrize("T", [20, 200])
+@pytest.mark.parametrize("T", [6, 20, 200])
 def test_bad_segments_are_cut_and_flagged(M, T):
     p = Problem([T // 2, T // 2], [0, 1], 2, 16, 72, 64, seed=5)
     p.strided()

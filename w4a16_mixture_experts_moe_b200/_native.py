@@ -109,15 +109,40 @@ def _ptr(x):
     return x.data_ptr()
 
 
+def _dev(x, cur):
+    """_ptr of an argument that a kernel dereferences: a tensor has to live on the current device `cur` (an address
+    that this device cannot reach would fault it)."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.get_device() != cur:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"tensor on {x.device}, but the current device is cuda:{cur}")
+    return x.data_ptr()
+
+
+_torch = None
+
+
+def _current_device() -> int:
+    """torch's current CUDA device (-2 without one). Asked of torch's C layer:
+    the public call costs half a microsecond more on every launch."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    try:
+        return _torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
 def _addr(arr):
     return C.cast(arr, C.c_void_p).value
 
 
 def _stream(s):
-    if s is None:
-        import torch
-        # the raw handle of torch's current stream, without the Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if s is None:  # the raw handle of torch's current stream, without the Stream object around it
+        d = _current_device()
+        return _torch._C._cuda_getCurrentRawStream(d)
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -211,18 +236,21 @@ def moe_grouped_gemm_workspace_size(R, E, N, K) -> int:
 
 
 def moe_grouped_gemm(x, ldx, offsets, w, w_stride, R, E, N, K, flags, y, ldy, ws, ws_bytes, stream=None):
-    _check(lib.moe_grouped_gemm(_ptr(x), ldx, _ptr(offsets), _ptr(w), w_stride, R, E, N, K, flags, _ptr(y), ldy,
-                                _ptr(ws), ws_bytes, _stream(stream)))
+    d = _current_device()
+    _check(lib.moe_grouped_gemm(_dev(x, d), ldx, _dev(offsets, d), _dev(w, d), w_stride, R, E, N, K, flags, _dev(y, d),
+                                ldy, _dev(ws, d), ws_bytes, _stream(stream)))
 
 
 def moe_grouped_gemm_dgrad(dy, lddy, offsets, w, w_stride, R, E, N, K, flags, dx, lddx, ws, ws_bytes, stream=None):
-    _check(lib.moe_grouped_gemm_dgrad(_ptr(dy), lddy, _ptr(offsets), _ptr(w), w_stride, R, E, N, K, flags, _ptr(dx),
-                                      lddx, _ptr(ws), ws_bytes, _stream(stream)))
+    d = _current_device()
+    _check(lib.moe_grouped_gemm_dgrad(_dev(dy, d), lddy, _dev(offsets, d), _dev(w, d), w_stride, R, E, N, K, flags,
+                                      _dev(dx, d), lddx, _dev(ws, d), ws_bytes, _stream(stream)))
 
 
 def moe_grouped_gemm_wgrad(dy, lddy, x, ldx, offsets, R, E, N, K, flags, dw, dw_stride, ws, ws_bytes, stream=None):
-    _check(lib.moe_grouped_gemm_wgrad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(offsets), R, E, N, K, flags, _ptr(dw),
-                                      dw_stride, _ptr(ws), ws_bytes, _stream(stream)))
+    d = _current_device()
+    _check(lib.moe_grouped_gemm_wgrad(_dev(dy, d), lddy, _dev(x, d), ldx, _dev(offsets, d), R, E, N, K, flags,
+                                      _dev(dw, d), dw_stride, _dev(ws, d), ws_bytes, _stream(stream)))
 
 
 def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
@@ -231,17 +259,19 @@ def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
 
 def moe_lora_linear(x, ldx, w, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters, rank, N, K, u, y, ldy,
                     ws, ws_bytes, stream=None):
-    _check(lib.moe_lora_linear(_ptr(x), ldx, _ptr(w), _ptr(seg_offsets), _ptr(seg_adapter), _ptr(lora_a), _ptr(lora_b),
-                               _ptr(scale), T, S, n_adapters, rank, N, K, _ptr(u), _ptr(y), ldy, _ptr(ws), ws_bytes,
-                               _stream(stream)))
+    d = _current_device()
+    _check(lib.moe_lora_linear(_dev(x, d), ldx, _dev(w, d), _dev(seg_offsets, d), _dev(seg_adapter, d), _dev(lora_a, d),
+                               _dev(lora_b, d), _dev(scale, d), T, S, n_adapters, rank, N, K, _dev(u, d), _dev(y, d),
+                               ldy, _dev(ws, d), ws_bytes, _stream(stream)))
 
 
 def moe_lora_linear_backward(dy, lddy, x, ldx, w, u, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters,
                              rank, N, K, du, dx, lddx, d_lora_a, d_lora_b, ws, ws_bytes, stream=None):
-    _check(lib.moe_lora_linear_backward(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(u), _ptr(seg_offsets),
-                                        _ptr(seg_adapter), _ptr(lora_a), _ptr(lora_b), _ptr(scale), T, S, n_adapters,
-                                        rank, N, K, _ptr(du), _ptr(dx), lddx, _ptr(d_lora_a), _ptr(d_lora_b), _ptr(ws),
-                                        ws_bytes, _stream(stream)))
+    d = _current_device()
+    _check(lib.moe_lora_linear_backward(_dev(dy, d), lddy, _dev(x, d), ldx, _dev(w, d), _dev(u, d), _dev(seg_offsets, d),
+                                        _dev(seg_adapter, d), _dev(lora_a, d), _dev(lora_b, d), _dev(scale, d), T, S,
+                                        n_adapters, rank, N, K, _dev(du, d), _dev(dx, d), lddx, _dev(d_lora_a, d),
+                                        _dev(d_lora_b, d), _dev(ws, d), ws_bytes, _stream(stream)))
 
 
 def moe_debug_stall_next_tc_ffn(calls: int):

@@ -143,7 +143,9 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
   }
   // with adapters: one group, the rows up to the end of the last segment
   const int o0 = late ? 0 : a.offsets[e], o1 = late ? a.seg_offsets[a.segs] : a.offsets[e + 1];
-  if ((o0 < 0 || o1 < o0 || o1 > a.R) && blockIdx.x == 0 && tid == 0) flag_error(a.err, MOE_DEVERR_OFFSETS);
+  // (segments start at row 0, groups anywhere)
+  if ((o0 < 0 || o1 < o0 || o1 > a.R || (a.index && e == 0 && o0 != 0)) && blockIdx.x == 0 && tid == 0)
+    flag_error(a.err, MOE_DEVERR_OFFSETS);
   const int lo = min(max(o0, 0), a.R), cnt = min(o1, a.R) - lo;
   if (cnt <= 0) return;
   const int wi = a.index ? a.index[e] : e;

@@ -641,7 +641,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
         store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, v);
       };
-      if (a.out_f32)
+      if (zero && a.accumulate) {
+        // nothing to add
+      } else if (a.out_f32)
         for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
       else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
         const int rows = min(OUT_ROWS, tl.nvalid - j0);
@@ -859,6 +861,11 @@ int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op,
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (major != 10) return set_error(MOE_ERR_UNSUPPORTED, "%s: needs sm_100", what);
   if (!tensor_map_encoder()) return set_error(MOE_ERR_UNSUPPORTED, "%s: cuTensorMapEncodeTiled is not available", what);
+  // the tile list is counted in 32 bits
+  const int64_t cols = (int64_t(a.M) + 255) / 256;
+  const int64_t rows = mode == GEMM_WGRAD ? int64_t(a.groups) * ((int64_t(a.NC) + 255) / 256) : int64_t(a.R) / a.bn + a.groups;
+  if (cols * rows > (int64_t(1) << 30))
+    return set_error(MOE_ERR_SHAPE, "%s: too many tiles (%lld)", what, (long long)(cols * rows));
   return mode == GEMM_FWD     ? launch_mode<GEMM_FWD>(a, op, s, what)
          : mode == GEMM_DGRAD ? launch_mode<GEMM_DGRAD>(a, op, s, what)
                               : launch_mode<GEMM_WGRAD>(a, op, s, what);
