@@ -167,6 +167,10 @@ CASES = [
     ([5] * 3, [1, -1, 1], 2, 8, 2048, 2048, 0),
     ([2500, 1700], [0, 1], 2, 16, 136, 264, 0),                   # the wide tile of the inner products
     ([3000, 1300, 8], [1, 2, 0], 3, 128, 264, 136, 0),
+    # more tiles than the decode form takes: the tensor-core engine, with blocks that segments share
+    ([300, 0, 133, 5, 2, 467], [0, 3, 2, 1, -1, 0], 5, 32, 1032, 1160, 9),
+    ([1] * 660, [i % 7 - 1 for i in range(660)], 6, 24, 1032, 1040, 3),
+    ([777, 1, 230], [1, -1, 0], 2, 128, 1096, 1032, 0),
     ([40, 0, 3, 90, 1], [1, 0, 1, -1, 0], 2, 16, 256, 192, 0),
     ([300, 0, 45, 0, 171], [0, 3, 2, 1, 0], 5, 32, 384, 520, 9),  # adapters without rows, one with two segments
     ([64, 64, 128, 256], [0, 1, 2, 3], 4, 128, 264, 136, 0),
@@ -189,9 +193,9 @@ def test_forward_and_backward(M, case):
     p.check_backward()
 
 
-@pytest.mark.parametrize("lens", [[1, 2, 1, 4], [50, 3, 80]])
-def test_strides(M, lens):
-    p = Problem(lens, [1, -1, 0, 1][:len(lens)], 2, 16, 136, 264, tail=4, pad=16, seed=3)
+@pytest.mark.parametrize("lens,N,K", [([1, 2, 1, 4], 136, 264), ([50, 3, 80], 136, 264), ([411, 3, 290], 1032, 1064)])
+def test_strides(M, lens, N, K):
+    p = Problem(lens, [1, -1, 0, 1][:len(lens)], 2, 16, N, K, tail=4, pad=16, seed=3)
     p.strided()
     ws = p.workspace(M)
     p.forward(M, ws)
@@ -201,12 +205,13 @@ def test_strides(M, lens):
     p.check_backward()
 
 
-@pytest.mark.parametrize("lens", [[1] * 6, [20, 9, 40], [70, 33, 61]])
-def test_other_segments_values_do_not_enter(M, lens):
+@pytest.mark.parametrize("lens,N,K", [([1] * 6, 264, 136), ([20, 9, 40], 264, 136), ([70, 33, 61], 264, 136),
+                                      ([370, 33, 261], 1032, 1064)])
+def test_other_segments_values_do_not_enter(M, lens, N, K):
     """An infinity in one request's row stays out of the other requests' rows
     and gradients, though they share tiles."""
     def run(dirty):
-        p = Problem(lens, [i % 3 for i in range(len(lens))], 3, 16, 264, 136, seed=7)
+        p = Problem(lens, [i % 3 for i in range(len(lens))], 3, 16, N, K, seed=7)
         lo, hi = p.off[1], p.off[2]
         p.x[lo:hi, ::3] = float("inf") if dirty else 0
         p.dy[lo:hi, ::5] = NAN if dirty else 0
@@ -223,11 +228,11 @@ def test_other_segments_values_do_not_enter(M, lens):
         assert torch.isfinite(b).all() and torch.equal(a, b)
 
 
-@pytest.mark.parametrize("scale", [1, 2, 10])
-def test_adapters_that_hold_nan_are_not_read_for_other_rows(M, scale):
-    # the decode and the batch form, with shared 16-row blocks
+@pytest.mark.parametrize("scale,N,K", [(1, 136, 72), (2, 136, 72), (10, 136, 72), (51, 1032, 1064)])
+def test_adapters_that_hold_nan_are_not_read_for_other_rows(M, scale, N, K):
+    # every form of the projection; the engine's with shared 16-row blocks
     lens = [4 * scale, 6 * scale, 3 * scale]
-    p = Problem(lens, [0, 1, -1], 2, 16, 136, 72, seed=9)
+    p = Problem(lens, [0, 1, -1], 2, 16, N, K, seed=9)
     p.strided()
     ws = p.workspace(M)
     p.forward(M, ws)
@@ -241,9 +246,9 @@ def test_adapters_that_hold_nan_are_not_read_for_other_rows(M, scale):
     assert torch.equal(p.da[0], da[0])
 
 
-@pytest.mark.parametrize("T", [6, 20, 200])
-def test_bad_segments_are_cut_and_flagged(M, T):
-    p = Problem([T // 2, T // 2], [0, 1], 2, 16, 72, 64, seed=5)
+@pytest.mark.parametrize("T,N,K", [(6, 72, 64), (20, 72, 64), (200, 72, 64), (700, 1032, 1040)])
+def test_bad_segments_are_cut_and_flagged(M, T, N, K):
+    p = Problem([T // 2, T // 2], [0, 1], 2, 16, N, K, seed=5)
     p.strided()
     ws = p.workspace(M)
     good = p.seg_off.clone()
@@ -325,9 +330,9 @@ def test_gradients_against_differences(M):
         assert abs((got.double() * v).sum() - num) <= bound
 
 
-@pytest.mark.parametrize("lens", [[1] * 9, [100, 31, 70]])
-def test_captured_replayed_and_equal_bits(M, lens):
-    p = Problem(lens, [i % 3 - 1 for i in range(len(lens))], 2, 16, 264, 200, seed=12)
+@pytest.mark.parametrize("lens,N,K", [([1] * 9, 264, 200), ([100, 31, 70], 264, 200), ([401, 31, 270], 1032, 1040)])
+def test_captured_replayed_and_equal_bits(M, lens, N, K):
+    p = Problem(lens, [i % 3 - 1 for i in range(len(lens))], 2, 16, N, K, seed=12)
     p.strided()
     ws = p.workspace(M)
     s = torch.cuda.Stream()

@@ -715,6 +715,8 @@ static int launch_shrink(const ShrinkArgs &a, const Rows &z, const uint16_t *p, 
                         : launch_shrink_as<64, TRANS, 64>(a, z, p, s, what);
 }
 
+static int proj_parts(int tiles, int nc);
+
 template <bool TRANS, int ROWS>
 static int launch_proj_as(const ProjArgs &a, const Rows &z, const uint16_t *w, cudaStream_t s, const char *what) {
   using Cfg = ProjCfg<TRANS, ROWS>;
@@ -729,9 +731,7 @@ static int launch_proj_as(const ProjArgs &a, const Rows &z, const uint16_t *w, c
   const int st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
   const int tiles = (a.M + Cfg::BJ - 1) / Cfg::BJ, row_tiles = (a.T + ROWS - 1) / ROWS;
-  const int nc = (a.C + Cfg::CC - 1) / Cfg::CC;
-  int parts = 1;  // until the CTAs cover the SMs, each with two stages of work at least
-  while (parts < 8 && tiles * row_tiles * parts * 2 <= sm_count() && nc >= parts * 4) parts *= 2;
+  const int parts = proj_parts(tiles * row_tiles, (a.C + Cfg::CC - 1) / Cfg::CC);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles * parts), unsigned(row_tiles));
   cfg.blockDim = dim3(CONSUMERS + 32);
@@ -837,12 +837,30 @@ static int check_rows(const char *who, const char *name, const void *p, int64_t 
   return MOE_OK;
 }
 
-// Up to this many rows the projection is a weight stream (proj_kernel: N = 4096,
-// K = 2048, four requests of rank 16: 18 us at 128 rows and 35 us at 192,
-// where the tensor-core engine takes 22 us at both); the forward pass of the
-// fewest rows runs in gemm_gemv.cu, with one launch's prologue less to wait for.
-constexpr int PROJ_MAX_T = 128;
+// The forward pass of the fewest rows runs in gemm_gemv.cu.
 constexpr int GEMV_MAX_T = 8;
+
+// CTAs of proj_kernel that split one tile's reduction (a cluster): doubled until
+// the CTAs cover the SMs, each with two stages of work at least.
+static int proj_parts(int tiles, int nc) {
+  int parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= sm_count() && nc >= parts * 4) parts *= 2;
+  return parts;
+}
+
+// Whether M columns of T rows, reduced over C, run as a weight stream
+// (proj_kernel) rather than on the tensor-core engine. Its 64 x 64 tiles have to
+// fit the SMs at once (K = N = 1024, four requests of rank 16: T = 512 14 us
+// against the engine's 15, T = 768, two rounds, 25 against 16) and a CTA's share
+// of the reduction has to be short: 128 columns cost it 0.9 us and the engine
+// 0.55, but the engine starts 7 us behind (N = 2048, T = 192: K = 2048 16 us
+// against 20, K = 4096 42 against 31).
+static bool use_proj(int T, int M, int C) {
+  if (T <= 32) return true;  // a tile is one or two rows of MMAs: bound by W's bytes
+  const int64_t tiles = int64_t((T + 63) / 64) * ((M + 63) / 64);
+  const int nc = (C + 127) / 128;
+  return tiles <= sm_count() && nc <= 18 * proj_parts(int(tiles), nc);
+}
 
 static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const int32_t *seg_adapter, int T, int S,
                              int n_adapters, int rank, int N, int K, void *out, int64_t ldo, int32_t *err) {
@@ -930,7 +948,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.u = u; v.lora_b = lora_b;
     return launch_gemm_gemv(v, 1, s, who);
   }
-  if (T <= lora::PROJ_MAX_T) {
+  if (lora::use_proj(T, N, K)) {
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, K, N, rank, u, lora_b, y, ldy, err};
     return lora::launch_proj<false>(v, {x, ldx, K}, w, s, who);
   }
@@ -973,7 +991,7 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
   int32_t *err = static_cast<int32_t *>(ws);
   const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, du, err};
   if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
-  if (dx && T <= lora::PROJ_MAX_T) {
+  if (dx && lora::use_proj(T, K, N)) {
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, du, lora_a, dx, lddx, err};
     if ((st = lora::launch_proj<true>(v, {dy, lddy, N}, w, s, who)) != MOE_OK) return st;
   } else if (dx) {
