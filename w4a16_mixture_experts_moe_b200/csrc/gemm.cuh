@@ -28,6 +28,7 @@ struct TcGemmArgs {
   // the launch before (lora.cu); row of block b: 16 b, or 16 owner if delta_by_seg
   const float *delta;
   int delta_by_seg;
+  int late;  // the launches before this one wait for everything but u / du, delta and the output
   int32_t *err;
 };
 

@@ -476,7 +476,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       next();
     }
     if constexpr (MODE != GEMM_WGRAD) {
-      if (more && a.delta) pdl_wait();  // returns at once when the launches before are done
+      if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
       while (known && more && ok) {
         const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
         const int er0 = tl.row + col + int(rank) * whalf;  // this CTA's half of the segment's rows
@@ -554,10 +554,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   pdl_trigger();
-  // Only the epilogue needs the launch before this one when that launch
-  // computes the shared blocks: it waits for what this kernel otherwise reads
-  // before it lets this kernel start.
-  if (MODE == GEMM_WGRAD || !a.delta) pdl_wait();
+  // With adapters (`late`) only their k-steps and the epilogue need the launches
+  // before this one; those wait, before they let this kernel start, for all that
+  // it reads until then.
+  if (MODE == GEMM_WGRAD || !a.late) pdl_wait();
   if (warp == 0) {
     int v[8], local = 0;
     bool bad = false;
@@ -613,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3, part = warp >> 2;
     const bool issuer = q == 0 && lane == 0;
     const uint32_t out_buf = smem_u32(smem + STAGES * STAGE_BYTES + part * OUT_BYTES);
-    if (MODE != GEMM_WGRAD && a.delta) pdl_wait();
+    if (MODE != GEMM_WGRAD && a.late) pdl_wait();
     for (int i = 0;; ++i) {
       const int t = sched_pos(i);
       if (t >= total) break;

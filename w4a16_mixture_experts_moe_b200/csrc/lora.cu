@@ -4,12 +4,13 @@
 //   dA_a  = sum_t du[t]^T x[t]     dB_a  = sum_t dy[t]^T u[t]
 // for row t of a segment with adapter a. This file holds the entry points and
 // the products of small rank (u, du; dA, dB); the projection with the adapters
-// folded into its sums is gemm_tc.cu's (batches) or gemm_gemv.cu's (decode).
+// folded into its sums is gemm_tc.cu's (batches), proj_kernel's below (decode) or
+// gemm_gemv.cu's (a few rows).
 //
 // u and du are rounded to BF16 once: they are operands of the BF16 matrix
 // instructions that follow, and the adapter's part is a small share of y, so
-// the rounding (2^-9 relative, independent from value to value) stays below
-// y's own.
+// the rounding (at most 2^-8 relative, independent from value to value) stays
+// below y's own.
 //
 // The small-rank products read each row of x (dy) once and do 2 rank
 // operations per value: at rank 64 that is 64 operations a byte, far below the
@@ -531,8 +532,8 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring0 = tma::smem_u32(sm);
   ring_init(ring, a.stages);
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // behind the wait, as in shrink_kernel
   const bool is_a = int(blockIdx.x) < a.slabs_a;
   const int c0 = (is_a ? blockIdx.x : blockIdx.x - a.slabs_a) * AG_COLS, C = is_a ? a.K : a.N;
   int slot = 0, round = 0;
@@ -887,6 +888,7 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
   g.bn = bn;
   g.out = out;
   g.ldo = ldo;
+  g.late = 1;
   g.err = err;
   return g;
 }
@@ -991,23 +993,31 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
   int32_t *err = static_cast<int32_t *>(ws);
   const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, du, err};
   if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
-  if (dx && lora::use_proj(T, K, N)) {
-    const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, du, lora_a, dx, lddx, err};
-    if ((st = lora::launch_proj<true>(v, {dy, lddy, N}, w, s, who)) != MOE_OK) return st;
-  } else if (dx) {
-    TcGemmArgs g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
+  const bool engine = dx && !lora::use_proj(T, K, N);
+  TcGemmArgs g = {};
+  if (engine) {
+    g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
     g.ext_a = lora_a;
     g.ext_b = du;
     if ((st = lora::shared_blocks<true>(g, T, S, ws, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
-    const TcGemmOperands op = {w, dy, K, int64_t(N) * K, lddy};
-    if ((st = launch_gemm_tc(GEMM_DGRAD, g, op, s, who)) != MOE_OK) return st;
   }
-  if (!d_lora_a) return MOE_OK;
-  const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, (K + lora::AG_COLS - 1) / lora::AG_COLS,
-                                   0, d_lora_a, d_lora_b, err};
-  const char *what = "moe_lora_linear_backward (adapters)";
-  const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
-  // loads of 128 rows, or of 32 where segments are short on average
-  return T >= 64 * S ? lora::launch_adapter_grad<128>(q, rx, rdy, ru, rdu, s, what)
-                     : lora::launch_adapter_grad<32>(q, rx, rdy, ru, rdu, s, what);
+  // The engine goes behind the adapters' gradients: it starts while they end and
+  // waits for them only in its epilogue (six adapters of rank 16 at T = 2041, one
+  // segment: 38.5 -> 35.1 us). The decode form overlaps du instead (T = 200, K = N
+  // = 1024: 14.1 us, behind the gradients 16.2).
+  if (dx && !engine) {
+    const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, du, lora_a, dx, lddx, err};
+    if ((st = lora::launch_proj<true>(v, {dy, lddy, N}, w, s, who)) != MOE_OK) return st;
+  }
+  if (d_lora_a) {
+    const int slabs_a = (K + lora::AG_COLS - 1) / lora::AG_COLS;
+    const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, slabs_a, 0, d_lora_a, d_lora_b, err};
+    const char *what = "moe_lora_linear_backward (adapters)";
+    const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
+    // loads of 128 rows, or of 32 where segments are short on average
+    st = T >= 64 * int64_t(S) ? lora::launch_adapter_grad<128>(q, rx, rdy, ru, rdu, s, what)
+                              : lora::launch_adapter_grad<32>(q, rx, rdy, ru, rdu, s, what);
+    if (st != MOE_OK) return st;
+  }
+  return engine ? launch_gemm_tc(GEMM_DGRAD, g, TcGemmOperands{w, dy, K, int64_t(N) * K, lddy}, s, who) : MOE_OK;
 }
