@@ -256,16 +256,17 @@ struct DeltaArgs {
 
 // The adapters' part of the 16-row blocks that several segments share, as fp32
 // rows for the projection's epilogue: delta[j][f] = u[row j] . w_a[f], row j's
-// own adapter a. A CTA does 128 columns of four rows of a block (a row's loads
-// wait on nothing but its adapter's index, but follow the row before): blocks
-// by their owning segment, or all blocks where segments are many. A thread
-// keeps its column of the adapter in registers while rows share it.
-constexpr int DELTA_ROWS = 4;
-
-template <bool COLS>
+// own adapter a. Few segments: a CTA does 128 columns of one block, found by
+// its owning segment; a thread loads its column of the adapter once for the rows
+// that share it, and all CTAs run at once (13 segments, rank 64, N = 4096: one
+// wave instead of two and a half with four rows a CTA). Many segments: all
+// blocks, four rows a CTA, since each row waits for another adapter's loads.
+// A pass takes CH ranks: the thread's column of the adapter in CH registers, a
+// running sum per row.
+template <bool COLS, int CH>
 __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
-  __shared__ __align__(16) uint16_t us[DELTA_ROWS][MAX_RANK];
-  __shared__ int ads[DELTA_ROWS];
+  __shared__ __align__(16) float us[16][MAX_RANK];
+  __shared__ int ads[16];
   pdl_wait();
   pdl_trigger();  // behind the wait, as in shrink_kernel
   const int end = min(a.seg_offsets[a.segs], a.T), tid = threadIdx.x;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
                           first_segment(a.seg_offsets, a.segs, min(row + 15, end - 1)))
       return;
   }
-  const int j0 = blockIdx.z * DELTA_ROWS, n = min(DELTA_ROWS, end - row - j0);  // this CTA's rows: row + j0 ...
+  const int per = 16 / gridDim.z, j0 = blockIdx.z * per, n = min(per, end - row - j0);  // this CTA's rows: row + j0 ...
   if (n <= 0) return;
   float *out = a.delta + (a.by_seg ? int64_t(blockIdx.y) * 16 : int64_t(row)) * a.M + int64_t(j0) * a.M;
   row += j0;
@@ -290,45 +291,60 @@ __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
     if (ad >= a.n_adapters) ad = -1;
     ads[tid] = ad;
   }
-  const int pieces = a.rank / 8;
-  for (int p = tid; p < n * pieces; p += 128)
-    *reinterpret_cast<uint4 *>(&us[p / pieces][p % pieces * 8]) =
-        *reinterpret_cast<const uint4 *>(a.u + int64_t(row + p / pieces) * a.rank + p % pieces * 8);
+  const int width = (a.rank + CH - 1) / CH * CH;  // whole passes, zeros behind the rank
+  for (int p = tid; p < n * width; p += 128) {
+    const int j = p / width, i = p % width;
+    us[j][i] = i < a.rank ? bf16_to_f(a.u[int64_t(row + j) * a.rank + i]) : 0.f;
+  }
   __syncthreads();
   const int f = blockIdx.x * 128 + tid;
   if (f >= a.M) return;
-  out += f;
-  uint4 w[MAX_RANK / 8];
-  int prev = -1;
-  for (int j = 0; j < n; ++j) {
-    const int ad = ads[j];
-    float d = 0.f;
-    if (ad >= 0) {
+  float acc[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+  for (int i0 = 0; i0 < a.rank; i0 += CH) {
+    float w[CH];
+    int prev = -1;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j >= n) break;
+      const int ad = ads[j];
+      if (ad < 0) continue;
       if (ad != prev) {
         prev = ad;
 #pragma unroll
-        for (int i = 0; i < MAX_RANK / 8; ++i) {
-          if (i * 8 >= a.rank) break;
-          if (COLS) {
-            const uint16_t *c = a.w + (int64_t(ad) * a.rank + i * 8) * a.M + f;
-            uint32_t q[4];
+        for (int i = 0; i < CH; i += 8) {
+          uint32_t q[4] = {0, 0, 0, 0};
+          if (i0 + i < a.rank) {
+            if (COLS) {
+              const uint16_t *c = a.w + (int64_t(ad) * a.rank + i0 + i) * a.M + f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = c[int64_t(2 * k) * a.M] | uint32_t(c[int64_t(2 * k + 1) * a.M]) << 16;
-            w[i] = make_uint4(q[0], q[1], q[2], q[3]);
-          } else {
-            w[i] = *(reinterpret_cast<const uint4 *>(a.w + (int64_t(ad) * a.M + f) * a.rank) + i);
+              for (int k = 0; k < 4; ++k) q[k] = c[int64_t(2 * k) * a.M] | uint32_t(c[int64_t(2 * k + 1) * a.M]) << 16;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4 *>(a.w + (int64_t(ad) * a.M + f) * a.rank + i0 + i);
+              q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[i + 2 * k] = bf16_lo(q[k]);
+            w[i + 2 * k + 1] = bf16_hi(q[k]);
           }
         }
       }
 #pragma unroll
-      for (int i = 0; i < MAX_RANK / 8; ++i) {
-        if (i * 8 >= a.rank) break;
-        const uint4 y = *reinterpret_cast<const uint4 *>(&us[j][i * 8]);
-        d = dot8(w[i], y, d);
+      for (int i = 0; i < CH; i += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(&us[j][i0 + i]);
+        acc[j] = fmaf(w[i], y.x, acc[j]);
+        acc[j] = fmaf(w[i + 1], y.y, acc[j]);
+        acc[j] = fmaf(w[i + 2], y.z, acc[j]);
+        acc[j] = fmaf(w[i + 3], y.w, acc[j]);
       }
     }
-    out[int64_t(j) * a.M] = d;
   }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < n) out[int64_t(j) * a.M + f] = acc[j];
 }
 
 struct ProjArgs {
@@ -761,8 +777,9 @@ static int launch_proj(const ProjArgs &a, const Rows &z, const uint16_t *w, cuda
 
 template <bool COLS>
 static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
-  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.by_seg ? a.segs : (a.T + 15) / 16), 16 / DELTA_ROWS);
-  const cudaError_t e = launch_pdl(delta_kernel<COLS>, grid, dim3(128), 0, s, a);
+  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.by_seg ? a.segs : (a.T + 15) / 16), a.by_seg ? 1u : 4u);
+  const cudaError_t e = a.rank <= 16 ? launch_pdl(delta_kernel<COLS, 16>, grid, dim3(128), 0, s, a)
+                                     : launch_pdl(delta_kernel<COLS, 64>, grid, dim3(128), 0, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
