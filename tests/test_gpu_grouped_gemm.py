@@ -142,6 +142,48 @@ def test_accumulate(M, direction, counts):
     _run(M, direction, counts, 144, 96, "f32", accumulate=True, seed=60)
 
 
+@pytest.mark.parametrize("direction,counts,N,K", [
+    ("fwd", [40, 300], 256, 14336), ("fwd", [3, 1, 8, 2], 128, 14336), ("fwd", [130], 320, 1088),
+    ("dgrad", [40, 300], 14336, 256), ("dgrad", [2, 7, 1, 4], 14336, 128),
+    ("wgrad", [16384, 900, 0, 1025], 256, 320)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_error_of_long_reductions(M, direction, counts, N, K, accumulate):
+    """The error of an fp32 output as a whole. A matrix unit may cut the running
+    sum off at each addition: half a unit of the last place on average, 2^-24 of
+    a sum that grows with the root of the number of terms. 64 additions, which
+    are 1024 products at 16 each, lose at most 64 2^-24 of the result on average;
+    longer reductions are to lose no more."""
+    E, R = len(counts), sum(counts)
+    off = [sum(counts[:i]) for i in range(E + 1)]
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    x, dy, w = _rand((R, K), 21), _rand((R, N), 22), _rand((E, N, K), 23)
+    flags = M.MOE_GEMM_OUT_F32 | (M.MOE_GEMM_ACCUMULATE if accumulate else 0)
+    ws = torch.zeros(M.moe_grouped_gemm_workspace_size(R, E, N, K), dtype=torch.uint8, device="cuda")
+    shape = {"fwd": (R, N), "dgrad": (R, K), "wgrad": (E, N, K)}[direction]
+    o = torch.full(shape, 1.5, device="cuda")
+    if direction == "fwd":
+        M.moe_grouped_gemm(x, K, offsets, w, N * K, R, E, N, K, flags, o, N, ws, ws.numel())
+    elif direction == "dgrad":
+        M.moe_grouped_gemm_dgrad(dy, N, offsets, w, N * K, R, E, N, K, flags, o, K, ws, ws.numel())
+    else:
+        M.moe_grouped_gemm_wgrad(dy, N, x, K, offsets, R, E, N, K, flags, o, N * K, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert M.moe_read_device_error(ws) == 0
+    err = size = 0.0
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        if direction == "fwd":
+            ref, got = x[r].double() @ w[e].double().T, o[r]
+        elif direction == "dgrad":
+            ref, got = dy[r].double() @ w[e].double(), o[r]
+        else:
+            ref, got = dy[r].double().T @ x[r].double(), o[e]
+        ref += 1.5 * accumulate
+        err += float((got.double() - ref).square().sum())
+        size += float(ref.square().sum())
+    assert err ** 0.5 <= 64 * 2.0 ** -24 * size ** 0.5
+
+
 @pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
 @pytest.mark.parametrize("E,rows", [(256, 0), (256, 1), (256, 40), (64, 200)])
 def test_many_groups(M, direction, E, rows):

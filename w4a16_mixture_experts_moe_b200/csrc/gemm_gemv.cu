@@ -49,11 +49,11 @@ __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, 
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint16_t *wr = w + int64_t(n0 + g) * a.K + 8 * t;
   const uint16_t *xr = a.in + (r0 + g) * a.ldi + 8 * t;
-  float acc[NT][4];
+  float sum[NT][4];  // each piece's MMAs start from zero: their truncating additions stay few
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
+    for (int q = 0; q < 4; ++q) sum[i][q] = 0.f;
 #pragma unroll 1
   for (int k0 = warp * CH * 32; k0 < a.K; k0 += WARPS * CH * 32) {
     uint4 wv[2][CH];
@@ -70,12 +70,15 @@ __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, 
         xv[c] = k0 + 32 * c + 8 * t < a.K && g + 8 * i < rows
                     ? __ldg(reinterpret_cast<const uint4 *>(xr + 8 * i * a.ldi + k0 + 32 * c))
                     : zero;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const uint4 &wa = wv[0][c], &wb = wv[1][c];
-        mma_16816(acc[i], wa.x, wb.x, wa.y, wb.y, xv[c].x, xv[c].y);
-        mma_16816(acc[i], wa.z, wb.z, wa.w, wb.w, xv[c].z, xv[c].w);
+        mma_16816(acc, wa.x, wb.x, wa.y, wb.y, xv[c].x, xv[c].y);
+        mma_16816(acc, wa.z, wb.z, wa.w, wb.w, xv[c].z, xv[c].w);
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[i][q] += acc[q];
     }
   }
   // (c0, c1) = weight row g, rows 2t, 2t+1 of the 8-row tile; (c2, c3) = weight row g + 8
@@ -83,7 +86,7 @@ __device__ __forceinline__ void rows_pass(const GemvArgs &a, const uint16_t *w, 
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) o[(8 * i + 2 * t + (q & 1)) * LD + g + (q >> 1) * 8] = acc[i][q];
+    for (int q = 0; q < 4; ++q) o[(8 * i + 2 * t + (q & 1)) * LD + g + (q >> 1) * 8] = sum[i][q];
 }
 
 // The dot product of u[row] and row n of the adapter of row's segment.

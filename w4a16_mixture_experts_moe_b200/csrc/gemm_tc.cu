@@ -65,6 +65,13 @@ constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
 // HAND_FIRST (a tile's first k-step, which overwrites the accumulator).
 constexpr int HAND_KK = 7, HAND_LAST = 8, HAND_SET = 16, HAND_STOP = 31, HAND_FIRST = 31;
 constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the output columns
+// The tensor core adds to its fp32 accumulator with truncation, an error that
+// grows with the number of additions: 1e-6 of the result after 1024 products,
+// 1.6e-5 after 14,336. For fp32 outputs a longer reduction is therefore cut into
+// parts of at most F32_STEPS k-steps, which are added up in memory, rounded to
+// nearest, by the threads that own the values (14,336: 9e-7; 105 -> 134 us for
+// 4096 rows of 1024; at 32 steps a part 2e-6 and 124 us).
+constexpr int F32_WHOLE = 16, F32_STEPS = 14;
 constexpr int OUT_ROWS = 32;       // output rows per staged store
 constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // one per half of the epilogue warps
 constexpr int SMEM = STAGES * STAGE_BYTES + 2 * OUT_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
@@ -256,6 +263,12 @@ __device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, in
                : "memory");
 }
 
+// Parts of a tile's reduction of `steps` k-steps, and the first k-step of part p.
+__device__ __forceinline__ int reduction_parts(const TcGemmArgs &a, int steps) {
+  return !a.out_f32 || steps <= F32_WHOLE ? 1 : (steps + F32_STEPS - 1) / F32_STEPS;
+}
+__device__ __forceinline__ int part_start(int steps, int parts, int p) { return steps * p / parts; }
+
 struct Tile {
   int e;       // group
   int row;     // first row of the output tile (fwd, dgrad: row of x / dy; wgrad: row n of dW_e)
@@ -330,22 +343,27 @@ __device__ __forceinline__ uint32_t pack_acc(uint32_t lo, uint32_t hi) {
 }
 
 // Stores n <= 16 output rows of column f (rows a.ldo elements apart from
-// element `at`); `whole`: all of the warp's columns exist. BF16 values go two
-// rows per store: neighbouring lanes swap one value each, so an even lane holds
-// columns f, f + 1 of row j and an odd lane f - 1, f of row j + 1.
-__device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int n, int f, bool whole, const uint32_t (&v)[16]) {
+// element `at`), or adds to them (fp32): a thread adds to its own values only,
+// in order, without waiting for what they held. `whole`: all of the warp's
+// columns exist. BF16 values go two rows per store: neighbouring lanes swap one
+// value each, so an even lane holds columns f, f + 1 of row j and an odd lane
+// f - 1, f of row j + 1.
+__device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int n, int f, bool whole, bool add,
+                                            const uint32_t (&v)[16]) {
   if (a.out_f32) {
     float *o = static_cast<float *>(a.out) + at;
-    if (n == 16 && whole && !a.accumulate) {
+    const bool full = n == 16 && whole;
+    if (add) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j, o += a.ldo)
+        if (full || (j < n && f < a.M)) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(o), "f"(__uint_as_float(v[j])) : "memory");
+    } else if (full) {
 #pragma unroll
       for (int j = 0; j < 16; ++j, o += a.ldo) *o = __uint_as_float(v[j]);
     } else if (f < a.M) {
-      float add[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) add[j] = a.accumulate && j < n ? o[j * a.ldo] : 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        if (j < n) o[j * a.ldo] = __uint_as_float(v[j]) + add[j];
+        if (j < n) o[j * a.ldo] = __uint_as_float(v[j]);
     }
   } else {
     const int odd = threadIdx.x & 1;
@@ -425,8 +443,12 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       return true;
     };
     bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
+    const int parts = reduction_parts(a, nsteps);
+    int part = 0, part_end = part_start(nsteps, parts, 1);
+    bool part_first = true;
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
       if (ks + 1 == nsteps) { more = next_seg(); known = true; }
+      const bool part_last = ks + 1 == part_end;
       uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
       const int left = min(BK, red - ks * BK);
       const bool fix = MODE == GEMM_WGRAD && (left & 15);
@@ -436,7 +458,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       if (elect_one()) {
         if (A_SIDE) {
           sh.step[s] = Step{max(0, (left + 15) >> 4),
-                            (ks == 0 ? STEP_FIRST : 0) | (ks + 1 == nsteps && !more ? STEP_LAST : 0) | (fix ? STEP_FIX_TAIL : 0),
+                            (part_first ? STEP_FIRST : 0) | (part_last && !more ? STEP_LAST : 0) | (fix ? STEP_FIX_TAIL : 0),
                             n16, 0};
           if (fix) mbar_arrive_expect_tx(&sh.landed[s], A_BYTES + b_bytes);
           if (rank == 0) {
@@ -474,6 +496,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       }
       __syncwarp();
       next();
+      part_first = part_last;
+      if (part_last) part_end = part_start(nsteps, parts, ++part + 1);
     }
     if constexpr (MODE != GEMM_WGRAD) {
       if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
@@ -614,12 +638,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const bool issuer = q == 0 && lane == 0;
     const uint32_t out_buf = smem_u32(smem + STAGES * STAGE_BYTES + part * OUT_BYTES);
     if (MODE != GEMM_WGRAD && a.late) pdl_wait();
-    for (int i = 0;; ++i) {
-      const int t = sched_pos(i);
-      if (t >= total) break;
-      const Tile tl = decode_tile<MODE>(sh, a, t);
-      const int b = i & 1;
-      if (!__all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (i >> 1) & 1, a.err))) break;
+    Tile tl = {};
+    int parts = 0;  // of the tile's reduction still to come
+    for (int i = 0, unit = 0;; ++unit) {  // unit & 1: the accumulator
+      const bool add = parts > 0 || a.accumulate;
+      if (parts == 0) {
+        const int t = sched_pos(i++);
+        if (t >= total) break;
+        tl = decode_tile<MODE>(sh, a, t);
+        parts = reduction_parts(a, ((MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD) + BK - 1) / BK);
+      }
+      --parts;
+      const int b = unit & 1;
+      if (!__all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (unit >> 1) & 1, a.err))) break;
       tc_fence_after();
       const int fw = tl.f0 + int(rank) * BMC + q * 32, f = fw + lane;
       const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
@@ -635,9 +666,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         const int n = min(16, tl.nvalid - j0);
         if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
-        store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, v);
+        store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
       };
-      if (zero && a.accumulate) {
+      if (zero && add) {
         // nothing to add
       } else if (a.out_f32)
         for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
