@@ -142,6 +142,24 @@ def test_accumulate(M, direction, counts):
     _run(M, direction, counts, 144, 96, "f32", accumulate=True, seed=60)
 
 
+@pytest.mark.parametrize("counts,N", [
+    ([32], 64), ([33], 64), ([0, 64], 264), ([0, 65], 264),     # few wide tiles: up to 32 rows a group stream
+    ([1, 0, 0, 15], 4096), ([1, 0, 0, 16], 4096),               # 64 of them: up to 4
+    ([2] * 64, 2048), ([2] * 63 + [3], 2048), ([1] * 9 + [0] * 54 + [119], 2048)])  # many: up to 2
+def test_both_sides_of_the_streaming_rule(M, counts, N):
+    _run(M, "fwd", counts, N, 136, seed=70)
+    _run(M, "fwd", counts, N, 136, "f32", lead=3, tail=0, seed=71)
+
+
+def test_no_rows_with_gaps_between_the_gradients(M):
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for dt, flags in ((torch.bfloat16, 0), (torch.float32, M.MOE_GEMM_OUT_F32)):
+        dw = torch.full((3, 160), 2.0, dtype=dt, device="cuda")
+        M.moe_grouped_gemm_wgrad(None, 16, None, 8, off, 0, 3, 16, 8, flags, dw, 160, ws, 256)
+        assert (dw[:, :128] == 0).all() and (dw[:, 128:] == 2).all()
+
+
 @pytest.mark.parametrize("direction,counts,N,K", [
     ("fwd", [40, 300], 256, 14336), ("fwd", [3, 1, 8, 2], 128, 14336), ("fwd", [130], 320, 1088),
     ("dgrad", [40, 300], 14336, 256), ("dgrad", [2, 7, 1, 4], 14336, 128),

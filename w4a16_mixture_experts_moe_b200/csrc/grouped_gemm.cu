@@ -5,9 +5,21 @@
 
 namespace moe {
 
-// Up to this many rows per group on average the forward product streams the
-// weights (gemm_gemv.cu).
-constexpr int GEMV_MAX_ROWS_PER_GROUP = 16;
+// Whether the forward product streams the weights (gemm_gemv.cu) or takes the
+// tensor-core engine. Streaming reads a group's weights once per 16 rows but
+// spreads them over all SMs whatever their number; the engine reads them once
+// and gives 256 columns of a group to a pair of SMs. So the rows per group up to
+// which streaming is faster fall with the number of the engine's tiles, from
+// 32 at a few (8 groups of 16, N = 512, K = 2048: 7.1 against 13.2 us) over 8
+// (2 groups of 8, N = K = 4096: 12.9 against 20.0) to 2 at several per pair (64
+// groups of 2, N = 2048, K = 1024: 45.5 against 49.6; groups of 12: 67 against
+// 50). Where rows are few on average but not in every group (64 groups, 256
+// skewed rows: 41 against 38 us; all 256 in one: 83 against 12), the engine loses
+// little when it should and streaming much, hence not more than 2.
+static bool use_gemv(int R, int E, int N) {
+  const int64_t tiles = int64_t(E) * ((N + 255) / 256), most = 4 * 74 / tiles;
+  return int64_t(R) <= int64_t(E) * (most < 2 ? 2 : most > 32 ? 32 : most);
+}
 
 static int check_grouped(const char *who, int R, int E, int N, int K, int flags, const void *offsets, const void *ws,
                          size_t ws_bytes) {
@@ -69,7 +81,7 @@ extern "C" int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *o
       (st = check_matrix(who, "w", w, w_stride, int64_t(N) * K)) != MOE_OK)
     return st;
   cudaStream_t s = as_stream(stream);
-  if (int64_t(R) <= int64_t(GEMV_MAX_ROWS_PER_GROUP) * E) {
+  if (use_gemv(R, E, N)) {
     GemvArgs v = {};
     v.in = x; v.ldi = ldx; v.offsets = offsets; v.w = w; v.w_stride = w_stride;
     v.groups = E; v.n_weights = E; v.R = R; v.N = N; v.K = K;
@@ -114,10 +126,12 @@ extern "C" int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const mo
   if ((st = check_matrix(who, "dw", dw, dw_stride, int64_t(N) * K)) != MOE_OK) return st;
   cudaStream_t s = as_stream(stream);
   if (R == 0) {  // no rows: zero gradients (nothing to add when accumulating)
-    const size_t el = (flags & MOE_GEMM_OUT_F32) ? 4 : 2;
-    const cudaError_t e = (flags & MOE_GEMM_ACCUMULATE)
-                              ? cudaSuccess
-                              : cudaMemset2DAsync(dw, size_t(dw_stride) * el, 0, size_t(N) * K * el, size_t(E), s);
+    const size_t el = (flags & MOE_GEMM_OUT_F32) ? 4 : 2, bytes = size_t(N) * K * el;
+    const bool whole = dw_stride == int64_t(N) * K;
+    cudaError_t e = cudaSuccess;
+    if (!(flags & MOE_GEMM_ACCUMULATE))
+      for (int g = 0; g < (whole ? 1 : E) && e == cudaSuccess; ++g)
+        e = cudaMemsetAsync(static_cast<uint8_t *>(dw) + size_t(g) * dw_stride * el, 0, whole ? bytes * E : bytes, s);
     return e == cudaSuccess ? MOE_OK : set_error(MOE_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
   }
   if ((st = check_matrix(who, "dy", dy, lddy, N)) != MOE_OK || (st = check_matrix(who, "x", x, ldx, K)) != MOE_OK)
