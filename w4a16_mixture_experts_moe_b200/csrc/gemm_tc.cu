@@ -264,8 +264,9 @@ __device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, in
 }
 
 // Parts of a tile's reduction of `steps` k-steps, and the first k-step of part p.
-__device__ __forceinline__ int reduction_parts(const TcGemmArgs &a, int steps) {
-  return !a.out_f32 || steps <= F32_WHOLE ? 1 : (steps + F32_STEPS - 1) / F32_STEPS;
+template <bool F32>
+__device__ __forceinline__ int reduction_parts(int steps) {
+  return !F32 || steps <= F32_WHOLE ? 1 : (steps + F32_STEPS - 1) / F32_STEPS;
 }
 __device__ __forceinline__ int part_start(int steps, int parts, int p) { return steps * p / parts; }
 
@@ -348,9 +349,10 @@ __device__ __forceinline__ uint32_t pack_acc(uint32_t lo, uint32_t hi) {
 // columns exist. BF16 values go two rows per store: neighbouring lanes swap one
 // value each, so an even lane holds columns f, f + 1 of row j and an odd lane
 // f - 1, f of row j + 1.
+template <bool F32>
 __device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int n, int f, bool whole, bool add,
                                             const uint32_t (&v)[16]) {
-  if (a.out_f32) {
+  if (F32) {
     float *o = static_cast<float *>(a.out) + at;
     const bool full = n == 16 && whole;
     if (add) {
@@ -393,7 +395,7 @@ __device__ __forceinline__ int sched_pos(int i) {
 // warp issuing both took 490 cycles a k-step, as long as its MMAs.) The warp
 // stays converged and elects the issuing lane, which keeps the loads' operands
 // in uniform registers.
-template <int MODE, bool A_SIDE>
+template <int MODE, bool F32, bool A_SIDE>
 __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const Maps &m, uint8_t *smem, uint32_t rank,
                                         int total) {
   int s = 0, round = 0;  // ring slot and its use
@@ -443,12 +445,12 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       return true;
     };
     bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
-    const int parts = reduction_parts(a, nsteps);
+    const int parts = reduction_parts<F32>(nsteps);
     int part = 0, part_end = part_start(nsteps, parts, 1);
     bool part_first = true;
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
       if (ks + 1 == nsteps) { more = next_seg(); known = true; }
-      const bool part_last = ks + 1 == part_end;
+      const bool part_last = ks + 1 == (F32 ? part_end : nsteps);
       uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
       const int left = min(BK, red - ks * BK);
       const bool fix = MODE == GEMM_WGRAD && (left & 15);
@@ -496,8 +498,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       }
       __syncwarp();
       next();
-      part_first = part_last;
-      if (part_last) part_end = part_start(nsteps, parts, ++part + 1);
+      part_first = F32 && part_last;
+      if (F32 && part_last) part_end = part_start(nsteps, parts, ++part + 1);
     }
     if constexpr (MODE != GEMM_WGRAD) {
       if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
@@ -548,7 +550,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
   __syncwarp();
 }
 
-template <int MODE>
+template <int MODE, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gemm_kernel(const TcGemmArgs a, const __grid_constant__ Maps m) {
   extern __shared__ uint8_t smem_raw[];
@@ -638,88 +640,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const bool issuer = q == 0 && lane == 0;
     const uint32_t out_buf = smem_u32(smem + STAGES * STAGE_BYTES + part * OUT_BYTES);
     if (MODE != GEMM_WGRAD && a.late) pdl_wait();
-    Tile tl = {};
-    int parts = 0;  // of the tile's reduction still to come
-    for (int i = 0, unit = 0;; ++unit) {  // unit & 1: the accumulator
-      const bool add = parts > 0 || a.accumulate;
-      if (parts == 0) {
-        const int t = sched_pos(i++);
-        if (t >= total) break;
-        tl = decode_tile<MODE>(sh, a, t);
-        parts = reduction_parts(a, ((MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD) + BK - 1) / BK);
-      }
-      --parts;
-      const int b = unit & 1;
-      if (!__all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (unit >> 1) & 1, a.err))) break;
-      tc_fence_after();
-      const int fw = tl.f0 + int(rank) * BMC + q * 32, f = fw + lane;
-      const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
-      const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
-      const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
-      // accumulator columns j0 .. j0 + 15, row by row from registers
-      auto direct = [&](int j0) {
-        uint32_t v[16];
-        tmem_ld16(tb + j0, v);
-        if (zero) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = 0;
-        }
-        const int n = min(16, tl.nvalid - j0);
-        if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
-        store_block(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
-      };
-      if (zero && add) {
-        // nothing to add
-      } else if (a.out_f32)
-        for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
-      else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
-        const int rows = min(OUT_ROWS, tl.nvalid - j0);
-        if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
-            !(MODE != GEMM_WGRAD && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
-          // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
-          // warps write 128 columns of them to shared memory, one thread sends
-          // them off
-          uint32_t x[16], y[16];
-          tmem_ld_frag(tb + j0, x, y);
+    bool ok = true;
+    for (int i = 0, unit = 0; ok; ++i) {  // unit & 1: the accumulator
+      const int t = sched_pos(i);
+      if (t >= total) break;
+      const Tile tl = decode_tile<MODE>(sh, a, t);
+      const int parts = reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD) + BK - 1) / BK);
+      for (int p = 0; p < parts; ++p, ++unit) {
+        const bool add = F32 && (p > 0 || a.accumulate);
+        const int b = unit & 1;
+        ok = __all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (unit >> 1) & 1, a.err));
+        if (!ok) break;
+        tc_fence_after();
+        const int fw = tl.f0 + int(rank) * BMC + q * 32, f = fw + lane;
+        const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
+        const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
+        const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
+        // accumulator columns j0 .. j0 + 15, row by row from registers
+        auto direct = [&](int j0) {
+          uint32_t v[16];
+          tmem_ld16(tb + j0, v);
           if (zero) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = y[j] = 0;
+            for (int j = 0; j < 16; ++j) v[j] = 0;
           }
-          if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          out_sync(part);
-          const int piece = q * 4 + (lane >> 3);  // 8 columns
+          const int n = min(16, tl.nvalid - j0);
+          if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
+          store_block<F32>(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
+        };
+        if (zero && add) {
+          // nothing to add
+        } else if (F32)
+          for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
+        else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
+          const int rows = min(OUT_ROWS, tl.nvalid - j0);
+          if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
+              !(MODE != GEMM_WGRAD && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
+            // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
+            // warps write 128 columns of them to shared memory, one thread sends
+            // them off
+            uint32_t x[16], y[16];
+            tmem_ld_frag(tb + j0, x, y);
+            if (zero) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane & 7);
-            stmatrix_trans(out_buf + (piece >> 3) * (OUT_ROWS * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
-                           pack_acc(x[4 * i], x[4 * i + 1]), pack_acc(x[4 * i + 2], x[4 * i + 3]),
-                           pack_acc(y[4 * i], y[4 * i + 1]), pack_acc(y[4 * i + 2], y[4 * i + 3]));
-          }
-          fence_proxy_async();
-          out_sync(part);
-          if (issuer) {
-            const int fc = tl.f0 + int(rank) * BMC;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (fc + 64 * h >= a.M) break;
-              if (MODE == GEMM_WGRAD) store_3d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0, tl.e);
-              else store_2d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0);
+              for (int j = 0; j < 16; ++j) x[j] = y[j] = 0;
             }
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            out_sync(part);
+            const int piece = q * 4 + (lane >> 3);  // 8 columns
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane & 7);
+              stmatrix_trans(out_buf + (piece >> 3) * (OUT_ROWS * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                             pack_acc(x[4 * i], x[4 * i + 1]), pack_acc(x[4 * i + 2], x[4 * i + 3]),
+                             pack_acc(y[4 * i], y[4 * i + 1]), pack_acc(y[4 * i + 2], y[4 * i + 3]));
+            }
+            fence_proxy_async();
+            out_sync(part);
+            if (issuer) {
+              const int fc = tl.f0 + int(rank) * BMC;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (fc + 64 * h >= a.M) break;
+                if (MODE == GEMM_WGRAD) store_3d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0, tl.e);
+                else store_2d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0);
+              }
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            continue;
           }
-          continue;
+          for (int j1 = j0; j1 < j0 + rows; j1 += 16) direct(j1);
         }
-        for (int j1 = j0; j1 < j0 + rows; j1 += 16) direct(j1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
     }
     if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == A_WARP) {
-    produce<MODE, true>(sh, a, m, smem, rank, total);
+    produce<MODE, F32, true>(sh, a, m, smem, rank, total);
   } else if (warp == B_WARP) {
-    produce<MODE, false>(sh, a, m, smem, rank, total);
+    produce<MODE, F32, false>(sh, a, m, smem, rank, total);
   } else if (warp == FIX_WARP) {
     // ================================================================ tails
     if (MODE == GEMM_WGRAD) {
@@ -833,7 +834,7 @@ bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4],
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
+template <int MODE, bool F32>
 static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what) {
   gt::Maps m = {};
   bool ok = true;
@@ -859,7 +860,7 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
   } else {
     for (int i = 0; i < 3; ++i) ok &= map_bf16(&m.b[i], op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, 32 << i, 1, 1});
   }
-  if (!a.out_f32)
+  if (!F32)
     ok &= MODE == GEMM_WGRAD
               ? map_bf16(&m.out, a.out, 3, {K, N, a.groups, 1}, {a.ldo, a.out_gstride, 0}, {64, gt::OUT_ROWS, 1, 1})
               : map_bf16(&m.out, a.out, 2, {a.M, a.R, 1, 1}, {a.ldo, 0, 0}, {64, gt::OUT_ROWS, 1, 1});
@@ -873,10 +874,10 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
       ok &= map_bf16(&m.eb[i], a.ext_b, 2, {a.rank, a.R, 1, 1}, {a.rank, 0, 0}, {64, 32 << i, 1, 1});
   }
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE>), gt::SMEM, what);
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE, F32>), gt::SMEM, what);
   if (st != MOE_OK) return st;
   const int grid = sm_count() & ~1;
-  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, m);
+  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE, F32>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, m);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -892,9 +893,11 @@ int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op,
   const int64_t rows = mode == GEMM_WGRAD ? int64_t(a.groups) * ((int64_t(a.NC) + 255) / 256) : int64_t(a.R) / a.bn + a.groups;
   if (cols * rows > (int64_t(1) << 30))
     return set_error(MOE_ERR_SHAPE, "%s: too many tiles (%lld)", what, (long long)(cols * rows));
-  return mode == GEMM_FWD     ? launch_mode<GEMM_FWD>(a, op, s, what)
-         : mode == GEMM_DGRAD ? launch_mode<GEMM_DGRAD>(a, op, s, what)
-                              : launch_mode<GEMM_WGRAD>(a, op, s, what);
+  switch (mode) {
+    case GEMM_FWD: return a.out_f32 ? launch_mode<GEMM_FWD, true>(a, op, s, what) : launch_mode<GEMM_FWD, false>(a, op, s, what);
+    case GEMM_DGRAD: return a.out_f32 ? launch_mode<GEMM_DGRAD, true>(a, op, s, what) : launch_mode<GEMM_DGRAD, false>(a, op, s, what);
+    default: return a.out_f32 ? launch_mode<GEMM_WGRAD, true>(a, op, s, what) : launch_mode<GEMM_WGRAD, false>(a, op, s, what);
+  }
 }
 
 }  // namespace moe
