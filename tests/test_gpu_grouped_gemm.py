@@ -263,6 +263,39 @@ def test_bad_offsets_are_cut_and_flagged(M, R, E):
     assert M.moe_read_device_error(ws) == 0
 
 
+LO, HI = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("off", [[0, 3, 1, 2, 3], [0, 2, LO, 2, 3], [HI, LO, HI, LO, HI], [1, LO, 3, LO, 2], [2, 2, 2, 2, HI]])
+@pytest.mark.parametrize("R", [3, 90, 2000])  # a pass per grid row, later passes, the tensor cores
+def test_extreme_offsets(M, off, R):
+    E, N, K = 4, 64, 72
+    off = torch.tensor([min(o * (R // 3), HI) if 0 < o < HI else o for o in off], dtype=torch.int32, device="cuda")
+    x, dy, w = _rand((R, K), 1), _rand((R, N), 3), _rand((E, N, K), 2)
+    guard = 64  # rows before and behind what the calls may write
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for flags, dt in ((0, torch.bfloat16), (M.MOE_GEMM_OUT_F32, torch.float32)):
+        y = torch.zeros(R + 2 * guard, N, dtype=dt, device="cuda")
+        dx = torch.zeros(R + 2 * guard, K, dtype=dt, device="cuda")
+        dw = torch.zeros(E + 2, N, K, dtype=dt, device="cuda")
+        M.moe_grouped_gemm(x, K, off, w, N * K, R, E, N, K, flags, y[guard:], N, ws, 256)
+        assert M.moe_read_device_error(ws) == M.MOE_DEVERR_OFFSETS
+        M.moe_grouped_gemm_dgrad(dy, N, off, w, N * K, R, E, N, K, flags, dx[guard:], K, ws, 256)
+        assert M.moe_read_device_error(ws) == M.MOE_DEVERR_OFFSETS
+        M.moe_grouped_gemm_wgrad(dy, N, x, K, off, R, E, N, K, flags, dw[1:], N * K, ws, 256)
+        assert M.moe_read_device_error(ws) == M.MOE_DEVERR_OFFSETS
+        for t in (y, dx):
+            assert torch.isfinite(t).all() and (t[:guard] == 0).all() and (t[-guard:] == 0).all()
+        assert torch.isfinite(dw).all() and (dw[0] == 0).all() and (dw[-1] == 0).all()
+
+
+@pytest.mark.parametrize("counts", [[200, 0, 1], [1, 0, 100, 0, 0, 17, 16, 33], [0] * 50 + [49] + [0] * 4, [0] * 30 + [64, 1] + [0] * 32])
+def test_passes_of_long_groups_beside_short_ones(M, counts):
+    N = 8 if len(counts) < 50 else 264  # narrow: such groups stream
+    _run(M, "fwd", counts, N, 200, seed=75)
+    _run(M, "fwd", counts, N, 200, "f32", accumulate=True, seed=76)
+
+
 def test_equal_calls_give_equal_bits(M):
     for d in ("fwd", "dgrad", "wgrad"):
         a = _run(M, d, [300, 0, 511, 40], 512, 456, "f32", seed=80)

@@ -268,6 +268,40 @@ def test_bad_segments_are_cut_and_flagged(M, T, N, K):
     p.check_backward()
 
 
+LO, HI = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("off", [[0, 3, 1, 2, 3], [0, 2, LO, 2, 3], [HI, LO, HI, LO, HI], [1, LO, 3, LO, 2], [2, 2, 2, 2, HI]])
+@pytest.mark.parametrize("T,N,K", [(6, 64, 72), (60, 64, 72), (201, 64, 72), (2010, 2048, 2048)])
+def test_extreme_segments(M, off, T, N, K):
+    p = Problem([T, 0, 0, 0], [0, 1, HI, LO], 2, 16, N, K, seed=7)
+    p.xs, p.dys = p.x, p.dy
+    p.seg_off.copy_(torch.tensor([min(o * (T // 3), HI) if 0 < o < HI else o for o in off], dtype=torch.int32))
+    ws = p.workspace(M)
+    p.u.zero_(), p.du.zero_()
+    guard = 64  # rows before and behind what the calls may write
+    y, dx = (torch.zeros(T + 2 * guard, c, dtype=torch.bfloat16, device="cuda") for c in (N, K))
+    p.y, p.dx = y[guard:], dx[guard:]
+    p.forward(M, ws)
+    assert M.moe_read_device_error(ws) in (M.MOE_DEVERR_OFFSETS, M.MOE_DEVERR_EXPERT_ID)
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) in (M.MOE_DEVERR_OFFSETS, M.MOE_DEVERR_EXPERT_ID)
+    for t in (y, dx):
+        assert (t[:guard] == 0).all() and (t[-guard:] == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[1] * 30 + [400], [400] + [1] * 40 + [0, 17, 33, 16], [500] + [0] * 40])
+def test_long_segments_among_many_short_ones(M, lens):
+    p = Problem(lens, [i % 4 - 1 for i in range(len(lens))], 3, 24, 136, 264, seed=8)
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_forward()
+    p.backward(M, ws)
+    p.check_backward()
+
+
 def test_no_rows_and_partial_gradients(M):
     p = Problem([30, 20], [0, 1], 2, 16, 72, 64, seed=6)
     p.strided()

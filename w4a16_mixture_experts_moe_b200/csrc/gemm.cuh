@@ -60,6 +60,12 @@ bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4],
 
 int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what);
 
+// Who does a group's passes of GEMV_PASS rows: one grid row per group all of
+// them; grid row y the y-th pass of all groups (few rows, many groups); or grid
+// rows [0, groups) the groups' first passes and those behind the later ones.
+constexpr int GEMV_PASS = 16;
+enum GemvSplit { GEMV_WHOLE = 0, GEMV_ALL_PASSES = 1, GEMV_LATER_PASSES = 2 };
+
 // One product for the weight-streaming kernel (gemm_gemv.cu): out[r] = in[r] W^T
 // for the rows of each group, W [N][K] at w + index * w_stride.
 struct GemvArgs {
@@ -70,7 +76,7 @@ struct GemvArgs {
   const uint16_t *w;
   int64_t w_stride;
   int groups, n_weights, R, N, K;
-  int compact;             // grid row y = the y-th group with rows
+  int split;               // GEMV_*
   const float *scale;      // [n_weights] factor of each weight matrix, or nullptr
   void *out;
   int64_t ldo;
@@ -82,7 +88,6 @@ struct GemvArgs {
   const uint16_t *u, *lora_b;
 };
 
-// grid_groups: grid rows (groups, or R with `compact`).
-int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what);
+int launch_gemm_gemv(GemvArgs a, cudaStream_t s, const char *what);
 
 }  // namespace moe

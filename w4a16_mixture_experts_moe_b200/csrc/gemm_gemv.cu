@@ -11,6 +11,11 @@
 // for the rows of `in` (8 per MMA) as well. The warps' partial sums meet in
 // shared memory and are added in a fixed order.
 //
+// A pass takes 16 rows and reads the weights again (from L2): groups of a few
+// rows are one pass. Passes of long groups go to CTAs of their own, which find
+// theirs by counting (the whole projection, N = K = 2048, rank 16, of 99 single
+// rows and a segment of 1400: 262 -> 46 us; 64 groups of 2 rows 44 -> 45).
+//
 // Per-request adapters are added where the sums meet: out[r][n] gets the dot
 // product of u[r] and row n of its adapter's B (rank values, contiguous), so
 // they cost one small read per (row, column). u comes from the launch before:
@@ -23,7 +28,7 @@ namespace gv {
 constexpr int COLS = 16;     // output columns per CTA
 constexpr int LD = COLS + 1; // row stride of the partial sums
 constexpr int CH = 4;        // 32-wide chunks of a piece
-constexpr int MAXNT = 2;     // 8-row tiles of `in` per pass
+constexpr int MAXNT = GEMV_PASS / 8;  // 8-row tiles of `in` per pass
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -117,40 +122,53 @@ struct Cfg {
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const GemvArgs a) {
   extern __shared__ float red[];
-  __shared__ int found[32], which;
+  __shared__ int found[32], which, pass;
   const bool late = a.seg_adapter != nullptr;  // the previous launch only writes u
   if (!late) pdl_wait();
   pdl_trigger();  // behind the wait: a launch that starts early may count on what this one waited for
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int e = blockIdx.y;
-  if (a.compact) {  // the blockIdx.y-th group with rows
+  int e = blockIdx.y, r_first = 0;
+  if (a.split == GEMV_ALL_PASSES || (a.split == GEMV_LATER_PASSES && e >= a.groups)) {
+    // the want-th pass of the groups' passes, counted from each group's `from`-th
+    const int from = a.split == GEMV_ALL_PASSES ? 0 : 1, want = e - from * a.groups;
+    const bool check = want == 0 && from == 0;  // looks at every group
     if (tid == 0) which = -1;
     int base = 0;
-    for (int e0 = 0; e0 < a.groups; e0 += WARPS * 32) {
+    for (int e0 = 0; e0 < a.groups && (base <= want || check); e0 += WARPS * 32) {
       const int q = e0 + tid;
-      const bool has = q < a.groups && a.offsets[q + 1] > a.offsets[q];
-      const uint32_t m = __ballot_sync(0xffffffffu, has);
+      const int o0 = q < a.groups ? a.offsets[q] : 0, o1 = q < a.groups ? a.offsets[q + 1] : 0;
+      if (check && blockIdx.x == 0 && (o0 < 0 || o1 < o0 || o1 > a.R)) flag_error(a.err, MOE_DEVERR_OFFSETS);
+      const int rows = min(max(o1, 0), a.R) - min(max(o0, 0), a.R);
+      const int n = max(0, (rows + MAXNT * 8 - 1) / (MAXNT * 8) - from);
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int p = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += p;
+      }
       __syncthreads();
-      if (lane == 0) found[warp] = __popc(m);
+      if (lane == 31) found[warp] = incl;
       __syncthreads();
-      int before = base + __popc(m & ((1u << lane) - 1));
+      int before = base + incl - n;
       for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += found[w];
         base += found[w];
       }
-      if (has && before == int(blockIdx.y)) which = q;
+      if (before <= want && want < before + n) { which = q; pass = want - before + from; }
     }
     __syncthreads();
     e = which;
     if (e < 0) return;
+    r_first = pass * MAXNT * 8;
   }
   // with adapters: one group, the rows up to the end of the last segment
   const int o0 = late ? 0 : a.offsets[e], o1 = late ? a.seg_offsets[a.segs] : a.offsets[e + 1];
   // (segments start at row 0, groups anywhere)
   if ((o0 < 0 || o1 < o0 || o1 > a.R || (a.index && e == 0 && o0 != 0)) && blockIdx.x == 0 && tid == 0)
     flag_error(a.err, MOE_DEVERR_OFFSETS);
-  const int lo = min(max(o0, 0), a.R), cnt = min(o1, a.R) - lo;
-  if (cnt <= 0) return;
+  const int lo = min(max(o0, 0), a.R), rows_in = min(max(o1, 0), a.R) - lo;
+  if (rows_in <= 0) return;
+  const int cnt = a.split == GEMV_WHOLE ? rows_in : min(rows_in, r_first + MAXNT * 8);  // this CTA's: r_first .. cnt - 1
   const int wi = a.index ? a.index[e] : e;
   const bool none = wi < 0 || wi >= a.n_weights;
   if (none && wi != -1 && blockIdx.x == 0 && tid == 0) flag_error(a.err, MOE_DEVERR_EXPERT_ID);
@@ -159,7 +177,7 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
   const int n0 = blockIdx.x * COLS;
 
 #pragma unroll 1
-  for (int r0 = 0; r0 < cnt; r0 += MAXNT * 8) {
+  for (int r0 = r_first; r0 < cnt; r0 += MAXNT * 8) {
     const int rows = min(MAXNT * 8, cnt - r0);
     int nt = 1;  // 8-row tiles of this pass, the stride of the partial sums
     if (!none) {
@@ -209,12 +227,16 @@ static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const c
 
 }  // namespace gv
 
-int launch_gemm_gemv(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
-  if (a.seg_adapter) return gv::launch_as<8>(a, grid_groups, s, what);  // one group of few rows
+int launch_gemm_gemv(GemvArgs a, cudaStream_t s, const char *what) {
+  // at most one pass per row; at most (R - 1) / GEMV_PASS behind the groups' first
+  const int64_t later = (a.R - 1) / GEMV_PASS;
+  if (a.split == GEMV_LATER_PASSES && a.groups + later > 65535) a.split = GEMV_WHOLE;  // a grid dimension's limit
+  const int ny = a.split == GEMV_ALL_PASSES ? a.R : a.split == GEMV_LATER_PASSES ? int(a.groups + later) : a.groups;
+  if (a.seg_adapter) return gv::launch_as<8>(a, ny, s, what);  // one group of few rows
   // few CTAs: more warps share a CTA's reduction
-  const int64_t ctas = int64_t(grid_groups) * ((a.N + 15) / 16);
-  if (ctas <= 2 * 148) return gv::launch_as<16>(a, grid_groups, s, what);
-  return gv::launch_as<4>(a, grid_groups, s, what);
+  const int64_t ctas = int64_t(ny) * ((a.N + 15) / 16);
+  if (ctas <= 2 * 148) return gv::launch_as<16>(a, ny, s, what);
+  return gv::launch_as<4>(a, ny, s, what);
 }
 
 }  // namespace moe

@@ -431,8 +431,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
         const bool in = sg + lane < a.segs;
         const int o0 = in ? a.offsets[sg + lane] : INT32_MAX, o1 = in ? a.offsets[sg + lane + 1] : 0;
         my_a = in ? a.adapter[sg + lane] : -1;
-        my_lo = o0 < tile_end ? (max(o0 - tl.row, 0) + 15) & ~15 : 0;
-        my_hi = o1 >= tile_end ? n16 * 16 : (o1 - tl.row) & ~15;
+        my_lo = o0 < tile_end ? (max(o0, tl.row) - tl.row + 15) & ~15 : 0;
+        my_hi = o1 >= tile_end ? n16 * 16 : (max(o1, tl.row) - tl.row) & ~15;
         found = __ballot_sync(0xffffffffu, o0 < tile_end && my_hi > my_lo && my_a >= 0 && my_a < a.n_adapters);
         end = __any_sync(0xffffffffu, o0 >= tile_end);
         sg += 32;
@@ -594,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (e < a.groups) {
         const int o0 = a.adapter ? 0 : a.offsets[e], o1 = a.adapter ? a.offsets[a.segs] : a.offsets[e + 1];
         bad |= o0 < 0 || o1 < o0 || o1 > a.R;
-        const int lo = min(max(o0, 0), a.R), cnt = max(0, min(o1, a.R) - lo);
+        const int lo = min(max(o0, 0), a.R), cnt = max(0, min(max(o1, 0), a.R) - lo);
         sh.lo[e] = lo;
         sh.cnt[e] = cnt;
         v[i] = (cnt + a.bn - 1) / a.bn * FT;

@@ -13,9 +13,8 @@ namespace moe {
 // 32 at a few (8 groups of 16, N = 512, K = 2048: 7.1 against 13.2 us) over 8
 // (2 groups of 8, N = K = 4096: 12.9 against 20.0) to 2 at several per pair (64
 // groups of 2, N = 2048, K = 1024: 45.5 against 49.6; groups of 12: 67 against
-// 50). Where rows are few on average but not in every group (64 groups, 256
-// skewed rows: 41 against 38 us; all 256 in one: 83 against 12), the engine loses
-// little when it should and streaming much, hence not more than 2.
+// 50). Rows that are few on average but not in every group cost streaming more
+// than the engine, too (64 groups, 256 skewed rows: 41 against 38 us).
 static bool use_gemv(int R, int E, int N) {
   const int64_t tiles = int64_t(E) * ((N + 255) / 256), most = 4 * 74 / tiles;
   return int64_t(R) <= int64_t(E) * (most < 2 ? 2 : most > 32 ? 32 : most);
@@ -85,12 +84,12 @@ extern "C" int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *o
     GemvArgs v = {};
     v.in = x; v.ldi = ldx; v.offsets = offsets; v.w = w; v.w_stride = w_stride;
     v.groups = E; v.n_weights = E; v.R = R; v.N = N; v.K = K;
-    v.compact = R < E;
+    v.split = R < E ? GEMV_ALL_PASSES : GEMV_LATER_PASSES;
     v.out = y; v.ldo = ldy;
     v.out_f32 = (flags & MOE_GEMM_OUT_F32) != 0;
     v.accumulate = (flags & MOE_GEMM_ACCUMULATE) != 0;
     v.err = static_cast<int32_t *>(ws);
-    return launch_gemm_gemv(v, v.compact ? R : E, s, who);
+    return launch_gemm_gemv(v, s, who);
   }
   TcGemmArgs a = grouped_args(offsets, R, E, flags, y, ldy, ws);
   a.M = N;

@@ -953,7 +953,8 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.w = lora_a; v.w_stride = int64_t(rank) * K;
     v.groups = S; v.n_weights = n_adapters; v.R = T; v.N = rank; v.K = K;
     v.scale = scale; v.out = u; v.ldo = rank; v.err = err;
-    st = launch_gemm_gemv(v, S, s, "moe_lora_linear (adapters)");
+    v.split = GEMV_LATER_PASSES;
+    st = launch_gemm_gemv(v, s, "moe_lora_linear (adapters)");
   } else {
     const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, u, err};
     st = lora::launch_shrink<false>(h, {x, ldx, K}, lora_a, s, "moe_lora_linear (adapters)");
@@ -965,7 +966,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.out = y; v.ldo = ldy; v.err = err;
     v.seg_offsets = seg_offsets; v.seg_adapter = seg_adapter; v.segs = S; v.n_adapters = n_adapters; v.rank = rank;
     v.u = u; v.lora_b = lora_b;
-    return launch_gemm_gemv(v, 1, s, who);
+    return launch_gemm_gemv(v, s, who);
   }
   if (lora::use_proj(T, N, K)) {
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, K, N, rank, u, lora_b, y, ldy, err};
