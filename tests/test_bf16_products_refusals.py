@@ -110,9 +110,9 @@ def test_adapter_backward_rows(N, bad):
 def test_workspace_sizes(N):
     assert N.moe_grouped_gemm_workspace_size(0, 1, 8, 8) >= 256
     base = N.moe_lora_workspace_size(8192, 1, 4, 16, 4096, 2048)
-    # fp32 rows for the 16-row blocks that segments share: 16 per segment, at most one per row
-    assert N.moe_lora_workspace_size(8192, 13, 4, 16, 4096, 2048) == base + 13 * 16 * 4096 * 4
-    assert N.moe_lora_workspace_size(40, 40, 4, 16, 2048, 4096) == base + 48 * 4096 * 4
+    # fp32 rows for the 16-row blocks that segments share: 16 per segment, at most one per row; the rows' segments
+    assert N.moe_lora_workspace_size(8192, 13, 4, 16, 4096, 2048) == base + 13 * 16 * 4096 * 4 + 8192 * 4
+    assert N.moe_lora_workspace_size(40, 40, 4, 16, 2048, 4096) == base + 48 * 4096 * 4 + 40 * 4
 
 
 def test_names_are_public(N):

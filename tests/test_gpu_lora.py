@@ -176,6 +176,13 @@ CASES = [
     ([64, 64, 128, 256], [0, 1, 2, 3], 4, 128, 264, 136, 0),
     ([1000, 777], [1, 0], 2, 72, 512, 648, 0),
     ([0, 0, 70], [0, 1, 1], 2, 40, 72, 1032, 0),
+    # the engine's shared blocks by every width of rank, found by number and by owning segment
+    ([1] * 200 + [500], [i % 4 - 1 for i in range(201)], 3, 8, 1032, 1040, 5),
+    ([3] * 150 + [411, 0], [i % 9 - 1 for i in range(152)], 8, 16, 1040, 1032, 0),
+    ([900, 37, 0, 1111, 5], [0, 2, 1, -1, 1], 3, 64, 1032, 1040, 0),
+    ([1] * 99 + [901], [i % 3 for i in range(100)], 3, 120, 1032, 1040, 0),
+    ([1] * 20 + [1400], [i % 6 - 1 for i in range(21)], 5, 40, 1032, 1160, 2),
+    ([17] * 140, [i % 6 - 1 for i in range(140)], 5, 16, 1032, 1040, 2),
 ]
 
 

@@ -28,6 +28,7 @@ struct TcGemmArgs {
   // the launch before (lora.cu); row of block b: 16 b, or 16 owner if delta_by_seg
   const float *delta;
   int delta_by_seg;
+  const int32_t *row_seg;  // [R] the rows' segments (with delta)
   int late;  // the launches before this one wait for everything but u / du, delta and the output
   int32_t *err;
 };
@@ -81,6 +82,7 @@ struct GemvArgs {
   void *out;
   int64_t ldo;
   int out_f32, accumulate;
+  int32_t *row_seg;        // [R] the rows' groups, written (or nullptr)
   int32_t *err;
   // adapters added to a single group's product: out[r] += u[r] B_a^T
   const int32_t *seg_offsets, *seg_adapter;

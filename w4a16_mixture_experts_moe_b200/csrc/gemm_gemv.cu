@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
   const int lo = min(max(o0, 0), a.R), rows_in = min(max(o1, 0), a.R) - lo;
   if (rows_in <= 0) return;
   const int cnt = a.split == GEMV_WHOLE ? rows_in : min(rows_in, r_first + MAXNT * 8);  // this CTA's: r_first .. cnt - 1
+  if (a.row_seg && blockIdx.x == 0)
+    for (int r = r_first + tid; r < cnt; r += WARPS * 32) a.row_seg[lo + r] = e;
   const int wi = a.index ? a.index[e] : e;
   const bool none = wi < 0 || wi >= a.n_weights;
   if (none && wi != -1 && blockIdx.x == 0 && tid == 0) flag_error(a.err, MOE_DEVERR_EXPERT_ID);

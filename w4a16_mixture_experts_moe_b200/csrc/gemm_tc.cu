@@ -316,10 +316,9 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
 // Whether several segments share the n <= 16 rows from `row`; *first: the
 // segment of the first of them.
 __device__ __forceinline__ bool shared_block(const TcGemmArgs &a, int row, int n, int *first = nullptr) {
-  const int sg = first_segment(a.offsets, a.segs, (threadIdx.x & 1) ? row + n - 1 : row);
-  const int s0 = __shfl_sync(0xffffffffu, sg, 0);
+  const int s0 = a.row_seg[row];
   if (first) *first = s0;
-  return s0 != __shfl_sync(0xffffffffu, sg, 1);
+  return s0 != a.row_seg[row + n - 1];
 }
 
 // The adapters' part of a 16-row block that several segments share (a block
@@ -327,7 +326,7 @@ __device__ __forceinline__ bool shared_block(const TcGemmArgs &a, int row, int n
 __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, int n, int f, uint32_t (&v)[16]) {
   int s0;
   if (!shared_block(a, row, n, &s0)) return;
-  const int64_t r0 = a.delta_by_seg ? int64_t(min(s0 + 1, a.segs - 1)) * 16 : row;
+  const int64_t r0 = a.delta_by_seg ? int64_t(min(max(s0, 0), a.segs - 2) + 1) * 16 : row;
   const float *d = a.delta + r0 * a.M + min(f, a.M - 1);
   float add[16];
 #pragma unroll

@@ -93,8 +93,8 @@ struct ShrinkArgs {
   const int32_t *seg_offsets, *seg_adapter;
   const float *scale;
   int segs, n_adapters, T, C, rank;
-  int split;          // CTAs that share a row tile's segments
   uint16_t *out;      // [T][rank]
+  int32_t *row_seg;   // [T] the rows' segments, written for the launches behind (or nullptr)
   int32_t *err;
 };
 
@@ -143,11 +143,36 @@ __device__ __forceinline__ void stage_mma(float (&acc)[Cfg::MT][BJ / 8][4], uint
   }
 }
 
+// The unit-th piece of the rows that tiles of `rows` rows and segments cut out:
+// tile and segment starts, merged in order (equal ones: segments first), each
+// begin a piece, so there are at most tiles + segs of them and some are empty.
+// Returns the segment; the piece is rows [lo, hi) of one tile, whatever the
+// offsets hold.
+__device__ __forceinline__ int find_piece(const int32_t *off, int segs, int T, int rows, int unit, int &lo, int &hi) {
+  const int tiles = (T + rows - 1) / rows;
+  int s = max(0, unit - tiles), e = min(unit, segs);  // segment starts among the first `unit`
+  while (s < e) {
+    const int mid = (s + e) >> 1;
+    if (off[mid] <= (unit - 1 - mid) * rows) s = mid + 1; else e = mid;
+  }
+  int t = unit - s;
+  if (s < segs && (t >= tiles || off[s] <= t * rows)) {
+    lo = off[s++];
+  } else {
+    lo = t++ * rows;
+  }
+  lo = max(lo, (t - 1) * rows);
+  hi = min(min(off[s], t * rows), T);  // off[segs]: the end of the last
+  if (s < 1 || t < 1 || t > tiles) hi = lo;
+  return s - 1;
+}
+
 // out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]), z = x and P = lora_a, or
-// z = dy and P_a[j][c] = lora_b[a][c][j] (TRANS). A tile may hold several
-// segments: each CTA of the tile (blockIdx.y of `split`) takes every split-th
-// of them, runs the whole tile through that segment's adapter (rows are
-// independent) and stores the segment's rows.
+// z = dy and P_a[j][c] = lora_b[a][c][j] (TRANS). A CTA takes one segment's rows
+// of one tile: it runs the whole tile through that segment's adapter (rows are
+// independent) and stores the segment's rows. (A CTA per tile that went through
+// the tile's segments one by one took 192 us where 200 single rows precede 8000
+// of one segment, K = 4096, rank 16; this 32.)
 template <int BJ, bool TRANS, int ROWS>
 __global__ void __launch_bounds__(CONSUMERS + 32)
     shrink_kernel(const ShrinkArgs a, const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_p) {
@@ -161,94 +186,93 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   ring_init(ring, Cfg::STAGES);
   pdl_wait();     // in this order: the launches behind this one may start before u is there, but
   pdl_trigger();  // not before what this launch itself waits for
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
     for (int s = tid; s < a.segs; s += CONSUMERS + 32) {
       const int o0 = a.seg_offsets[s], o1 = a.seg_offsets[s + 1], ad = a.seg_adapter[s];
       if (o0 < 0 || o1 < o0 || o1 > a.T || (s == 0 && o0 != 0)) flag_error(a.err, MOE_DEVERR_OFFSETS);
       if (ad < -1 || ad >= a.n_adapters) flag_error(a.err, MOE_DEVERR_EXPERT_ID);
     }
   }
-  const int row0 = blockIdx.x * ROWS, row1 = min(row0 + ROWS, a.T), j0 = blockIdx.z * BJ;
+  const int j0 = blockIdx.y * BJ;
+  int lo, hi;
+  const int sg = find_piece(a.seg_offsets, a.segs, a.T, ROWS, blockIdx.x, lo, hi);
+  if (hi <= lo) return;
+  const int row0 = lo / ROWS * ROWS, ad = a.seg_adapter[sg];
+  if (a.row_seg && blockIdx.y == 0)
+    for (int p = tid; p < hi - lo; p += CONSUMERS + 32) a.row_seg[lo + p] = sg;
   const int nc = (a.C + Cfg::CC - 1) / Cfg::CC;
-  int turn = 0, slot = 0, round = 0;
+  int slot = 0, round = 0;
   bool ok = true;
-  for (int sg = first_segment(a.seg_offsets, a.segs, row0); sg < a.segs && ok; ++sg) {
-    const int o0 = a.seg_offsets[sg];
-    if (o0 >= row1) break;
-    const int lo = max(o0, row0), hi = min(a.seg_offsets[sg + 1], row1), ad = a.seg_adapter[sg];
-    if (hi <= lo || turn++ % a.split != int(blockIdx.y)) continue;
-    if (ad < 0 || ad >= a.n_adapters) {  // no adapter: nothing is added to these rows
-      if (warp < 8)
-        for (int p = tid; p < (hi - lo) * BJ; p += CONSUMERS)
-          if (j0 + p % BJ < a.rank) a.out[int64_t(lo + p / BJ) * a.rank + j0 + p % BJ] = 0;
-      continue;
-    }
-    if (warp == 8) {
-      for (int c = 0; c < nc; ++c) {
-        ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
-        if (!ok) break;
-        if (tma::elect_one()) {
-          uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
-          tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
+  if (ad < 0 || ad >= a.n_adapters) {  // no adapter: nothing is added to these rows
+    if (warp < 8)
+      for (int p = tid; p < (hi - lo) * BJ; p += CONSUMERS)
+        if (j0 + p % BJ < a.rank) a.out[int64_t(lo + p / BJ) * a.rank + j0 + p % BJ] = 0;
+    return;
+  }
+  if (warp == 8) {
+    for (int c = 0; c < nc; ++c) {
+      ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
+      if (!ok) break;
+      if (tma::elect_one()) {
+        uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+        tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
+#pragma unroll
+        for (int b = 0; b < Cfg::CC / 64; ++b)
+          tma::tma_load_2d(z + b * ROWS * 128, &tm_z, c * Cfg::CC + b * 64, row0, &ring.full[slot]);
+        if (TRANS) {
+          tma::tma_load_3d(p, &tm_p, j0, c * Cfg::CC, ad, &ring.full[slot]);
+        } else {
 #pragma unroll
           for (int b = 0; b < Cfg::CC / 64; ++b)
-            tma::tma_load_2d(z + b * ROWS * 128, &tm_z, c * Cfg::CC + b * 64, row0, &ring.full[slot]);
-          if (TRANS) {
-            tma::tma_load_3d(p, &tm_p, j0, c * Cfg::CC, ad, &ring.full[slot]);
-          } else {
-#pragma unroll
-            for (int b = 0; b < Cfg::CC / 64; ++b)
-              tma::tma_load_3d(p + b * BJ * 128, &tm_p, c * Cfg::CC + b * 64, j0, ad, &ring.full[slot]);
-          }
+            tma::tma_load_3d(p + b * BJ * 128, &tm_p, c * Cfg::CC + b * 64, j0, ad, &ring.full[slot]);
         }
-        __syncwarp();
-        if (++slot == Cfg::STAGES) { slot = 0; ++round; }
       }
-      continue;
-    }
-    const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
-    float acc[Cfg::MT][BJ / 8][4];
-#pragma unroll
-    for (int i = 0; i < Cfg::MT; ++i)
-#pragma unroll
-      for (int j = 0; j < BJ / 8; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-    for (int c = 0; c < nc; ++c) {
-      ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
-      if (!ok) break;
-      stage_mma<Cfg, BJ, TRANS, ROWS>(acc, ring0 + slot * Cfg::STAGE, rw, kw);
       __syncwarp();
-      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
       if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
-    // the KW partial sums, added in a fixed order
+    return;
+  }
+  const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
+  float acc[Cfg::MT][BJ / 8][4];
 #pragma unroll
-    for (int i = 0; i < Cfg::MT; ++i)
+  for (int i = 0; i < Cfg::MT; ++i)
 #pragma unroll
-      for (int j = 0; j < BJ / 8; ++j)
+    for (int j = 0; j < BJ / 8; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          red[(kw * ROWS + (rw * Cfg::MT + i) * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[i][j][q];
-    consumer_sync();
-    const float sc = a.scale ? a.scale[ad] : 1.f;
-    for (int p = tid; p < (hi - lo) * (BJ / 2); p += CONSUMERS) {
-      const int r = lo - row0 + p / (BJ / 2), jj = p % (BJ / 2) * 2;
-      if (j0 + jj >= a.rank) continue;
-      float v0 = 0.f, v1 = 0.f;
+      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
+  for (int c = 0; c < nc; ++c) {
+    ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
+    if (!ok) break;
+    stage_mma<Cfg, BJ, TRANS, ROWS>(acc, ring0 + slot * Cfg::STAGE, rw, kw);
+    __syncwarp();
+    if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+    if (++slot == Cfg::STAGES) { slot = 0; ++round; }
+  }
+  // the KW partial sums, added in a fixed order
 #pragma unroll
-      for (int k = 0; k < Cfg::KW; ++k) {
-        v0 += red[(k * ROWS + r) * (BJ + 1) + jj];
-        v1 += red[(k * ROWS + r) * (BJ + 1) + jj + 1];
-      }
-      *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = pack_bf16x2(v0 * sc, v1 * sc);
+  for (int i = 0; i < Cfg::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < BJ / 8; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[(kw * ROWS + (rw * Cfg::MT + i) * 16 + g + (q >> 1) * 8) * (BJ + 1) + j * 8 + 2 * t4 + (q & 1)] = acc[i][j][q];
+  consumer_sync();
+  const float sc = a.scale ? a.scale[ad] : 1.f;
+  for (int p = tid; p < (hi - lo) * (BJ / 2); p += CONSUMERS) {
+    const int r = lo - row0 + p / (BJ / 2), jj = p % (BJ / 2) * 2;
+    if (j0 + jj >= a.rank) continue;
+    float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < Cfg::KW; ++k) {
+      v0 += red[(k * ROWS + r) * (BJ + 1) + jj];
+      v1 += red[(k * ROWS + r) * (BJ + 1) + jj + 1];
     }
-    consumer_sync();
+    *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = pack_bf16x2(v0 * sc, v1 * sc);
   }
 }
 
 struct DeltaArgs {
-  const int32_t *seg_offsets, *seg_adapter;
+  const int32_t *seg_offsets, *seg_adapter, *row_seg;
   const uint16_t *u, *w;  // u / du [T][rank]; lora_b [n][M][rank], or lora_a [n][rank][M] (COLS)
   int segs, n_adapters, T, rank, M, by_seg;
   float *delta;
@@ -256,14 +280,128 @@ struct DeltaArgs {
 
 // The adapters' part of the 16-row blocks that several segments share, as fp32
 // rows for the projection's epilogue: delta[j][f] = u[row j] . w_a[f], row j's
-// own adapter a. Few segments: a CTA does 128 columns of one block, found by
-// its owning segment; a thread loads its column of the adapter once for the rows
-// that share it, and all CTAs run at once (13 segments, rank 64, N = 4096: one
-// wave instead of two and a half with four rows a CTA). Many segments: all
-// blocks, four rows a CTA, since each row waits for another adapter's loads.
-// A pass takes CH ranks: the thread's column of the adapter in CH registers, a
-// running sum per row.
-template <bool COLS, int CH>
+// own adapter a. A CTA does 128 threads' columns of one block, which it finds by
+// the block's owning segment where segments are few, or by its number.
+// Latency bounds it, not the bytes: the rows' segments come as a list from the
+// launch before (a search in the offsets takes log2(segs) loads, one after the
+// other, in every CTA), and a thread has the loads of two or four rows, each another
+// request's perhaps, in flight at once; rows of one segment share them. (200
+// single rows before 8000 of one segment, rank 64, N = 4096: 27 us, 50 with a
+// search and one row's loads at a time; 256 single rows, rank 16: 22 -> 9.)
+//
+// lora_a's columns f are neighbours in memory: a thread takes two, all ranks.
+// lora_b has a column's ranks in a row: G lanes (G 8 >= rank) take 8 each, G
+// loads fetch 32 columns a warp, and the lanes' sums are exchanged so that each
+// lane ends with one column's.
+constexpr int DELTA_COLS = 128;  // columns a CTA, twice as many of lora_a
+
+template <int G>
+__device__ __forceinline__ void delta_rows(const DeltaArgs &a, const float (*us)[MAX_RANK], const int *ads, int n, float *out) {
+  constexpr int CW = 32 / G, RB = G <= 4 ? 4 : 2;  // columns a load; rows in flight
+  const int lane = threadIdx.x & 31, gl = lane % G, c0 = blockIdx.x * DELTA_COLS + (threadIdx.x >> 5) * 32, own = c0 + gl * CW + lane / G;
+  const bool in_rank = gl * 8 < a.rank;
+  for (int g = 0; g < n; g += RB) {
+    uint4 q[RB][G];
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      const int ad = ads[g + j];
+      if (ad < 0 || (j > 0 && ad == ads[g + j - 1])) continue;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int col = c0 + i * CW + lane / G;
+        q[j][i] = in_rank && col < a.M
+                      ? *reinterpret_cast<const uint4 *>(a.w + (int64_t(ad) * a.M + col) * a.rank + gl * 8)
+                      : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+      if (g + j >= n) break;
+      float v[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) v[i] = 0.f;
+      if (ads[g + j] >= 0) {
+        if (j > 0 && ads[g + j] == ads[g + j - 1]) {
+#pragma unroll
+          for (int i = 0; i < G; ++i) q[j][i] = q[j - 1][i];
+        }
+        const float4 y0 = *reinterpret_cast<const float4 *>(&us[g + j][gl * 8]);
+        const float4 y1 = *reinterpret_cast<const float4 *>(&us[g + j][gl * 8 + 4]);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const uint4 w = q[j][i];
+          float d = bf16_lo(w.x) * y0.x;
+          d = fmaf(bf16_hi(w.x), y0.y, d); d = fmaf(bf16_lo(w.y), y0.z, d); d = fmaf(bf16_hi(w.y), y0.w, d);
+          d = fmaf(bf16_lo(w.z), y1.x, d); d = fmaf(bf16_hi(w.z), y1.y, d);
+          d = fmaf(bf16_lo(w.w), y1.z, d); d = fmaf(bf16_hi(w.w), y1.w, d);
+          v[i] = d;
+        }
+#pragma unroll
+        for (int h = G / 2; h > 0; h >>= 1)
+#pragma unroll
+          for (int k = 0; k < h; ++k) {
+            const bool up = gl & h;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + h], h);
+            v[k] = (up ? v[k + h] : v[k]) + got;
+          }
+      }
+      if (own < a.M) out[int64_t(g + j) * a.M + own] = v[0];
+    }
+  }
+}
+
+__device__ __forceinline__ void delta_cols(const DeltaArgs &a, const float (*us)[MAX_RANK], const int *ads, int n, float *out) {
+  constexpr int CH = 16;  // ranks a pass
+  const int f = (blockIdx.x * DELTA_COLS + threadIdx.x) * 2;
+  if (f >= a.M) return;
+  for (int g = 0; g < n; g += 4) {
+    float acc[4][2];
+    int ad[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ad[j] = ads[g + j];  // -1 behind the rows
+      acc[j][0] = acc[j][1] = 0.f;
+    }
+    for (int i0 = 0; i0 < a.rank; i0 += CH) {
+      uint32_t q[4][CH];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (ad[j] < 0 || (j > 0 && ad[j] == ad[j - 1])) continue;
+#pragma unroll
+        for (int i = 0; i < CH; i += 8) {
+          const bool in = i0 + i < a.rank;
+          const uint16_t *c = a.w + (int64_t(ad[j]) * a.rank + i0 + i) * a.M + f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[j][i + k] = in ? *reinterpret_cast<const uint32_t *>(c + int64_t(k) * a.M) : 0u;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (ad[j] < 0) continue;
+        if (j > 0 && ad[j] == ad[j - 1]) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) q[j][i] = q[j - 1][i];
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i += 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(&us[g + j][i0 + i]);
+          const float yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[j][0] = fmaf(bf16_lo(q[j][i + k]), yv[k], acc[j][0]);
+            acc[j][1] = fmaf(bf16_hi(q[j][i + k]), yv[k], acc[j][1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (g + j < n) *reinterpret_cast<float2 *>(out + int64_t(g + j) * a.M + f) = make_float2(acc[j][0], acc[j][1]);
+  }
+}
+
+// G: see delta_rows; 0: lora_a.
+template <int G>
 __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
   __shared__ __align__(16) float us[16][MAX_RANK];
   __shared__ int ads[16];
@@ -277,74 +415,25 @@ __global__ void __launch_bounds__(128) delta_kernel(const DeltaArgs a) {
     if (o <= 0 || o == row || o >= end || (s > 0 && a.seg_offsets[s - 1] > row)) return;
   } else {
     row = blockIdx.y * 16;
-    if (row >= end || first_segment(a.seg_offsets, a.segs, row) ==
-                          first_segment(a.seg_offsets, a.segs, min(row + 15, end - 1)))
-      return;
+    if (row >= end || a.row_seg[row] == a.row_seg[min(row + 15, end - 1)]) return;
   }
   const int per = 16 / gridDim.z, j0 = blockIdx.z * per, n = min(per, end - row - j0);  // this CTA's rows: row + j0 ...
   if (n <= 0) return;
   float *out = a.delta + (a.by_seg ? int64_t(blockIdx.y) * 16 : int64_t(row)) * a.M + int64_t(j0) * a.M;
   row += j0;
-  if (tid < n) {
-    const int sg = first_segment(a.seg_offsets, a.segs, row + tid);
-    int ad = sg < a.segs && a.seg_offsets[sg] <= row + tid ? a.seg_adapter[sg] : -1;
-    if (ad >= a.n_adapters) ad = -1;
-    ads[tid] = ad;
+  if (tid < 16) {
+    const int sg = tid < n ? a.row_seg[row + tid] : -1;
+    const int ad = sg >= 0 && sg < a.segs ? a.seg_adapter[sg] : -1;
+    ads[tid] = ad < a.n_adapters ? ad : -1;
   }
-  const int width = (a.rank + CH - 1) / CH * CH;  // whole passes, zeros behind the rank
+  const int width = G ? G * 8 : (a.rank + 15) & ~15;  // whole passes, zeros behind the rank
   for (int p = tid; p < n * width; p += 128) {
     const int j = p / width, i = p % width;
     us[j][i] = i < a.rank ? bf16_to_f(a.u[int64_t(row + j) * a.rank + i]) : 0.f;
   }
   __syncthreads();
-  const int f = blockIdx.x * 128 + tid;
-  if (f >= a.M) return;
-  float acc[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  for (int i0 = 0; i0 < a.rank; i0 += CH) {
-    float w[CH];
-    int prev = -1;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j >= n) break;
-      const int ad = ads[j];
-      if (ad < 0) continue;
-      if (ad != prev) {
-        prev = ad;
-#pragma unroll
-        for (int i = 0; i < CH; i += 8) {
-          uint32_t q[4] = {0, 0, 0, 0};
-          if (i0 + i < a.rank) {
-            if (COLS) {
-              const uint16_t *c = a.w + (int64_t(ad) * a.rank + i0 + i) * a.M + f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) q[k] = c[int64_t(2 * k) * a.M] | uint32_t(c[int64_t(2 * k + 1) * a.M]) << 16;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4 *>(a.w + (int64_t(ad) * a.M + f) * a.rank + i0 + i);
-              q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[i + 2 * k] = bf16_lo(q[k]);
-            w[i + 2 * k + 1] = bf16_hi(q[k]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < CH; i += 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(&us[j][i0 + i]);
-        acc[j] = fmaf(w[i], y.x, acc[j]);
-        acc[j] = fmaf(w[i + 1], y.y, acc[j]);
-        acc[j] = fmaf(w[i + 2], y.z, acc[j]);
-        acc[j] = fmaf(w[i + 3], y.w, acc[j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < n) out[int64_t(j) * a.M + f] = acc[j];
+  if constexpr (G == 0) delta_cols(a, us, ads, n, out);
+  else delta_rows<G>(a, us, ads, n, out);
 }
 
 struct ProjArgs {
@@ -695,7 +784,7 @@ struct Rows {
 };
 
 template <int BJ, bool TRANS, int ROWS>
-static int launch_shrink_as(ShrinkArgs a, const Rows &z, const uint16_t *p, cudaStream_t s, const char *what) {
+static int launch_shrink_as(const ShrinkArgs &a, const Rows &z, const uint16_t *p, cudaStream_t s, const char *what) {
   using Cfg = ShrinkCfg<BJ, TRANS, ROWS>;
   CUtensorMap tz, tp;
   bool ok = map_bf16(&tz, z.p, 2, {z.width, a.T, 1, 1}, {z.ld, 0, 0}, {64, ROWS, 1, 1});
@@ -706,12 +795,7 @@ static int launch_shrink_as(ShrinkArgs a, const Rows &z, const uint16_t *p, cuda
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, ROWS>), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
-  // as many CTAs per row tile as it holds segments on average, and one more:
-  // a tile with a boundary inside does not run twice as long (a CTA without a
-  // segment leaves at once)
-  const int64_t per = (int64_t(a.segs) * ROWS + a.T - 1) / a.T + (a.segs > 1 ? 1 : 0);
-  a.split = int(per < 1 ? 1 : per > ROWS ? ROWS : per);
-  const dim3 grid(unsigned((a.T + ROWS - 1) / ROWS), unsigned(a.split), unsigned((a.rank + BJ - 1) / BJ));
+  const dim3 grid(unsigned((a.T + ROWS - 1) / ROWS) + unsigned(a.segs), unsigned((a.rank + BJ - 1) / BJ));
   const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS, ROWS>, grid, dim3(CONSUMERS + 32), Cfg::SMEM, s, a, tz, tp);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
@@ -775,13 +859,27 @@ static int launch_proj(const ProjArgs &a, const Rows &z, const uint16_t *w, cuda
                      : launch_proj_as<TRANS, 64>(a, z, w, s, what);
 }
 
-template <bool COLS>
-static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
-  const dim3 grid(unsigned((a.M + 127) / 128), unsigned(a.by_seg ? a.segs : (a.T + 15) / 16), a.by_seg ? 1u : 4u);
-  const cudaError_t e = a.rank <= 16 ? launch_pdl(delta_kernel<COLS, 16>, grid, dim3(128), 0, s, a)
-                                     : launch_pdl(delta_kernel<COLS, 64>, grid, dim3(128), 0, s, a);
+template <int G>
+static int launch_delta_as(const DeltaArgs &a, cudaStream_t s, const char *what) {
+  constexpr int cols = G ? DELTA_COLS : 2 * DELTA_COLS;
+  // Four CTAs a block, unless lora_b's blocks alone are eight rounds of the SMs,
+  // most of them owned by no segment (forward, rank 16, N = 4096, T = 8000: 400
+  // segments 278 us with four, 248 with one; rank 128, 16 segments 223 and 230).
+  const unsigned x = unsigned((a.M + cols - 1) / cols), y = unsigned(a.by_seg ? a.segs : (a.T + 15) / 16);
+  const dim3 grid(x, y, a.by_seg && G && int64_t(x) * y > 8 * sm_count() ? 1u : 4u);
+  const cudaError_t e = launch_pdl(delta_kernel<G>, grid, dim3(128), 0, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
+}
+
+template <bool COLS>
+static int launch_delta(const DeltaArgs &a, cudaStream_t s, const char *what) {
+  return COLS            ? launch_delta_as<0>(a, s, what)
+         : a.rank <= 8   ? launch_delta_as<1>(a, s, what)
+         : a.rank <= 16  ? launch_delta_as<2>(a, s, what)
+         : a.rank <= 32  ? launch_delta_as<4>(a, s, what)
+         : a.rank <= 64  ? launch_delta_as<8>(a, s, what)
+                         : launch_delta_as<16>(a, s, what);
 }
 
 template <int RJ, int AG_ROWS>
@@ -826,6 +924,11 @@ static size_t delta_rows(int T, int S) {
   if (T < 1 || S < 2) return 0;
   const size_t by_seg = size_t(S) * 16, by_row = (size_t(T) + 15) / 16 * 16;
   return by_seg < by_row ? by_seg : by_row;
+}
+
+// The rows' segments, behind those sums.
+static int32_t *row_segments(int T, int S, int N, int K, void *ws) {
+  return reinterpret_cast<int32_t *>(static_cast<char *>(ws) + WS_HEADER + delta_rows(T, S) * size_t(N > K ? N : K) * 4);
 }
 
 // The arguments both entry points share.
@@ -913,11 +1016,12 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
 // Launches the sums of the blocks that several segments share and points the
 // projection at them (one segment shares no block).
 template <bool COLS>
-static int shared_blocks(TcGemmArgs &g, int T, int S, void *ws, cudaStream_t s, const char *what) {
+static int shared_blocks(TcGemmArgs &g, int T, int S, int N, int K, void *ws, cudaStream_t s, const char *what) {
   if (S < 2) return MOE_OK;
   g.delta = reinterpret_cast<const float *>(static_cast<char *>(ws) + WS_HEADER);
   g.delta_by_seg = int64_t(S) * 16 < (int64_t(T) + 15) / 16 * 16;
-  const DeltaArgs d = {g.offsets, g.adapter, g.ext_b, g.ext_a, S, g.n_adapters, T, g.rank, g.M, g.delta_by_seg,
+  g.row_seg = row_segments(T, S, N, K, ws);
+  const DeltaArgs d = {g.offsets, g.adapter, g.row_seg, g.ext_b, g.ext_a, S, g.n_adapters, T, g.rank, g.M, g.delta_by_seg,
                        const_cast<float *>(g.delta)};
   return launch_delta<COLS>(d, s, what);
 }
@@ -927,7 +1031,7 @@ static int shared_blocks(TcGemmArgs &g, int T, int S, void *ws, cudaStream_t s, 
 
 extern "C" size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K) {
   (void)n_adapters; (void)rank;
-  return moe::WS_HEADER + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4;
+  return moe::WS_HEADER + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4 + (T < 1 || S < 2 ? 0 : size_t(T) * 4);
 }
 
 extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w, const int32_t *seg_offsets,
@@ -945,18 +1049,23 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     return st;
   cudaStream_t s = as_stream(stream);
   int32_t *err = static_cast<int32_t *>(ws);
+  const bool engine = T > lora::GEMV_MAX_T && !lora::use_proj(T, N, K);
+  int32_t *row_seg = engine && S > 1 ? lora::row_segments(T, S, N, K, ws) : nullptr;
 
-  if (T <= lora::GEMV_MAX_T || T < 16 * int64_t(S)) {
-    // short segments: each streams its adapter's A
+  if (T <= lora::GEMV_MAX_T || (rank <= 16 && T < 4 * int64_t(S))) {
+    // short segments of small rank: each streams its adapter's A (whole call,
+    // 256 single rows, K = N = 2048: rank 16 21 us against the shrink kernel's
+    // 23.5, rank 64 39; 250 rows behind 99 single ones, rank 64: 36 against 27)
     GemvArgs v = {};
     v.in = x; v.ldi = ldx; v.offsets = seg_offsets; v.index = seg_adapter;
     v.w = lora_a; v.w_stride = int64_t(rank) * K;
     v.groups = S; v.n_weights = n_adapters; v.R = T; v.N = rank; v.K = K;
     v.scale = scale; v.out = u; v.ldo = rank; v.err = err;
     v.split = GEMV_LATER_PASSES;
+    v.row_seg = row_seg;
     st = launch_gemm_gemv(v, s, "moe_lora_linear (adapters)");
   } else {
-    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, 1, u, err};
+    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, u, row_seg, err};
     st = lora::launch_shrink<false>(h, {x, ldx, K}, lora_a, s, "moe_lora_linear (adapters)");
   }
   if (st != MOE_OK) return st;
@@ -968,14 +1077,14 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.u = u; v.lora_b = lora_b;
     return launch_gemm_gemv(v, s, who);
   }
-  if (lora::use_proj(T, N, K)) {
+  if (!engine) {
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, K, N, rank, u, lora_b, y, ldy, err};
     return lora::launch_proj<false>(v, {x, ldx, K}, w, s, who);
   }
   TcGemmArgs g = lora::projection(GEMM_FWD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, y, ldy, err);
   g.ext_a = lora_b;
   g.ext_b = u;
-  if ((st = lora::shared_blocks<false>(g, T, S, ws, s, "moe_lora_linear (shared blocks)")) != MOE_OK) return st;
+  if ((st = lora::shared_blocks<false>(g, T, S, N, K, ws, s, "moe_lora_linear (shared blocks)")) != MOE_OK) return st;
   const TcGemmOperands op = {w, x, K, int64_t(N) * K, ldx};
   return launch_gemm_tc(GEMM_FWD, g, op, s, who);
 }
@@ -1009,15 +1118,15 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
                     (st = lora::check_rows(who, "u", u, rank, rank)) != MOE_OK)))
     return st;
   int32_t *err = static_cast<int32_t *>(ws);
-  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, 1, du, err};
-  if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
   const bool engine = dx && !lora::use_proj(T, K, N);
+  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, du, engine && S > 1 ? lora::row_segments(T, S, N, K, ws) : nullptr, err};
+  if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
   TcGemmArgs g = {};
   if (engine) {
     g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
     g.ext_a = lora_a;
     g.ext_b = du;
-    if ((st = lora::shared_blocks<true>(g, T, S, ws, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
+    if ((st = lora::shared_blocks<true>(g, T, S, N, K, ws, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
   }
   // The engine goes behind the adapters' gradients: it starts while they end and
   // waits for them only in its epilogue (six adapters of rank 16 at T = 2041, one
