@@ -428,7 +428,8 @@ int moe_combine(const float *y, const float *topk_w,
 
 /*
  * Synchronises `stream`, reads the device error word of a workspace written
- * by moe_group_tokens or moe_grouped_w4a16_ffn, clears it, and returns
+ * by moe_group_tokens, moe_grouped_w4a16_ffn, a moe_grouped_gemm* or a
+ * moe_lora_linear* call, clears it, and returns
  * MOE_OK or MOE_ERR_DEVICE (the code is stored in *code if code != NULL).
  */
 int moe_read_device_error(void *ws, moe_stream_t stream, int32_t *code);

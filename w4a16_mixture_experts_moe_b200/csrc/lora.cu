@@ -10,7 +10,8 @@
 // u and du are rounded to BF16 once: they are operands of the BF16 matrix
 // instructions that follow, and the adapter's part is a small share of y, so
 // the rounding (at most 2^-8 relative, independent from value to value) stays
-// below y's own.
+// below y's own. dA and dB, which they enter alone, carry that half step beside
+// their own.
 //
 // The small-rank products read each row of x (dy) once and do 2 rank
 // operations per value: at rank 64 that is 64 operations a byte, far below the
