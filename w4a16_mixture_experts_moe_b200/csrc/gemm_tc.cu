@@ -73,8 +73,11 @@ constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the outp
 // 4096 rows of 1024; at 32 steps a part 2e-6 and 124 us).
 constexpr int F32_WHOLE = 16, F32_STEPS = 14;
 constexpr int OUT_ROWS = 32;       // output rows per staged store
-constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // one per half of the epilogue warps
-constexpr int SMEM = STAGES * STAGE_BYTES + 2 * OUT_BYTES + 1024 /*align*/ + 4096 /*Shared*/;
+constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // of the four epilogue warps of a half
+// Each half has two staging buffers: with one, every 32 rows wait for the store
+// before them to have been read (BF16 gradients of 8 experts of 64 rows, K = 4096,
+// N = 14336: 238 -> 189 us; 64 experts of 256 rows, K = 2048, N = 1024: 94 -> 76).
+constexpr int SMEM = STAGES * STAGE_BYTES + 4 * OUT_BYTES + 3072 /*Shared*/;
 constexpr int OUT_BAR = 2;         // named barriers 2, 3: the four epilogue warps that share a staging buffer
 
 // One k-step, written by the first CTA's producer for its waiter.
@@ -96,11 +99,14 @@ struct Shared {
   uint32_t tmem_base;
   int32_t abort;
   int32_t total;
-  int32_t lo[MAX_E], cnt[MAX_E];
-  int32_t tstart[MAX_E + 1];  // first tile of each group (fwd, dgrad)
-  int16_t order[MAX_E];       // groups by falling row count (wgrad)
+  int32_t lo[MAX_E + 1];        // the groups' first rows
+  union {
+    int32_t tstart[MAX_E + 1];  // first tile of each group (fwd, dgrad)
+    int16_t order[MAX_E];       // groups by falling row count (wgrad)
+  };
+  __device__ __forceinline__ int cnt(int e) const { return max(0, lo[e + 1] - lo[e]); }  // rows of group e
 };
-static_assert(sizeof(Shared) <= 4096, "shared tables budget");
+static_assert(sizeof(Shared) <= 3072, "shared tables budget");
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -299,7 +305,7 @@ __device__ __forceinline__ Tile decode_tile(const Shared &sh, const TcGemmArgs &
       const int mid = (lo_e + hi_e) >> 1;
       if (sh.tstart[mid] <= t) lo_e = mid; else hi_e = mid;
     }
-    const int cnt = sh.cnt[lo_e], idx = t - sh.tstart[lo_e];
+    const int cnt = sh.cnt(lo_e), idx = t - sh.tstart[lo_e];
     const int rt = (cnt + a.bn - 1) / a.bn;
     const int w = ((cnt + rt - 1) / rt + 15) & ~15;
     const int blk = idx / (ROW_BLOCK * FT), rem = idx - blk * ROW_BLOCK * FT;
@@ -383,6 +389,10 @@ __device__ __forceinline__ void store_block(const TcGemmArgs &a, int64_t at, int
 // The map of B for `half` rows per CTA: boxes of 32, 64, 128 rows.
 __device__ __forceinline__ int row_box(int half) { return half <= 32 ? 0 : half <= 64 ? 1 : 2; }
 
+// Adapters join the two directions of a projection, whose outputs are BF16.
+template <int MODE, bool F32>
+constexpr bool ADAPTERS = MODE != GEMM_WGRAD && !F32;
+
 // The pair's i-th tile, in a snake over the pairs.
 __device__ __forceinline__ int sched_pos(int i) {
   const int G = int(gridDim.x) >> 1, c = int(blockIdx.x) >> 1;
@@ -413,17 +423,17 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
     const Tile tl = decode_tile<MODE>(sh, a, t);
     const int n16 = (tl.nvalid + 15) >> 4, half = n16 * 8;  // rows (wgrad: columns of dy) per CTA
     const int f = tl.f0 + int(rank) * BMC, r0 = tl.row + int(rank) * half;
-    const int red = MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD;
+    const int red = MODE == GEMM_WGRAD ? sh.cnt(tl.e) : a.KD;
     const int nsteps = MODE == GEMM_WGRAD && red == 0 ? 1 : (red + BK - 1) / BK;
     const int box = row_box(half), nb = (half + 63) >> 6;  // B's map; wgrad: 64-column blocks of B
     const int b_bytes = MODE == GEMM_WGRAD ? nb * 8192 : (32 << box) * BK * 2;
     // adapters: the next segment that has one and covers whole 16-row blocks of
     // the tile; the lanes look at 32 segments at a time
     const int lane = threadIdx.x & 31, tile_end = tl.row + tl.nvalid;
-    int sg = MODE != GEMM_WGRAD && a.adapter ? first_segment(a.offsets, a.segs, tl.row) : 0;
+    int sg = ADAPTERS<MODE, F32> && a.adapter ? first_segment(a.offsets, a.segs, tl.row) : 0;
     int my_lo = 0, my_hi = 0, my_a = -1, seg_lo = 0, seg_hi = 0, seg_a = -1;
     uint32_t found = 0;
-    bool end = MODE == GEMM_WGRAD || !a.adapter;
+    bool end = !ADAPTERS<MODE, F32> || !a.adapter;
     auto next_seg = [&]() {
       while (found == 0) {
         if (end) return false;
@@ -448,7 +458,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
     int part = 0, part_end = part_start(nsteps, parts, 1);
     bool part_first = true;
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
-      if (ks + 1 == nsteps) { more = next_seg(); known = true; }
+      if (ADAPTERS<MODE, F32> && ks + 1 == nsteps) { more = next_seg(); known = true; }
       const bool part_last = ks + 1 == (F32 ? part_end : nsteps);
       uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
       const int left = min(BK, red - ks * BK);
@@ -500,7 +510,7 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       part_first = F32 && part_last;
       if (F32 && part_last) part_end = part_start(nsteps, parts, ++part + 1);
     }
-    if constexpr (MODE != GEMM_WGRAD) {
+    if constexpr (ADAPTERS<MODE, F32>) {
       if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
       while (known && more && ok) {
         const int col = seg_lo, w16 = (seg_hi - seg_lo) >> 4, whalf = w16 * 8, ad = seg_a;
@@ -552,9 +562,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
 template <int MODE, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gemm_kernel(const TcGemmArgs a, const __grid_constant__ Maps m) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES + 2 * OUT_BYTES);
+  extern __shared__ __align__(1024) uint8_t smem[];  // all of the block's shared memory: swizzled tiles first
+  Shared &sh = *reinterpret_cast<Shared *>(smem + STAGES * STAGE_BYTES + 4 * OUT_BYTES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int FT = (a.M + 2 * BMC - 1) / (2 * BMC);
@@ -582,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // With adapters (`late`) only their k-steps and the epilogue need the launches
   // before this one; those wait, before they let this kernel start, for all that
   // it reads until then.
-  if (MODE == GEMM_WGRAD || !a.late) pdl_wait();
+  if (!ADAPTERS<MODE, F32> || !a.late) pdl_wait();
   if (warp == 0) {
     int v[8], local = 0;
     bool bad = false;
@@ -591,12 +600,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int e = lane * 8 + i;
       v[i] = 0;
       if (e < a.groups) {
-        const int o0 = a.adapter ? 0 : a.offsets[e], o1 = a.adapter ? a.offsets[a.segs] : a.offsets[e + 1];
+        const bool segs = ADAPTERS<MODE, F32> && a.adapter;
+        const int o0 = segs ? 0 : a.offsets[e], o1 = a.offsets[segs ? a.segs : e + 1];
         bad |= o0 < 0 || o1 < o0 || o1 > a.R;
-        const int lo = min(max(o0, 0), a.R), cnt = max(0, min(max(o1, 0), a.R) - lo);
+        const int lo = min(max(o0, 0), a.R), hi = min(max(o1, 0), a.R);
         sh.lo[e] = lo;
-        sh.cnt[e] = cnt;
-        v[i] = (cnt + a.bn - 1) / a.bn * FT;
+        if (e == a.groups - 1) sh.lo[e + 1] = hi;
+        v[i] = (max(0, hi - lo) + a.bn - 1) / a.bn * FT;
       }
       local += v[i];
     }
@@ -611,20 +621,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane * 8 + i;
-      if (e < a.groups) sh.tstart[e] = run;
+      if (MODE != GEMM_WGRAD && e < a.groups) sh.tstart[e] = run;
       run += v[i];
     }
     if (lane == 31) {
-      sh.tstart[a.groups] = incl;
+      if (MODE != GEMM_WGRAD) sh.tstart[a.groups] = incl;
       sh.total = MODE == GEMM_WGRAD ? a.groups * FT * ((a.NC + BN - 1) / BN) : incl;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (MODE == GEMM_WGRAD && tid < a.groups) {
-    const int mine = sh.cnt[tid];
+    const int mine = sh.cnt(tid);
     int r = 0;
-    for (int e = 0; e < a.groups; ++e) r += sh.cnt[e] > mine || (sh.cnt[e] == mine && e < tid);
+    for (int e = 0; e < a.groups; ++e) r += sh.cnt(e) > mine || (sh.cnt(e) == mine && e < tid);
     sh.order[r] = int16_t(tid);
   }
   __syncthreads();
@@ -637,14 +647,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ================================================================ epilogue
     const int q = warp & 3, part = warp >> 2;
     const bool issuer = q == 0 && lane == 0;
-    const uint32_t out_buf = smem_u32(smem + STAGES * STAGE_BYTES + part * OUT_BYTES);
-    if (MODE != GEMM_WGRAD && a.late) pdl_wait();
+    const uint32_t out_bufs = smem_u32(smem + STAGES * STAGE_BYTES + part * 2 * OUT_BYTES);
+    uint32_t stores = 0;
+    if (ADAPTERS<MODE, F32> && a.late) pdl_wait();
     bool ok = true;
     for (int i = 0, unit = 0; ok; ++i) {  // unit & 1: the accumulator
       const int t = sched_pos(i);
       if (t >= total) break;
       const Tile tl = decode_tile<MODE>(sh, a, t);
-      const int parts = reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt[tl.e] : a.KD) + BK - 1) / BK);
+      const int parts = reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt(tl.e) : a.KD) + BK - 1) / BK);
       for (int p = 0; p < parts; ++p, ++unit) {
         const bool add = F32 && (p > 0 || a.accumulate);
         const int b = unit & 1;
@@ -652,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const int fw = tl.f0 + int(rank) * BMC + q * 32, f = fw + lane;
-        const bool zero = MODE == GEMM_WGRAD && sh.cnt[tl.e] == 0;  // no rows: the gradient is zero, no MMA ran
+        const bool zero = MODE == GEMM_WGRAD && sh.cnt(tl.e) == 0;  // no rows: the gradient is zero, no MMA ran
         const int64_t base = (MODE == GEMM_WGRAD ? int64_t(tl.e) * a.out_gstride : 0) + int64_t(tl.row) * a.ldo + f;
         const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + b * BN;
         // accumulator columns j0 .. j0 + 15, row by row from registers
@@ -664,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int j = 0; j < 16; ++j) v[j] = 0;
           }
           const int n = min(16, tl.nvalid - j0);
-          if (MODE != GEMM_WGRAD && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
+          if (ADAPTERS<MODE, F32> && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
           store_block<F32>(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
         };
         if (zero && add) {
@@ -674,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
           const int rows = min(OUT_ROWS, tl.nvalid - j0);
           if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
-              !(MODE != GEMM_WGRAD && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
+              !(ADAPTERS<MODE, F32> && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
             // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
             // warps write 128 columns of them to shared memory, one thread sends
             // them off
@@ -684,7 +695,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) x[j] = y[j] = 0;
             }
-            if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            // (the store before the last one has been read)
+            if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            const uint32_t out_buf = out_bufs + (stores++ & 1) * OUT_BYTES;
             out_sync(part);
             const int piece = q * 4 + (lane >> 3);  // 8 columns
 #pragma unroll
@@ -729,7 +742,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int t = sched_pos(i);
         if (t >= total) break;
         const Tile tl = decode_tile<MODE>(sh, a, t);
-        const int red = sh.cnt[tl.e], left = red & 15;
+        const int red = sh.cnt(tl.e), left = red & 15;
         it += red > 0 ? (red + BK - 1) / BK : 1;
         if (left == 0) continue;
         const int s = (it - 1) % STAGES;
