@@ -398,3 +398,49 @@ def test_captured_replayed_and_equal_bits(M, lens, N, K):
     p.backward(M, ws)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(keep, (p.u, p.y, p.dx, p.da, p.db)))
+
+
+def test_calls_on_several_streams_at_once(M):
+    """Calls that overlap, each with a workspace of its own, directly and from
+    graphs: the bits of the same calls made one by one."""
+    probs = [Problem([1] * 60 + [900], [i % 6 - 1 for i in range(61)], 5, 64, 1032, 1040, seed=1),
+             Problem([700, 3, 801], [1, -1, 0], 2, 16, 1040, 1032, seed=2),
+             Problem([1] * 40, [i % 8 for i in range(40)], 8, 16, 1032, 1040, seed=3)]
+    outs, refs, spaces, streams, graphs = [], [], [], [torch.cuda.Stream() for _ in probs], []
+
+    def step(p, ws, stream=None):
+        p.forward(M, ws, stream)
+        p.backward(M, ws, stream)
+
+    for p in probs:
+        p.strided()
+        spaces.append(p.workspace(M))
+        step(p, spaces[-1])
+        torch.cuda.synchronize()
+        outs.append([p.u, p.y, p.du, p.dx, p.da, p.db])
+        refs.append([t.clone() for t in outs[-1]])
+
+    def check():
+        torch.cuda.synchronize()
+        for out, ref, ws in zip(outs, refs, spaces):
+            assert M.moe_read_device_error(ws) == 0
+            assert all(torch.equal(t, q) for t, q in zip(out, ref))
+            for t in out:
+                t.fill_(3.0)
+        torch.cuda.synchronize()
+
+    check()
+    for _ in range(5):
+        for p, ws, s in zip(probs, spaces, streams):
+            step(p, ws, s.cuda_stream)
+        check()
+    for p, ws, s in zip(probs, spaces, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step(p, ws, s.cuda_stream)
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        check()

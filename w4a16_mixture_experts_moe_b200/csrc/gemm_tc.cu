@@ -77,7 +77,7 @@ constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // of the four epilogue warps of 
 // Each half has two staging buffers: with one, every 32 rows wait for the store
 // before them to have been read (BF16 gradients of 8 experts of 64 rows, K = 4096,
 // N = 14336: 238 -> 189 us; 64 experts of 256 rows, K = 2048, N = 1024: 94 -> 76).
-constexpr int SMEM = STAGES * STAGE_BYTES + 4 * OUT_BYTES + 3072 /*Shared*/;
+constexpr int SMEM = STAGES * STAGE_BYTES + 4 * OUT_BYTES + 3 * 1024 /*Shared*/;
 constexpr int OUT_BAR = 2;         // named barriers 2, 3: the four epilogue warps that share a staging buffer
 
 // One k-step, written by the first CTA's producer for its waiter.
@@ -106,7 +106,7 @@ struct Shared {
   };
   __device__ __forceinline__ int cnt(int e) const { return max(0, lo[e + 1] - lo[e]); }  // rows of group e
 };
-static_assert(sizeof(Shared) <= 3072, "shared tables budget");
+static_assert(sizeof(Shared) <= 3 * 1024, "shared tables budget");
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
