@@ -618,6 +618,15 @@ struct AdapterGradCfg {
   static constexpr int smem(int stages) { return 1024 + stages * STAGE + RED + int(sizeof(Ring)); }
 };
 
+// The operands' maps: boxes of AG_ROWS rows, and of AG_SHORT for a chunk that
+// holds no more (what the stage holds behind them is cleared in the fragments as
+// well): the time of a box goes by its rows (dA and dB of 9 adapters, rank 8, 68
+// single rows, K = 1832, N = 280: 23 -> 11 us).
+constexpr int AG_SHORT = 8;
+struct AdapterGradMaps {
+  CUtensorMap x[2], dy[2], u[2], du[2];
+};
+
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
 // with p = du, z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
@@ -627,9 +636,7 @@ struct AdapterGradCfg {
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
 template <int RJ, int AG_ROWS>
 __global__ void __launch_bounds__(CONSUMERS + 32)
-    adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ CUtensorMap tm_x,
-                        const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_u,
-                        const __grid_constant__ CUtensorMap tm_du) {
+    adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ AdapterGradMaps maps) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -645,7 +652,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   int slot = 0, round = 0;
   bool ok = true;
   if (warp == 8) {
-    const CUtensorMap *tz = is_a ? &tm_x : &tm_dy, *tp = is_a ? &tm_du : &tm_u;
+    const CUtensorMap *tz = is_a ? maps.x : maps.dy, *tp = is_a ? maps.du : maps.u;
     for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
       for (int s0 = 0; s0 < a.segs && ok; s0 += 32) {  // the lanes look at 32 segments
         const int s = s0 + lane;
@@ -660,11 +667,12 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
             ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);
             if (ok && tma::elect_one()) {
               uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
+              const int few = e - r <= AG_SHORT;
               ring.rows[slot] = min(AG_ROWS, e - r);
-              tma::mbar_arrive_expect_tx(&ring.full[slot], Cfg::STAGE);
-              tma::tma_load_2d(z, tz, c0, r, &ring.full[slot]);
-              tma::tma_load_2d(p, tp, 0, r, &ring.full[slot]);
-              if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp, 64, r, &ring.full[slot]);
+              tma::mbar_arrive_expect_tx(&ring.full[slot], few ? Cfg::STAGE / AG_ROWS * AG_SHORT : Cfg::STAGE);
+              tma::tma_load_2d(z, tz + few, c0, r, &ring.full[slot]);
+              tma::tma_load_2d(p, tp + few, 0, r, &ring.full[slot]);
+              if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp + few, 64, r, &ring.full[slot]);
             }
             __syncwarp();
             if (++slot == a.stages) { slot = 0; ++round; }
@@ -887,12 +895,13 @@ template <int RJ, int AG_ROWS>
 static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &dy, const Rows &u,
                                   const Rows &du, cudaStream_t s, const char *what) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
-  CUtensorMap tx, tdy, tu, tdu;
+  AdapterGradMaps maps;
   bool ok = true;
   const Rows *r[4] = {&x, &dy, &u, &du};
-  CUtensorMap *m[4] = {&tx, &tdy, &tu, &tdu};
-  for (int i = 0; i < 4; ++i)
-    ok &= map_bf16(m[i], r[i]->p, 2, {r[i]->width, a.T, 1, 1}, {r[i]->ld, 0, 0}, {64, AG_ROWS, 1, 1});
+  CUtensorMap *m[4] = {maps.x, maps.dy, maps.u, maps.du};
+  for (int i = 0; i < 8; ++i)
+    ok &= map_bf16(m[i >> 1] + (i & 1), r[i >> 1]->p, 2, {r[i >> 1]->width, a.T, 1, 1}, {r[i >> 1]->ld, 0, 0},
+                   {64, i & 1 ? AG_SHORT : AG_ROWS, 1, 1});
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   // Up to four CTAs per SM, each going through every grid.y-th adapter: an
   // adapter's end (sums joined and stored) hides behind the other CTAs. A grid
@@ -905,7 +914,7 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
   if (st != MOE_OK) return st;
   const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ, AG_ROWS>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
-                                   tx, tdy, tu, tdu);
+                                   maps);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
