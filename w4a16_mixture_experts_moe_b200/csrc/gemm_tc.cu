@@ -69,10 +69,11 @@ constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the outp
 // grows with the number of additions: 1e-6 of the result after 1024 products,
 // 1.6e-5 after 14,336. For fp32 outputs a longer reduction is therefore cut into
 // parts of at most F32_STEPS k-steps, which are added up in memory, rounded to
-// nearest, by the threads that own the values (14,336: 9e-7; 105 -> 134 us for
+// nearest, by the warp that owns the values (14,336: 9e-7; 105 -> 134 us for
 // 4096 rows of 1024; at 32 steps a part 2e-6 and 124 us).
 constexpr int F32_WHOLE = 16, F32_STEPS = 14;
 constexpr int OUT_ROWS = 32;       // output rows per staged store
+constexpr int OUT_F32_ROWS = 16;   // fp32: per staged store of a warp's 32 columns
 constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // of the four epilogue warps of a half
 // Each half has two staging buffers: with one, every 32 rows wait for the store
 // before them to have been read (BF16 gradients of 8 experts of 64 rows, K = 4096,
@@ -107,6 +108,7 @@ struct Shared {
   __device__ __forceinline__ int cnt(int e) const { return max(0, lo[e + 1] - lo[e]); }  // rows of group e
 };
 static_assert(sizeof(Shared) <= 3 * 1024, "shared tables budget");
+static_assert(EPI_WARPS * 2 * OUT_F32_ROWS * 128 <= 4 * OUT_BYTES, "staging buffers of fp32 outputs");
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -231,7 +233,7 @@ struct Maps {
                       // for nothing, which costs less than a second load). wgrad: 64 reduction rows x 64 columns,
                       // x 2 blocks (if b_wide)
   CUtensorMap ea, eb[3];  // adapters: like a and b
-  CUtensorMap out;     // BF16 output: 32 rows x 64 columns
+  CUtensorMap out;     // output: 32 rows x 64 columns (BF16), 16 rows x 32 columns (fp32)
   int a_wide, b_wide;
 };
 
@@ -256,17 +258,32 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t saddr, uint32_t r0, uint
                "r"(r2), "r"(r3)
                : "memory");
 }
-__device__ __forceinline__ void store_2d(const CUtensorMap *tm, uint32_t src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(tm)),
-               "r"(c0), "r"(c1), "r"(src)
-               : "memory");
+// A box from shared memory, stored or (F32, add) added to what is there, rounded to nearest.
+template <bool F32>
+__device__ __forceinline__ void store_2d(const CUtensorMap *tm, uint32_t src, int c0, int c1, bool add = false) {
+  if (F32 && add)
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
 }
-__device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(tm)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(src)
-               : "memory");
+template <bool F32>
+__device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, int c0, int c1, int c2, bool add = false) {
+  if (F32 && add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
 }
 
 // Parts of a tile's reduction of `steps` k-steps, and the first k-step of part p.
@@ -648,6 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3, part = warp >> 2;
     const bool issuer = q == 0 && lane == 0;
     const uint32_t out_bufs = smem_u32(smem + STAGES * STAGE_BYTES + part * 2 * OUT_BYTES);
+    const uint32_t warp_bufs = smem_u32(smem + STAGES * STAGE_BYTES + warp * 2 * OUT_F32_ROWS * 128);
     uint32_t stores = 0;
     if (ADAPTERS<MODE, F32> && a.late) pdl_wait();
     bool ok = true;
@@ -658,6 +676,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int parts = reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt(tl.e) : a.KD) + BK - 1) / BK);
       for (int p = 0; p < parts; ++p, ++unit) {
         const bool add = F32 && (p > 0 || a.accumulate);
+        // what this warp has stored of the tile is there before more is added to it
+        if (F32 && p > 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         const int b = unit & 1;
         ok = __all_sync(0xffffffffu, wait(sh, &sh.tmem_full[b], (unit >> 1) & 1, a.err));
         if (!ok) break;
@@ -681,7 +701,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (zero && add) {
           // nothing to add
         } else if (F32)
-          for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) direct(j0);
+          for (int j0 = part * 16; j0 < tl.nvalid; j0 += 32) {
+            if (MODE != GEMM_WGRAD && tl.nvalid - j0 < OUT_F32_ROWS) {
+              direct(j0);
+              continue;
+            }
+            // 16 rows of the warp's 32 columns, through two buffers of its own (stores
+            // straight from the registers, a row of 32 columns each, cost the epilogue
+            // 8 cycles apiece and twice that where rows are not multiples of 128
+            // bytes: wgrad of 64 experts x 10 rows, N = 3592, K = 968, 262 -> 178 us;
+            // dgrad of 64 x 256 rows, K = 2048, N = 1024, 92 -> 80)
+            uint32_t v[16];
+            tmem_ld16(tb + j0, v);
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            const uint32_t buf = warp_bufs + (stores++ & 1) * (OUT_F32_ROWS * 128);
+#pragma unroll
+            for (int j = 0; j < OUT_F32_ROWS; ++j)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4),
+                           "r"(zero ? 0u : v[j])
+                           : "memory");
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (fw < a.M) {
+                if (MODE == GEMM_WGRAD) store_3d<F32>(&m.out, buf, fw, tl.row + j0, tl.e, add);
+                else store_2d<F32>(&m.out, buf, fw, tl.row + j0, add);
+              }
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
         else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
           const int rows = min(OUT_ROWS, tl.nvalid - j0);
           if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
@@ -714,8 +763,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 if (fc + 64 * h >= a.M) break;
-                if (MODE == GEMM_WGRAD) store_3d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0, tl.e);
-                else store_2d(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0);
+                if (MODE == GEMM_WGRAD) store_3d<false>(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0, tl.e);
+                else store_2d<false>(&m.out, out_buf + h * (OUT_ROWS * 128), fc + 64 * h, tl.row + j0);
               }
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -728,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0) arrive_leader(&sh.tmem_empty[b]);
       }
     }
-    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (F32 ? lane == 0 : issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == A_WARP) {
     produce<MODE, F32, true>(sh, a, m, smem, rank, total);
   } else if (warp == B_WARP) {
@@ -831,19 +880,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 }  // namespace gt
 
-bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
-                     const int (&box)[4]) {
+static bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *base, int nd, const int64_t (&dim)[4],
+                       const int64_t (&stride)[3], const int (&box)[4]) {
   cuuint64_t d[4], st[3];
   cuuint32_t bx[4], es[4];
   for (int i = 0; i < nd; ++i) {
     d[i] = cuuint64_t(dim[i]);
     bx[i] = cuuint32_t(box[i]);
     es[i] = 1;
-    if (i) st[i - 1] = cuuint64_t(stride[i - 1]) * 2;
+    if (i) st[i - 1] = cuuint64_t(stride[i - 1]) * size;
   }
-  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(nd), const_cast<void *>(base), d, st, bx,
-                              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return tensor_map_encoder()(m, type, cuuint32_t(nd), const_cast<void *>(base), d, st, bx, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],
+              const int (&box)[4]) {
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, nd, dim, stride, box);
 }
 
 template <int MODE, bool F32>
@@ -872,7 +926,12 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
   } else {
     for (int i = 0; i < 3; ++i) ok &= map_bf16(&m.b[i], op.b, 2, {width, a.R, 1, 1}, {op.ldb, 0, 0}, {64, 32 << i, 1, 1});
   }
-  if (!F32)
+  if (F32)
+    ok &= MODE == GEMM_WGRAD ? encode_map(&m.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.out, 3, {K, N, a.groups, 1},
+                                          {a.ldo, a.out_gstride, 0}, {32, gt::OUT_F32_ROWS, 1, 1})
+                             : encode_map(&m.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.out, 2, {a.M, a.R, 1, 1},
+                                          {a.ldo, 0, 0}, {32, gt::OUT_F32_ROWS, 1, 1});
+  else
     ok &= MODE == GEMM_WGRAD
               ? map_bf16(&m.out, a.out, 3, {K, N, a.groups, 1}, {a.ldo, a.out_gstride, 0}, {64, gt::OUT_ROWS, 1, 1})
               : map_bf16(&m.out, a.out, 2, {a.M, a.R, 1, 1}, {a.ldo, 0, 0}, {64, gt::OUT_ROWS, 1, 1});
