@@ -43,6 +43,7 @@
 // pair may name its peer's), so a k-step costs no message between the CTAs.
 // All waits are bounded (see tma.cuh).
 #include "gemm.cuh"
+#include "gemm_parts.h"
 
 namespace moe {
 namespace gt {
@@ -65,13 +66,6 @@ constexpr int HANDOFF_BAR = 1;  // named barrier of the waiter and the MMA warp
 // HAND_FIRST (a tile's first k-step, which overwrites the accumulator).
 constexpr int HAND_KK = 7, HAND_LAST = 8, HAND_SET = 16, HAND_STOP = 31, HAND_FIRST = 31;
 constexpr int ROW_BLOCK = 16;      // row tiles that share a sweep over the output columns
-// The tensor core adds to its fp32 accumulator with truncation, an error that
-// grows with the number of additions: 1e-6 of the result after 1024 products,
-// 1.6e-5 after 14,336. For fp32 outputs a longer reduction is therefore cut into
-// parts of at most F32_STEPS k-steps, which are added up in memory, rounded to
-// nearest, by the warp that owns the values (14,336: 9e-7; 8 groups of
-// 512 rows, N = 1024: 118 us, 95 with BF16 outputs in one part).
-constexpr int F32_WHOLE = 16, F32_STEPS = 14;
 constexpr int OUT_ROWS = 32;       // output rows per staged store
 constexpr int OUT_F32_ROWS = 16;   // fp32: per staged store of a warp's 32 columns
 constexpr int OUT_BYTES = OUT_ROWS * BMC * 2;  // of the four epilogue warps of a half
@@ -285,13 +279,6 @@ __device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, in
                  "r"(c0), "r"(c1), "r"(c2), "r"(src)
                  : "memory");
 }
-
-// Parts of a tile's reduction of `steps` k-steps, and the first k-step of part p.
-template <bool F32>
-__device__ __forceinline__ int reduction_parts(int steps) {
-  return !F32 || steps <= F32_WHOLE ? 1 : (steps + F32_STEPS - 1) / F32_STEPS;
-}
-__device__ __forceinline__ int part_start(int steps, int parts, int p) { return steps * p / parts; }
 
 struct Tile {
   int e;       // group
