@@ -57,3 +57,95 @@ def test_short_reductions_are_one_part(parts, steps):
 @pytest.mark.parametrize("steps", [1, 17, 1 << 24])
 def test_16_bit_outputs_are_one_part(parts, steps):
     assert parts.whole(steps) == 1
+
+
+@pytest.fixture(scope="module")
+def flow(tmp_path_factory):
+    return _compile(str(tmp_path_factory.mktemp("flow")), """
+#include <atomic>
+#include <chrono>
+#include <condition_variable>
+#include <mutex>
+#include <thread>
+#include <vector>
+#include "ring_flow.h"
+
+// A meeting of n threads that gives up after a while (a thread that never comes).
+struct Meeting {
+  std::mutex m;
+  std::condition_variable cv;
+  int n, in = 0, turn = 0;
+  bool all = true, last = true, stuck = false;
+  bool meet(bool ok) {
+    std::unique_lock<std::mutex> l(m);
+    const int mine = turn;
+    all = all && ok;
+    if (++in == n) {
+      last = all; all = true; in = 0; ++turn;
+      cv.notify_all();
+    } else if (!cv.wait_for(l, std::chrono::seconds(5), [&] { return turn != mine || stuck; }) || stuck) {
+      stuck = true;
+      cv.notify_all();
+      return false;
+    }
+    return last;
+  }
+};
+
+// n consumers go through groups of stages[g] stages each; consumer c's wait number
+// fail_at[c] (and all behind it) gives up. Behind a group with rows, two more
+// meetings follow, as for the join of partial sums. Returns 0: all of them ended
+// alike, 1: some group was left differently, 2: a meeting that not all came to,
+// 3: rows taken that do not belong to the group.
+extern "C" int run(int n, int groups, const int *stages, const int *fail_at) {
+  Meeting meeting;
+  meeting.n = n;
+  std::vector<std::vector<int>> got(n);
+  std::atomic<int> wrong{0};
+  std::vector<std::thread> t;
+  for (int c = 0; c < n; ++c)
+    t.emplace_back([&, c] {
+      int waits = 0;
+      for (int g = 0; g < groups; ++g) {
+        int i = 0, taken = 0;
+        const int r = moe::take_group(
+            [&] { return waits++ >= fail_at[c] ? -1 : i < stages[g] ? 10 + i++ : 0; },
+            [&](int rows) { taken += rows; },
+            [&](bool ok) { return meeting.meet(ok); });
+        got[c].push_back(r);
+        if (r < 0) return;
+        if (taken != 10 * stages[g] + stages[g] * (stages[g] - 1) / 2 || r != (stages[g] > 0)) wrong = 1;
+        if (r) { meeting.meet(true); meeting.meet(true); }
+      }
+    });
+  for (auto &x : t) x.join();
+  if (meeting.stuck) return 2;
+  for (int c = 1; c < n; ++c)
+    if (got[c] != got[0]) return 1;
+  return wrong ? 3 : 0;
+}
+""")
+
+
+def _run_flow(flow, stages, fail_at):
+    a, b = (C.c_int * len(stages))(*stages), (C.c_int * len(fail_at))(*fail_at)
+    return flow.run(len(fail_at), len(stages), a, b)
+
+
+NEVER = 1 << 30
+
+
+@pytest.mark.parametrize("stages", [[1], [0], [3, 0, 2], [0, 0, 0], [5, 1, 0, 7]])
+def test_groups_without_failures(flow, stages):
+    assert _run_flow(flow, stages, [NEVER] * 8) == 0
+
+
+@pytest.mark.parametrize("stages", [[1], [3, 0, 2], [0, 4, 0], [2, 2]])
+@pytest.mark.parametrize("late", [[0], [3], [0, 7], [1, 2, 3, 4, 5, 6, 7], list(range(8))])
+def test_a_wait_that_gives_up_takes_every_consumer_out(flow, stages, late):
+    """Some consumers' waits give up, at every place where they can, the others' do not (a stage that lands just at
+    the limit): all leave at the same group, and none stays at a meeting."""
+    for at in range(sum(stages) + len(stages)):
+        assert _run_flow(flow, stages, [at if c in late else NEVER for c in range(8)]) == 0, at
+        # ... and the others one wait later
+        assert _run_flow(flow, stages, [at if c in late else at + 1 for c in range(8)]) == 0, at

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "gemm.cuh"
+#include "ring_flow.h"
 
 namespace cg = cooperative_groups;
 
@@ -67,6 +68,15 @@ constexpr int CONSUMERS = 256;  // warps 0-7; warp 8 issues the loads
 constexpr int RING_MAX = 12;
 constexpr int CONSUMER_BAR = 1;
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync %0, %1;" ::"n"(CONSUMER_BAR), "n"(CONSUMERS) : "memory"); }
+// The consumers meet: whether all of them passed true.
+__device__ __forceinline__ bool consumer_all(bool ok) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(all)
+               : "r"(uint32_t(ok)), "n"(CONSUMER_BAR), "n"(CONSUMERS)
+               : "memory");
+  return all != 0;
+}
 
 struct Ring {
   uint64_t full[RING_MAX], empty[RING_MAX];
@@ -692,20 +702,25 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   }
   const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;
   const int lo = lane & 7, m8 = (lane >> 3) & 1, hi = lane >> 4;
-  for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
+  for (int ad = blockIdx.y; ad < a.n_adapters; ad += gridDim.y) {
     float acc[RJ / 8][4];
 #pragma unroll
     for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-    bool any = false, more = true;
-    while (more) {
-      ok = ring_wait(ring, &ring.full[slot], round & 1, a.err);
-      if (!ok) break;
+    auto release = [&]() {
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
+      if (++slot == a.stages) { slot = 0; ++round; }
+    };
+    auto next = [&]() {
+      if (!ring_wait(ring, &ring.full[slot], round & 1, a.err)) return -1;
       const int rows = ring.rows[slot];
+      if (rows == 0) release();
+      return rows;
+    };
+    auto stage = [&](int rows) {
       const uint32_t z = ring0 + slot * Cfg::STAGE, p = z + Cfg::Z;
-      more = rows > 0;
-      any |= more;
       auto products = [&](auto cut) {  // cut: the stage ends inside this warp's rows
 #pragma unroll
         for (int i = 0; i < AG_ROWS / 32; ++i) {
@@ -732,11 +747,12 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       };
       if (rows >= (kg + 1) * (AG_ROWS / 2)) products(std::false_type{});
       else if (rows > kg * (AG_ROWS / 2)) products(std::true_type{});
-      __syncwarp();
-      if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
-      if (++slot == a.stages) { slot = 0; ++round; }
-    }
-    if (!any) {  // no rows: zeros
+      release();
+    };
+    // (the meeting at a group's end is also behind the reads of the last group's sums)
+    const int got = take_group(next, stage, consumer_all);
+    if (got < 0) return;
+    if (got == 0) {  // no rows: zeros
       const uint4 zero = make_uint4(0, 0, 0, 0);
       for (int p = tid; p < AG_COLS * a.rank / 8; p += CONSUMERS) {
         if (is_a) {
@@ -781,7 +797,6 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
               pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
       }
     }
-    consumer_sync();  // the sums are read
   }
 }
 
