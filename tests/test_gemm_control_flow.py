@@ -124,6 +124,12 @@ extern "C" int run(int n, int groups, const int *stages, const int *fail_at) {
     if (got[c] != got[0]) return 1;
   return wrong ? 3 : 0;
 }
+
+// The waits of a producer's end after `issued` uses of a ring: parity[q], or -1 for a slot that is not waited for.
+extern "C" void ends(int stages, int issued, int *parity) {
+  for (int q = 0; q < stages; ++q) parity[q] = -1;
+  moe::last_uses(stages, issued % stages, issued / stages, [&](int q, int p) { parity[q] = parity[q] < 0 ? p : 9; });
+}
 """)
 
 
@@ -149,3 +155,14 @@ def test_a_wait_that_gives_up_takes_every_consumer_out(flow, stages, late):
         assert _run_flow(flow, stages, [at if c in late else NEVER for c in range(8)]) == 0, at
         # ... and the others one wait later
         assert _run_flow(flow, stages, [at if c in late else at + 1 for c in range(8)]) == 0, at
+
+
+@pytest.mark.parametrize("stages", [2, 3, 7, 12])
+def test_a_producer_ends_behind_its_last_loads(flow, stages):
+    for issued in range(4 * stages):
+        got = (C.c_int * stages)()
+        flow.ends(stages, issued, got)
+        want = [-1] * stages
+        for use in range(issued):           # phase `use // stages` of the slot's barrier
+            want[use % stages] = use // stages & 1
+        assert list(got) == want, issued

@@ -100,6 +100,12 @@ __device__ __forceinline__ bool ring_wait(Ring &ring, uint64_t *bar, uint32_t pa
   return __all_sync(0xffffffffu, ok);
 }
 
+// The producer's end: its loads have landed. A block whose waits gave up would
+// otherwise leave shared memory while copies are still on their way into it.
+__device__ __forceinline__ void ring_drain(Ring &ring, int stages, int slot, int round, int32_t *err) {
+  last_uses(stages, slot, round, [&](int q, int parity) { ring_wait(ring, &ring.full[q], uint32_t(parity), err, true); });
+}
+
 struct ShrinkArgs {
   const int32_t *seg_offsets, *seg_adapter;
   const float *scale;
@@ -241,6 +247,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       __syncwarp();
       if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
+    ring_drain(ring, Cfg::STAGES, slot, round, a.err);
     return;
   }
   const int rw = warp % Cfg::RW, kw = warp / Cfg::RW, g = lane >> 2, t4 = lane & 3;
@@ -512,6 +519,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       __syncwarp();
       if (++slot == Cfg::STAGES) { slot = 0; ++round; }
     }
+    ring_drain(ring, Cfg::STAGES, slot, round, a.err);
   } else {
     if (tid < ROWS) {  // the rows' adapters
       const int row = row0 + tid;
@@ -698,6 +706,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       __syncwarp();
       if (++slot == a.stages) { slot = 0; ++round; }
     }
+    ring_drain(ring, a.stages, slot, round, a.err);
     return;
   }
   const int cg = warp & 3, kg = warp >> 2, g = lane >> 2, t4 = lane & 3;

@@ -1,5 +1,5 @@
-// Control flow that the consumers of a ring of loads have to follow alike. Plain
-// C++ beside the kernels' code, so that it can be checked without a GPU.
+// Control flow around a ring of loads: what its consumers have to follow alike,
+// and what its producer waits for before it ends. Plain C++ beside the kernels' code, so that it can be checked without a GPU.
 #pragma once
 
 #ifdef __CUDACC__
@@ -24,6 +24,16 @@ MOE_FLOW int take_group(Wait wait, Products products, All all) {
     any = 1;
   }
   return all(rows == 0) ? any : -1;
+}
+
+// wait(slot, parity) for the last use of each slot of a ring that has been used:
+// the loads that may be in flight when use `round` of `slot` comes next.
+template <class Wait>
+MOE_FLOW void last_uses(int stages, int slot, int round, Wait wait) {
+  for (int q = 0; q < stages; ++q) {
+    const int uses = round + (q < slot ? 1 : 0);
+    if (uses > 0) wait(q, (uses - 1) & 1);
+  }
 }
 
 }  // namespace moe
