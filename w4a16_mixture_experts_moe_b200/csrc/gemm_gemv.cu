@@ -124,8 +124,11 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
   extern __shared__ float red[];
   __shared__ int found[32], which, pass;
   const bool late = a.seg_adapter != nullptr;  // the previous launch only writes u
+  // A launch that starts early may count on what this one waited for. With
+  // adapters the launch before has waited for all of that already, and this one
+  // waits for that launch before it ends.
   if (!late) pdl_wait();
-  pdl_trigger();  // behind the wait: a launch that starts early may count on what this one waited for
+  pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int e = blockIdx.y, r_first = 0;
   if (a.split == GEMV_ALL_PASSES || (a.split == GEMV_LATER_PASSES && e >= a.groups)) {
@@ -167,7 +170,10 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
   if ((o0 < 0 || o1 < o0 || o1 > a.R || (a.index && e == 0 && o0 != 0)) && blockIdx.x == 0 && tid == 0)
     flag_error(a.err, MOE_DEVERR_OFFSETS);
   const int lo = min(max(o0, 0), a.R), rows_in = min(max(o1, 0), a.R) - lo;
-  if (rows_in <= 0) return;
+  if (rows_in <= 0) {
+    if (late) pdl_wait();  // the launches behind this one wait for it alone
+    return;
+  }
   const int cnt = a.split == GEMV_WHOLE ? rows_in : min(rows_in, r_first + MAXNT * 8);  // this CTA's: r_first .. cnt - 1
   if (a.row_seg && blockIdx.x == 0)
     for (int r = r_first + tid; r < cnt; r += WARPS * 32) a.row_seg[lo + r] = e;
