@@ -131,7 +131,7 @@ def _current_device() -> int:
         _torch = torch
     try:
         return _torch._C._cuda_getDevice()
-    except RuntimeError:
+    except (RuntimeError, AttributeError):  # no driver or device; a torch built without CUDA has no such function
         return -2
 
 
@@ -142,15 +142,12 @@ def _addr(arr):
 def _stream(s):
     if s is None:  # the raw handle of torch's current stream, without the Stream object around it
         d = _current_device()
+        if d < 0:
+            return _torch.cuda.current_stream().cuda_stream  # says why there is none
         return _torch._C._cuda_getCurrentRawStream(d)
     if isinstance(s, int):
         return s
     return s.cuda_stream
-
-
-def _check(status: int):
-    if status != MOE_OK:
-        raise MoeError(status, lib.moe_last_error().decode())
 
 
 def moe_last_error() -> str:
