@@ -150,6 +150,11 @@ def _stream(s):
     return s.cuda_stream
 
 
+def _check(status: int):
+    if status != MOE_OK:
+        raise MoeError(status, lib.moe_last_error().decode())
+
+
 def moe_last_error() -> str:
     return lib.moe_last_error().decode()
 
