@@ -51,3 +51,16 @@ def test_a_device_that_torch_has_not_started_yet(N, monkeypatch):
     # the public call starts CUDA and finds the stream
     monkeypatch.setattr(N, "_torch", _Torch(RuntimeError, lambda: type("S", (), {"cuda_stream": 77})))
     assert N._stream(None) == 77
+
+
+def test_a_replaced_name_is_seen(N, monkeypatch):
+    import w4a16_mixture_experts_moe_b200 as moe
+    from w4a16_mixture_experts_moe_b200 import layer
+    assert moe.moe_abi_version is N.moe_abi_version and moe.ExpertBank is layer.ExpertBank
+    monkeypatch.setattr(N, "moe_abi_version", lambda: 1234)
+    monkeypatch.setattr(layer, "ExpertBank", int)
+    assert moe.moe_abi_version() == 1234 and moe.ExpertBank is int
+    monkeypatch.undo()
+    assert moe.moe_abi_version is N.moe_abi_version and moe.ExpertBank is layer.ExpertBank
+    with pytest.raises(AttributeError):
+        moe.no_such_name
