@@ -64,3 +64,133 @@ def test_a_replaced_name_is_seen(N, monkeypatch):
     assert moe.moe_abi_version is N.moe_abi_version and moe.ExpertBank is layer.ExpertBank
     with pytest.raises(AttributeError):
         moe.no_such_name
+
+
+# ---- what the grouped products and the projection with adapters refuse. The tensors live on the CPU, whose device
+# number is -1: with that as the current device, the checks behind the device's are reached.
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture
+def cpu(N, monkeypatch):
+    monkeypatch.setattr(N, "_current_device", lambda: -1)
+    calls = []
+
+    class Lib:  # the library, which only records what it is given
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+    monkeypatch.setattr(N, "lib", Lib())
+    monkeypatch.setattr(N, "_torch", torch)
+    for name, kinds in (("_BF16", (torch.bfloat16, torch.uint16, torch.int16)), ("_I32", (torch.int32,)), ("_F32", (torch.float32,))):
+        monkeypatch.setattr(N, name, kinds)
+    return calls
+
+
+R, E, n, k, T, S, A, r = 5, 3, 16, 24, 6, 2, 4, 8
+
+
+def _grouped(N, direction, **other):
+    out = {"fwd": ("y", R, n), "dgrad": ("dx", R, k), "wgrad": ("dw", E, n * k)}[direction]
+    t = dict(x=torch.zeros(R, k, dtype=BF), dy=torch.zeros(R, n, dtype=BF), w=torch.zeros(E, n, k, dtype=BF),
+             offsets=torch.zeros(E + 1, dtype=I32), ws=torch.zeros(256, dtype=torch.uint8), flags=0, ws_bytes=256)
+    t[out[0]] = torch.zeros(out[1], out[2], dtype=BF)
+    t.update(other)
+    if direction == "fwd":
+        N.moe_grouped_gemm(t["x"], t.get("ldx", k), t["offsets"], t["w"], n * k, R, E, n, k, t["flags"], t["y"], n, t["ws"], t["ws_bytes"], 0)
+    elif direction == "dgrad":
+        N.moe_grouped_gemm_dgrad(t["dy"], n, t["offsets"], t["w"], n * k, R, E, n, k, t["flags"], t["dx"], k, t["ws"], t["ws_bytes"], 0)
+    else:
+        N.moe_grouped_gemm_wgrad(t["dy"], n, t["x"], t.get("ldx", k), t["offsets"], R, E, n, k, t["flags"], t["dw"], n * k, t["ws"], t["ws_bytes"], 0)
+
+
+def _lora_args():
+    return dict(x=torch.zeros(T, k, dtype=BF), dy=torch.zeros(T, n, dtype=BF), w=torch.zeros(n, k, dtype=BF),
+                seg_offsets=torch.zeros(S + 1, dtype=I32), seg_adapter=torch.zeros(S, dtype=I32),
+                lora_a=torch.zeros(A, r, k, dtype=BF), lora_b=torch.zeros(A, n, r, dtype=BF), scale=torch.zeros(A, dtype=F32),
+                u=torch.zeros(T, r, dtype=BF), y=torch.zeros(T, n, dtype=BF), du=torch.zeros(T, r, dtype=BF),
+                dx=torch.zeros(T, k, dtype=BF), d_lora_a=torch.zeros(A, r, k, dtype=BF), d_lora_b=torch.zeros(A, n, r, dtype=BF),
+                ws=torch.zeros(256, dtype=torch.uint8))
+
+
+def _lora(N, back, **other):
+    t = {**_lora_args(), **other}
+    if back:
+        N.moe_lora_linear_backward(t["dy"], n, t["x"], k, t["w"], t["u"], t["seg_offsets"], t["seg_adapter"], t["lora_a"],
+                                   t["lora_b"], t["scale"], T, S, A, r, n, k, t["du"], t["dx"], k, t["d_lora_a"],
+                                   t["d_lora_b"], t["ws"], 256, 0)
+    else:
+        N.moe_lora_linear(t["x"], k, t["w"], t["seg_offsets"], t["seg_adapter"], t["lora_a"], t["lora_b"], t["scale"], T, S,
+                          A, r, n, k, t["u"], t["y"], n, t["ws"], 256, 0)
+
+
+def _refused(N, cpu, name, call):
+    with pytest.raises(N.MoeError, match=f"^.status {N.MOE_ERR_INVALID_ARG}. {name}: ") as ei:
+        call()
+    assert not cpu  # the library was not called
+    return str(ei.value)
+
+
+@pytest.mark.parametrize("direction", ["fwd", "dgrad", "wgrad"])
+def test_grouped_tensors(N, cpu, direction):
+    mine = {"fwd": ["x", "offsets", "w", "y", "ws"], "dgrad": ["dy", "offsets", "w", "dx", "ws"],
+            "wgrad": ["dy", "x", "offsets", "dw", "ws"]}[direction]
+    _grouped(N, direction)
+    assert len(cpu) == 1
+    full = dict(x=torch.zeros(R, k, dtype=BF), dy=torch.zeros(R, n, dtype=BF), w=torch.zeros(E, n, k, dtype=BF),
+                offsets=torch.zeros(E + 1, dtype=I32), ws=torch.zeros(256, dtype=torch.uint8), y=torch.zeros(R, n, dtype=BF),
+                dx=torch.zeros(R, k, dtype=BF), dw=torch.zeros(E, n * k, dtype=BF))
+    del cpu[:]
+    for name in mine:
+        t = full[name]
+        assert "reaches" in _refused(N, cpu, name, lambda: _grouped(N, direction, **{name: t.flatten()[:-1].clone()}))
+        wide = torch.zeros(1, dtype=t.dtype).expand(t.numel())   # one element under any number of indices
+        assert "reaches" in _refused(N, cpu, name, lambda: _grouped(N, direction, **{name: wide}))
+        if name != "ws":
+            for kind in (torch.float32, torch.float16, torch.int64):
+                assert str(kind) in _refused(N, cpu, name, lambda: _grouped(N, direction, **{name: t.to(kind)}))
+    out = {"fwd": "y", "dgrad": "dx", "wgrad": "dw"}[direction]
+    f32 = dict(flags=N.MOE_GEMM_OUT_F32)
+    assert "bfloat16" in _refused(N, cpu, out, lambda: _grouped(N, direction, **f32))
+    assert "reaches" in _refused(N, cpu, out, lambda: _grouped(N, direction, **f32, **{out: full[out].float().flatten()[1:].clone()}))
+    _grouped(N, direction, **f32, **{out: full[out].float()})
+    assert len(cpu) == 1
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_adapters_tensors(N, cpu, back):
+    mine = ["x", "w", "seg_offsets", "seg_adapter", "lora_a", "lora_b", "scale", "u", "ws"]
+    mine += ["dy", "du", "dx", "d_lora_a", "d_lora_b"] if back else ["y"]
+    _lora(N, back)
+    assert len(cpu) == 1
+    del cpu[:]
+    for name in mine:
+        t = _lora_args()[name]
+        assert "reaches" in _refused(N, cpu, name, lambda: _lora(N, back, **{name: t.flatten()[:-1].clone()}))
+        if name != "ws":
+            for kind in (torch.float16, torch.int64, torch.float64):
+                assert str(kind) in _refused(N, cpu, name, lambda: _lora(N, back, **{name: t.to(kind)}))
+
+
+def test_views_that_hold_what_the_call_reaches(N, cpu):
+    wide = torch.zeros(R, k + 40, dtype=BF)
+    _grouped(N, "fwd", x=wide[:, :k], ldx=k + 40)          # a strided view, its rows' padding in the storage
+    _grouped(N, "fwd", x=wide[:, 40:], ldx=k + 40)         # (the last row ends with the storage)
+    _grouped(N, "fwd", x=torch.zeros(R, k, dtype=torch.int16))  # 16-bit patterns
+    assert len(cpu) == 3
+    del cpu[:]
+    _refused(N, cpu, "x", lambda: _grouped(N, "fwd", x=wide[:, 41:], ldx=k + 40))
+    _refused(N, cpu, "x", lambda: _grouped(N, "fwd", x=wide[1:, :k], ldx=k + 40))
+    _refused(N, cpu, "ws", lambda: _grouped(N, "fwd", ws_bytes=257))
+    _lora(N, False, scale=None)
+    _lora(N, True, scale=None, dx=None, d_lora_a=None, d_lora_b=None, x=None, u=None)
+    assert len(cpu) == 2
+
+
+def test_no_rows_reach_nothing(N, cpu):
+    few = torch.zeros(1, dtype=BF)
+    off, ws = torch.zeros(E + 1, dtype=I32), torch.zeros(256, dtype=torch.uint8)
+    N.moe_grouped_gemm(few, k, off, few, n * k, 0, E, n, k, 0, few, n, ws, 256, 0)
+    N.moe_grouped_gemm_dgrad(few, n, off, few, n * k, 0, E, n, k, 0, few, k, ws, 256, 0)
+    N.moe_grouped_gemm_wgrad(few, n, few, k, off, 0, E, n, k, 0, torch.zeros(E, n, k, dtype=BF), n * k, ws, 256, 0)
+    assert len(cpu) == 3

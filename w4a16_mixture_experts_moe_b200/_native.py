@@ -109,26 +109,40 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _dev(x, cur):
-    """_ptr of an argument that a kernel dereferences: a tensor has to live on the current device `cur` (an address
-    that this device cannot reach would fault it)."""
-    if x is None or isinstance(x, int):
+def _dev(x, cur, name, kinds, need):
+    """_ptr of an argument that a kernel dereferences. A tensor has to live on the current device `cur` (an address
+    that this device cannot reach would fault it), be of one of `kinds` (dtype names; none: any) and hold `need` bytes
+    from its first element on, whatever strides its view of them has; an address is taken as it is."""
+    if x is None or x.__class__ is int:
         return x
-    if x.get_device() != cur:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"tensor on {x.device}, but the current device is cuda:{cur}")
+    if x.get_device() != cur or (kinds and x.dtype not in kinds) or x.nbytes < need or not x.is_contiguous():
+        _dev_slow(x, cur, name, kinds, need)
     return x.data_ptr()
 
 
+def _dev_slow(x, cur, name, kinds, need):
+    if x.get_device() != cur:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: tensor on {x.device}, but the current device is cuda:{cur}")
+    if kinds and x.dtype not in kinds:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: a tensor of {x.dtype}, not of {' or '.join(map(str, kinds))}")
+    have = x.untyped_storage().nbytes() - x.storage_offset() * x.itemsize
+    if have < need:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{name}: {have} bytes from the tensor's first element on, but the call "
+                                            f"reaches {need}")
+
+
 _torch = None
+_BF16 = _I32 = _F32 = ()  # dtypes of the arguments (filled with torch's): BF16 values or their 16-bit patterns
 
 
 def _current_device() -> int:
     """torch's current CUDA device (-2 without one). Asked of torch's C layer:
     the public call costs half a microsecond more on every launch."""
-    global _torch
+    global _torch, _BF16, _I32, _F32
     if _torch is None:
         import torch
         _torch = torch
+        _BF16, _I32, _F32 = (torch.bfloat16, torch.uint16, torch.int16), (torch.int32,), (torch.float32,)
     try:
         return _torch._C._cuda_getDevice()
     except (RuntimeError, AttributeError):  # no driver or device; a torch built without CUDA has no such function
@@ -239,20 +253,32 @@ def moe_grouped_gemm_workspace_size(R, E, N, K) -> int:
 
 def moe_grouped_gemm(x, ldx, offsets, w, w_stride, R, E, N, K, flags, y, ldy, ws, ws_bytes, stream=None):
     d = _current_device()
-    _check(lib.moe_grouped_gemm(_dev(x, d), ldx, _dev(offsets, d), _dev(w, d), w_stride, R, E, N, K, flags, _dev(y, d),
-                                ldy, _dev(ws, d), ws_bytes, _stream(stream)))
+    f32 = flags & MOE_GEMM_OUT_F32
+    _check(lib.moe_grouped_gemm(
+        _dev(x, d, "x", _BF16, R and 2 * ((R - 1) * ldx + K)), ldx, _dev(offsets, d, "offsets", _I32, 4 * E + 4),
+        _dev(w, d, "w", _BF16, R and 2 * ((E - 1) * w_stride + N * K)), w_stride, R, E, N, K, flags,
+        _dev(y, d, "y", _F32 if f32 else _BF16, R and (4 if f32 else 2) * ((R - 1) * ldy + N)), ldy,
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
 
 
 def moe_grouped_gemm_dgrad(dy, lddy, offsets, w, w_stride, R, E, N, K, flags, dx, lddx, ws, ws_bytes, stream=None):
     d = _current_device()
-    _check(lib.moe_grouped_gemm_dgrad(_dev(dy, d), lddy, _dev(offsets, d), _dev(w, d), w_stride, R, E, N, K, flags,
-                                      _dev(dx, d), lddx, _dev(ws, d), ws_bytes, _stream(stream)))
+    f32 = flags & MOE_GEMM_OUT_F32
+    _check(lib.moe_grouped_gemm_dgrad(
+        _dev(dy, d, "dy", _BF16, R and 2 * ((R - 1) * lddy + N)), lddy, _dev(offsets, d, "offsets", _I32, 4 * E + 4),
+        _dev(w, d, "w", _BF16, R and 2 * ((E - 1) * w_stride + N * K)), w_stride, R, E, N, K, flags,
+        _dev(dx, d, "dx", _F32 if f32 else _BF16, R and (4 if f32 else 2) * ((R - 1) * lddx + K)), lddx,
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
 
 
 def moe_grouped_gemm_wgrad(dy, lddy, x, ldx, offsets, R, E, N, K, flags, dw, dw_stride, ws, ws_bytes, stream=None):
     d = _current_device()
-    _check(lib.moe_grouped_gemm_wgrad(_dev(dy, d), lddy, _dev(x, d), ldx, _dev(offsets, d), R, E, N, K, flags,
-                                      _dev(dw, d), dw_stride, _dev(ws, d), ws_bytes, _stream(stream)))
+    f32 = flags & MOE_GEMM_OUT_F32
+    _check(lib.moe_grouped_gemm_wgrad(
+        _dev(dy, d, "dy", _BF16, R and 2 * ((R - 1) * lddy + N)), lddy, _dev(x, d, "x", _BF16, R and 2 * ((R - 1) * ldx + K)), ldx,
+        _dev(offsets, d, "offsets", _I32, 4 * E + 4), R, E, N, K, flags,
+        _dev(dw, d, "dw", _F32 if f32 else _BF16, E and (4 if f32 else 2) * ((E - 1) * dw_stride + N * K)), dw_stride,
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
 
 
 def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
@@ -262,18 +288,29 @@ def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
 def moe_lora_linear(x, ldx, w, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters, rank, N, K, u, y, ldy,
                     ws, ws_bytes, stream=None):
     d = _current_device()
-    _check(lib.moe_lora_linear(_dev(x, d), ldx, _dev(w, d), _dev(seg_offsets, d), _dev(seg_adapter, d), _dev(lora_a, d),
-                               _dev(lora_b, d), _dev(scale, d), T, S, n_adapters, rank, N, K, _dev(u, d), _dev(y, d),
-                               ldy, _dev(ws, d), ws_bytes, _stream(stream)))
+    bf, per = _BF16, 2 * n_adapters * rank
+    _check(lib.moe_lora_linear(
+        _dev(x, d, "x", bf, T and 2 * ((T - 1) * ldx + K)), ldx, _dev(w, d, "w", bf, 2 * N * K),
+        _dev(seg_offsets, d, "seg_offsets", _I32, 4 * S + 4), _dev(seg_adapter, d, "seg_adapter", _I32, 4 * S),
+        _dev(lora_a, d, "lora_a", bf, per * K), _dev(lora_b, d, "lora_b", bf, per * N),
+        _dev(scale, d, "scale", _F32, 4 * n_adapters), T, S, n_adapters, rank, N, K,
+        _dev(u, d, "u", bf, 2 * T * rank), _dev(y, d, "y", bf, T and 2 * ((T - 1) * ldy + N)), ldy,
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
 
 
 def moe_lora_linear_backward(dy, lddy, x, ldx, w, u, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters,
                              rank, N, K, du, dx, lddx, d_lora_a, d_lora_b, ws, ws_bytes, stream=None):
     d = _current_device()
-    _check(lib.moe_lora_linear_backward(_dev(dy, d), lddy, _dev(x, d), ldx, _dev(w, d), _dev(u, d), _dev(seg_offsets, d),
-                                        _dev(seg_adapter, d), _dev(lora_a, d), _dev(lora_b, d), _dev(scale, d), T, S,
-                                        n_adapters, rank, N, K, _dev(du, d), _dev(dx, d), lddx, _dev(d_lora_a, d),
-                                        _dev(d_lora_b, d), _dev(ws, d), ws_bytes, _stream(stream)))
+    bf, per = _BF16, 2 * n_adapters * rank
+    _check(lib.moe_lora_linear_backward(
+        _dev(dy, d, "dy", bf, T and 2 * ((T - 1) * lddy + N)), lddy, _dev(x, d, "x", bf, T and 2 * ((T - 1) * ldx + K)), ldx,
+        _dev(w, d, "w", bf, 2 * N * K), _dev(u, d, "u", bf, 2 * T * rank),
+        _dev(seg_offsets, d, "seg_offsets", _I32, 4 * S + 4), _dev(seg_adapter, d, "seg_adapter", _I32, 4 * S),
+        _dev(lora_a, d, "lora_a", bf, per * K), _dev(lora_b, d, "lora_b", bf, per * N),
+        _dev(scale, d, "scale", _F32, 4 * n_adapters), T, S, n_adapters, rank, N, K,
+        _dev(du, d, "du", bf, 2 * T * rank), _dev(dx, d, "dx", bf, T and 2 * ((T - 1) * lddx + K)), lddx,
+        _dev(d_lora_a, d, "d_lora_a", bf, per * K), _dev(d_lora_b, d, "d_lora_b", bf, per * N),
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
 
 
 def moe_debug_stall_next_tc_ffn(calls: int):
