@@ -15,6 +15,24 @@ def N():
     return _native
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: calls that pass the checks end for want of a device")
+@pytest.mark.parametrize("T", [4, 40, 700, 5000])
+def test_calls_without_a_device_end_with_an_error(N, T):
+    n, k = 1024, 1032
+    for f32 in (0, N.MOE_GEMM_OUT_F32):
+        calls = [N.lib.moe_grouped_gemm(P, k, P, P, n * k, T, 2, n, k, f32, P, n, P, BIG, None),
+                 N.lib.moe_grouped_gemm_dgrad(P, n, P, P, n * k, T, 2, n, k, f32, P, k, P, BIG, None),
+                 N.lib.moe_grouped_gemm_wgrad(P, n, P, k, P, T, 2, n, k, f32, P, n * k, P, BIG, None),
+                 N.lib.moe_grouped_gemm_wgrad(P, n, P, k, P, 0, 2, n, k, f32, P, n * k, P, BIG, None)]
+        assert all(st in (N.MOE_ERR_UNSUPPORTED, N.MOE_ERR_CUDA) for st in calls), calls
+    for S in (1, 3):
+        for r in (16, 128):
+            calls = [N.lib.moe_lora_linear(P, k, P, P, P, P, P, None, T, S, 3, r, n, k, P, P, n, P, BIG, None),
+                     N.lib.moe_lora_linear_backward(P, n, P, k, P, P, P, P, P, P, None, T, S, 3, r, n, k, P, P, k, P, P, P, BIG, None),
+                     N.lib.moe_lora_linear_backward(P, n, P, k, P, P, P, P, P, P, None, T, S, 3, r, n, k, P, None, k, P, P, P, BIG, None)]
+            assert all(st in (N.MOE_ERR_UNSUPPORTED, N.MOE_ERR_CUDA) for st in calls), calls
+
+
 class _NoCuda:
     """torch's C layer where its CUDA functions are missing or raise."""
     def __init__(self, error):

@@ -54,6 +54,10 @@ __device__ __forceinline__ int first_segment(const int32_t *off, int segs, int r
 // last segment's end). Several segments share it if one starts strictly inside;
 // the first that does owns the block.
 
+// MOE_OK, or MOE_ERR_UNSUPPORTED where the current device is not sm_100 or the
+// driver encodes no tensor maps (also: there is none).
+int check_device(const char *what);
+
 // A BF16 tensor map with the 128-byte swizzle: dimension 0 contiguous, the
 // others with strides in elements; out-of-range elements read as zero.
 bool map_bf16(CUtensorMap *m, const void *base, int nd, const int64_t (&dim)[4], const int64_t (&stride)[3],

@@ -867,6 +867,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 }  // namespace gt
 
+int check_device(const char *what) {
+  int dev = 0, major = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  if (major != 10) return set_error(MOE_ERR_UNSUPPORTED, "%s: needs sm_100", what);
+  if (!tensor_map_encoder()) return set_error(MOE_ERR_UNSUPPORTED, "%s: cuTensorMapEncodeTiled is not available", what);
+  return MOE_OK;
+}
+
 static bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *base, int nd, const int64_t (&dim)[4],
                        const int64_t (&stride)[3], const int (&box)[4]) {
   cuuint64_t d[4], st[3];
@@ -941,11 +950,8 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
 }
 
 int launch_gemm_tc(GemmMode mode, const TcGemmArgs &a, const TcGemmOperands &op, cudaStream_t s, const char *what) {
-  int dev = 0, major = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (major != 10) return set_error(MOE_ERR_UNSUPPORTED, "%s: needs sm_100", what);
-  if (!tensor_map_encoder()) return set_error(MOE_ERR_UNSUPPORTED, "%s: cuTensorMapEncodeTiled is not available", what);
+  const int st = check_device(what);
+  if (st != MOE_OK) return st;
   // the tile list is counted in 32 bits
   const int64_t cols = (int64_t(a.M) + 255) / 256;
   const int64_t rows = mode == GEMM_WGRAD ? int64_t(a.groups) * ((int64_t(a.NC) + 255) / 256) : int64_t(a.R) / a.bn + a.groups;

@@ -819,6 +819,8 @@ struct Rows {
 template <int BJ, bool TRANS, int ROWS>
 static int launch_shrink_as(const ShrinkArgs &a, const Rows &z, const uint16_t *p, cudaStream_t s, const char *what) {
   using Cfg = ShrinkCfg<BJ, TRANS, ROWS>;
+  int st = check_device(what);
+  if (st != MOE_OK) return st;
   CUtensorMap tz, tp;
   bool ok = map_bf16(&tz, z.p, 2, {z.width, a.T, 1, 1}, {z.ld, 0, 0}, {64, ROWS, 1, 1});
   if (TRANS)
@@ -826,7 +828,7 @@ static int launch_shrink_as(const ShrinkArgs &a, const Rows &z, const uint16_t *
   else
     ok &= map_bf16(&tp, p, 3, {a.C, a.rank, a.n_adapters, 1}, {a.C, int64_t(a.C) * a.rank, 0}, {64, BJ, 1, 1});
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, ROWS>), Cfg::SMEM, what);
+  st = allow_dynamic_smem(reinterpret_cast<const void *>(shrink_kernel<BJ, TRANS, ROWS>), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
   const dim3 grid(unsigned((a.T + ROWS - 1) / ROWS) + unsigned(a.segs), unsigned((a.rank + BJ - 1) / BJ));
   const cudaError_t e = launch_pdl(shrink_kernel<BJ, TRANS, ROWS>, grid, dim3(CONSUMERS + 32), Cfg::SMEM, s, a, tz, tp);
@@ -854,6 +856,8 @@ static int proj_parts(int tiles, int nc);
 template <bool TRANS, int ROWS>
 static int launch_proj_as(const ProjArgs &a, const Rows &z, const uint16_t *w, cudaStream_t s, const char *what) {
   using Cfg = ProjCfg<TRANS, ROWS>;
+  int st = check_device(what);
+  if (st != MOE_OK) return st;
   CUtensorMap tz, tw;
   bool ok = map_bf16(&tz, z.p, 2, {z.width, a.T, 1, 1}, {z.ld, 0, 0}, {64, ROWS, 1, 1});
   if (TRANS)
@@ -862,7 +866,7 @@ static int launch_proj_as(const ProjArgs &a, const Rows &z, const uint16_t *w, c
     ok &= map_bf16(&tw, w, 2, {a.C, a.M, 1, 1}, {a.C, 0, 0}, {64, Cfg::BJ, 1, 1});
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
   auto *kernel = proj_kernel<TRANS, ROWS>;
-  const int st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg::SMEM, what);
+  st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg::SMEM, what);
   if (st != MOE_OK) return st;
   const int tiles = (a.M + Cfg::BJ - 1) / Cfg::BJ, row_tiles = (a.T + ROWS - 1) / ROWS;
   const int parts = proj_parts(tiles * row_tiles, (a.C + Cfg::CC - 1) / Cfg::CC);
@@ -919,6 +923,8 @@ template <int RJ, int AG_ROWS>
 static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &dy, const Rows &u,
                                   const Rows &du, cudaStream_t s, const char *what) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
+  int st = check_device(what);
+  if (st != MOE_OK) return st;
   AdapterGradMaps maps;
   bool ok = true;
   const Rows *r[4] = {&x, &dy, &u, &du};
@@ -935,7 +941,7 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   ny = ny > a.n_adapters ? a.n_adapters : ny;
   a.stages = slabs * ny <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
   const dim3 grid{unsigned(slabs), unsigned(ny)};
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
+  st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
   if (st != MOE_OK) return st;
   const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ, AG_ROWS>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
                                    maps);
