@@ -406,6 +406,18 @@ int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy,
                              size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * The five calls above with their arguments as one host array of 64-bit words,
+ * in the order of their declarations: sizes, strides and flags as they are,
+ * addresses and the stream as integers (NULL as 0). For bindings that pay for
+ * each argument they convert.
+ */
+int moe_grouped_gemm_words(const int64_t *words);         /* 15 words */
+int moe_grouped_gemm_dgrad_words(const int64_t *words);   /* 15 */
+int moe_grouped_gemm_wgrad_words(const int64_t *words);   /* 15 */
+int moe_lora_linear_words(const int64_t *words);          /* 20 */
+int moe_lora_linear_backward_words(const int64_t *words); /* 25 */
+
+/*
  * Test hook for the failure path of the tensor-core FFN: the next `calls`
  * tensor-core launches run with producers that never publish a stage, so the
  * kernels' bounded waits (about two seconds each) run out, the kernels drain

@@ -212,3 +212,47 @@ def test_no_rows_reach_nothing(N, cpu):
     N.moe_grouped_gemm_dgrad(few, n, off, few, n * k, 0, E, n, k, 0, few, k, ws, 256, 0)
     N.moe_grouped_gemm_wgrad(few, n, few, k, off, 0, E, n, k, 0, torch.zeros(E, n, k, dtype=BF), n * k, ws, 256, 0)
     assert len(cpu) == 3
+
+
+# ---- the calls by words: the same answers as the calls themselves
+
+WORDS = [
+    ("moe_grouped_gemm", (P, 64, P, P, 64 * 32, 4, 2, 32, 64, 0, P, 32, P, BIG, 0)),
+    ("moe_grouped_gemm_dgrad", (P, 32, P, P, 64 * 32, 4, 2, 32, 64, 0, P, 64, P, BIG, 0)),
+    ("moe_grouped_gemm_wgrad", (P, 32, P, 64, P, 4, 2, 32, 64, 0, P, 64 * 32, P, BIG, 0)),
+    ("moe_lora_linear", (P, 64, P, P, P, P, P, 0, 4, 2, 3, 16, 32, 64, P, P, 32, P, BIG, 0)),
+    ("moe_lora_linear_backward", (P, 32, P, 64, P, P, P, P, P, P, 0, 4, 2, 3, 16, 32, 64, P, P, 64, P, P, P, BIG, 0)),
+]
+
+
+@pytest.mark.parametrize("name,args", WORDS)
+def test_words_give_the_answers_of_the_call(N, name, args):
+    import struct
+    if torch.cuda.is_available():
+        pytest.skip("what is not refused would run on made-up addresses")
+    call, words = getattr(N.lib, name), getattr(N.lib, name + "_words")
+    refused = 0
+    for i in range(len(args) - 1):            # the stream is not looked at
+        for value in (0, -1, 4, 12, P + 2, (1 << 31) - 1):
+            a = list(args)
+            a[i] = value
+            plain = [v or None if t is N._p else v for v, t in zip(a, N.SIGNATURES[name][1])]
+            st = call(*plain)
+            message = N.lib.moe_last_error() if st else b""
+            got = words(struct.pack(f"{len(a)}q", *a))
+            assert got == st and (N.lib.moe_last_error() if got else b"") == message, (i, value)
+            refused += st in (N.MOE_ERR_SHAPE, N.MOE_ERR_INVALID_ARG)
+    assert refused > 2 * len(args)
+
+
+def test_words_beyond_their_arguments_are_refused(N):
+    import struct
+    for name, args in WORDS:
+        words = getattr(N.lib, name + "_words")
+        sizes = [i for i, t in enumerate(N.SIGNATURES[name][1]) if t is N._i]
+        for i in sizes:
+            a = list(args)
+            a[i] += 1 << 32                   # would be the same number in 32 bits
+            assert words(struct.pack(f"{len(a)}q", *a)) == N.MOE_ERR_SHAPE
+            assert b"32 bits" in N.lib.moe_last_error() and name.encode() in N.lib.moe_last_error()
+        assert words(None) == N.MOE_ERR_INVALID_ARG

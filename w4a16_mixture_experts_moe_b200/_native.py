@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libexactmoe.so")
@@ -73,6 +74,11 @@ SIGNATURES = {
     "moe_lora_workspace_size": (_sz, [_i] * 6),
     "moe_lora_linear": (_i, [_p, _i64] + [_p] * 6 + [_i] * 6 + [_p, _p, _i64, _p, _sz, _p]),
     "moe_lora_linear_backward": (_i, [_p, _i64, _p, _i64] + [_p] * 7 + [_i] * 6 + [_p, _p, _i64, _p, _p, _p, _sz, _p]),
+    "moe_grouped_gemm_words": (_i, [C.c_char_p]),
+    "moe_grouped_gemm_dgrad_words": (_i, [C.c_char_p]),
+    "moe_grouped_gemm_wgrad_words": (_i, [C.c_char_p]),
+    "moe_lora_linear_words": (_i, [C.c_char_p]),
+    "moe_lora_linear_backward_words": (_i, [C.c_char_p]),
     "moe_debug_stall_next_tc_ffn": (_i, [_i]),
     "moe_combine": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_read_device_error": (_i, [_p, _p, C.POINTER(C.c_int32)]),
@@ -111,10 +117,10 @@ def _ptr(x):
 
 def _dev(x, cur, name, kinds, need):
     """_ptr of an argument that a kernel dereferences. A tensor has to live on the current device `cur` (an address
-    that this device cannot reach would fault it), be of one of `kinds` (dtype names; none: any) and hold `need` bytes
+    that this device cannot reach would fault it), be of one of `kinds` (its dtype; none: any) and hold `need` bytes
     from its first element on, whatever strides its view of them has; an address is taken as it is."""
-    if x is None or x.__class__ is int:
-        return x
+    if x is None or isinstance(x, int):
+        return x or 0
     if x.get_device() != cur or (kinds and x.dtype not in kinds) or x.nbytes < need or not x.is_contiguous():
         _dev_slow(x, cur, name, kinds, need)
     return x.data_ptr()
@@ -153,9 +159,10 @@ def _addr(arr):
     return C.cast(arr, C.c_void_p).value
 
 
-def _stream(s):
-    if s is None:  # the raw handle of torch's current stream, without the Stream object around it
-        d = _current_device()
+def _stream(s, d=None):
+    if s is None:  # the raw handle of torch's current stream (on device d), without the Stream object around it
+        if d is None:
+            d = _current_device()
         if d < 0:
             return _torch.cuda.current_stream().cuda_stream  # says why there is none
         return _torch._C._cuda_getCurrentRawStream(d)
@@ -251,34 +258,38 @@ def moe_grouped_gemm_workspace_size(R, E, N, K) -> int:
     return lib.moe_grouped_gemm_workspace_size(R, E, N, K)
 
 
+# Arguments as 64-bit words in one array: ctypes converts an argument in 0.1 us, and these calls have up to 25.
+_words15, _words20, _words25 = (struct.Struct(f"{n}q").pack for n in (15, 20, 25))
+
+
 def moe_grouped_gemm(x, ldx, offsets, w, w_stride, R, E, N, K, flags, y, ldy, ws, ws_bytes, stream=None):
     d = _current_device()
     f32 = flags & MOE_GEMM_OUT_F32
-    _check(lib.moe_grouped_gemm(
+    _check(lib.moe_grouped_gemm_words(_words15(
         _dev(x, d, "x", _BF16, R and 2 * ((R - 1) * ldx + K)), ldx, _dev(offsets, d, "offsets", _I32, 4 * E + 4),
         _dev(w, d, "w", _BF16, R and 2 * ((E - 1) * w_stride + N * K)), w_stride, R, E, N, K, flags,
         _dev(y, d, "y", _F32 if f32 else _BF16, R and (4 if f32 else 2) * ((R - 1) * ldy + N)), ldy,
-        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream, d) or 0)))
 
 
 def moe_grouped_gemm_dgrad(dy, lddy, offsets, w, w_stride, R, E, N, K, flags, dx, lddx, ws, ws_bytes, stream=None):
     d = _current_device()
     f32 = flags & MOE_GEMM_OUT_F32
-    _check(lib.moe_grouped_gemm_dgrad(
+    _check(lib.moe_grouped_gemm_dgrad_words(_words15(
         _dev(dy, d, "dy", _BF16, R and 2 * ((R - 1) * lddy + N)), lddy, _dev(offsets, d, "offsets", _I32, 4 * E + 4),
         _dev(w, d, "w", _BF16, R and 2 * ((E - 1) * w_stride + N * K)), w_stride, R, E, N, K, flags,
         _dev(dx, d, "dx", _F32 if f32 else _BF16, R and (4 if f32 else 2) * ((R - 1) * lddx + K)), lddx,
-        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream, d) or 0)))
 
 
 def moe_grouped_gemm_wgrad(dy, lddy, x, ldx, offsets, R, E, N, K, flags, dw, dw_stride, ws, ws_bytes, stream=None):
     d = _current_device()
     f32 = flags & MOE_GEMM_OUT_F32
-    _check(lib.moe_grouped_gemm_wgrad(
+    _check(lib.moe_grouped_gemm_wgrad_words(_words15(
         _dev(dy, d, "dy", _BF16, R and 2 * ((R - 1) * lddy + N)), lddy, _dev(x, d, "x", _BF16, R and 2 * ((R - 1) * ldx + K)), ldx,
         _dev(offsets, d, "offsets", _I32, 4 * E + 4), R, E, N, K, flags,
         _dev(dw, d, "dw", _F32 if f32 else _BF16, E and (4 if f32 else 2) * ((E - 1) * dw_stride + N * K)), dw_stride,
-        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream, d) or 0)))
 
 
 def moe_lora_workspace_size(T, S, n_adapters, rank, N, K) -> int:
@@ -289,20 +300,20 @@ def moe_lora_linear(x, ldx, w, seg_offsets, seg_adapter, lora_a, lora_b, scale, 
                     ws, ws_bytes, stream=None):
     d = _current_device()
     bf, per = _BF16, 2 * n_adapters * rank
-    _check(lib.moe_lora_linear(
+    _check(lib.moe_lora_linear_words(_words20(
         _dev(x, d, "x", bf, T and 2 * ((T - 1) * ldx + K)), ldx, _dev(w, d, "w", bf, 2 * N * K),
         _dev(seg_offsets, d, "seg_offsets", _I32, 4 * S + 4), _dev(seg_adapter, d, "seg_adapter", _I32, 4 * S),
         _dev(lora_a, d, "lora_a", bf, per * K), _dev(lora_b, d, "lora_b", bf, per * N),
         _dev(scale, d, "scale", _F32, 4 * n_adapters), T, S, n_adapters, rank, N, K,
         _dev(u, d, "u", bf, 2 * T * rank), _dev(y, d, "y", bf, T and 2 * ((T - 1) * ldy + N)), ldy,
-        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream, d) or 0)))
 
 
 def moe_lora_linear_backward(dy, lddy, x, ldx, w, u, seg_offsets, seg_adapter, lora_a, lora_b, scale, T, S, n_adapters,
                              rank, N, K, du, dx, lddx, d_lora_a, d_lora_b, ws, ws_bytes, stream=None):
     d = _current_device()
     bf, per = _BF16, 2 * n_adapters * rank
-    _check(lib.moe_lora_linear_backward(
+    _check(lib.moe_lora_linear_backward_words(_words25(
         _dev(dy, d, "dy", bf, T and 2 * ((T - 1) * lddy + N)), lddy, _dev(x, d, "x", bf, T and 2 * ((T - 1) * ldx + K)), ldx,
         _dev(w, d, "w", bf, 2 * N * K), _dev(u, d, "u", bf, 2 * T * rank),
         _dev(seg_offsets, d, "seg_offsets", _I32, 4 * S + 4), _dev(seg_adapter, d, "seg_adapter", _I32, 4 * S),
@@ -310,7 +321,7 @@ def moe_lora_linear_backward(dy, lddy, x, ldx, w, u, seg_offsets, seg_adapter, l
         _dev(scale, d, "scale", _F32, 4 * n_adapters), T, S, n_adapters, rank, N, K,
         _dev(du, d, "du", bf, 2 * T * rank), _dev(dx, d, "dx", bf, T and 2 * ((T - 1) * lddx + K)), lddx,
         _dev(d_lora_a, d, "d_lora_a", bf, per * K), _dev(d_lora_b, d, "d_lora_b", bf, per * N),
-        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream)))
+        _dev(ws, d, "ws", (), ws_bytes), ws_bytes, _stream(stream, d) or 0)))
 
 
 def moe_debug_stall_next_tc_ffn(calls: int):
