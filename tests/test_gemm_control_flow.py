@@ -92,12 +92,13 @@ struct Meeting {
   }
 };
 
-// n consumers go through groups of stages[g] stages each; consumer c's wait number
-// fail_at[c] (and all behind it) gives up. Behind a group with rows, two more
-// meetings follow, as for the join of partial sums. Returns 0: all of them ended
-// alike, 1: some group was left differently, 2: a meeting that not all came to,
-// 3: rows taken that do not belong to the group.
-extern "C" int run(int n, int groups, const int *stages, const int *fail_at) {
+// n consumers go through groups of stages[g] stages of 10, 11, ... rows; consumer
+// c's wait number fail_at[c] (and all behind it) gives up. Sums pass on behind
+// `most` additions, which takes a meeting, and a group with rows ends with one more.
+// Returns 0: all of them ended alike, 1: some group was left differently, 2: a
+// meeting that not all came to, 3: rows that are not the group's, or too many
+// before a pass.
+extern "C" int run(int n, int groups, const int *stages, const int *fail_at, int most) {
   Meeting meeting;
   meeting.n = n;
   std::vector<std::vector<int>> got(n);
@@ -107,15 +108,24 @@ extern "C" int run(int n, int groups, const int *stages, const int *fail_at) {
     t.emplace_back([&, c] {
       int waits = 0;
       for (int g = 0; g < groups; ++g) {
-        int i = 0, taken = 0;
-        const int r = moe::take_group(
-            [&] { return waits++ >= fail_at[c] ? -1 : i < stages[g] ? 10 + i++ : 0; },
-            [&](int rows) { taken += rows; },
-            [&](bool ok) { return meeting.meet(ok); });
-        got[c].push_back(r);
-        if (r < 0) return;
-        if (taken != 10 * stages[g] + stages[g] * (stages[g] - 1) / 2 || r != (stages[g] > 0)) wrong = 1;
-        if (r) { meeting.meet(true); meeting.meet(true); }
+        int i = 0, passed = 0, r;
+        bool first = true;
+        do {
+          int taken = 0, sums = 0;
+          r = moe::take_stages(
+              most, [&] { return waits++ >= fail_at[c] ? -1 : i < stages[g] ? 10 + i++ : 0; },
+              [&](int rows) { taken += rows; sums += (rows + 15) / 16; },
+              [&](bool ok) { return meeting.meet(ok); });
+          got[c].push_back(r);
+          if (r == moe::TAKEN_GAVE_UP) return;
+          if (sums > most + 3 || (r == moe::TAKEN_MORE && sums < most) || (r == moe::TAKEN_NOTHING && sums)) wrong = 1;
+          if (r == moe::TAKEN_NOTHING) break;
+          meeting.meet(true);
+          passed += taken;
+          first = false;
+        } while (r == moe::TAKEN_MORE);
+        if (passed != 10 * stages[g] + stages[g] * (stages[g] - 1) / 2 || first != (stages[g] == 0)) wrong = 1;
+        if (!first) meeting.meet(true);
       }
     });
   for (auto &x : t) x.join();
@@ -133,28 +143,30 @@ extern "C" void ends(int stages, int issued, int *parity) {
 """)
 
 
-def _run_flow(flow, stages, fail_at):
+def _run_flow(flow, stages, fail_at, most):
     a, b = (C.c_int * len(stages))(*stages), (C.c_int * len(fail_at))(*fail_at)
-    return flow.run(len(fail_at), len(stages), a, b)
+    return flow.run(len(fail_at), len(stages), a, b, most)
 
 
 NEVER = 1 << 30
 
 
-@pytest.mark.parametrize("stages", [[1], [0], [3, 0, 2], [0, 0, 0], [5, 1, 0, 7]])
-def test_groups_without_failures(flow, stages):
-    assert _run_flow(flow, stages, [NEVER] * 8) == 0
+@pytest.mark.parametrize("most", [1, 2, 3, 100])
+@pytest.mark.parametrize("stages", [[1], [0], [3, 0, 2], [0, 0, 0], [5, 1, 0, 7], [40, 2]])
+def test_groups_without_failures(flow, stages, most):
+    assert _run_flow(flow, stages, [NEVER] * 8, most) == 0
 
 
+@pytest.mark.parametrize("most", [1, 2, 100])
 @pytest.mark.parametrize("stages", [[1], [3, 0, 2], [0, 4, 0], [2, 2]])
 @pytest.mark.parametrize("late", [[0], [3], [0, 7], [1, 2, 3, 4, 5, 6, 7], list(range(8))])
-def test_a_wait_that_gives_up_takes_every_consumer_out(flow, stages, late):
+def test_a_wait_that_gives_up_takes_every_consumer_out(flow, stages, late, most):
     """Some consumers' waits give up, at every place where they can, the others' do not (a stage that lands just at
     the limit): all leave at the same group, and none stays at a meeting."""
     for at in range(sum(stages) + len(stages)):
-        assert _run_flow(flow, stages, [at if c in late else NEVER for c in range(8)]) == 0, at
+        assert _run_flow(flow, stages, [at if c in late else NEVER for c in range(8)], most) == 0, at
         # ... and the others one wait later
-        assert _run_flow(flow, stages, [at if c in late else at + 1 for c in range(8)]) == 0, at
+        assert _run_flow(flow, stages, [at if c in late else at + 1 for c in range(8)], most) == 0, at
 
 
 @pytest.mark.parametrize("stages", [2, 3, 7, 12])

@@ -37,3 +37,31 @@ def test_launches_behind_a_call_whose_last_segment_is_cut_to_nothing(M):
     _within(u, ref, K * SUM * mag * (1 + HALF) + HALF * ref.abs(), "u")
     _within(x, new, 8 * SUM * (src.double().abs() @ wx[0].double().abs().T) * (1 + HALF) + HALF * new.abs(), "the next call's rows")
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[1 << 20], [1 << 19, 0, (1 << 19) - 3, 3]])
+def test_gradients_of_an_adapter_with_a_million_rows(M, lens):
+    """All products of one sign, so that what additions cut off adds up. A matrix unit's additions may cut off up to
+    2^-23 of the running sum each, and there are at most 256 and a stage's before a sum passes on: 2^-14.9. The sums
+    passed on, two for each 4096 rows, are rounded to nearest, 2^-24 each: 2^-15. So before its own rounding, half a
+    BF16 step of its binade, a value is within 2^-13.9 of the exact sum of the operands that the call read (with the
+    inner gradient as it rounded it). A sum never passed on loses up to 3e-3."""
+    N = K = 512
+    r, S = 64, len(lens)
+    off = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    T = int(off[-1])
+    x, dy, u, b = (_rand(s, i).abs_().add_(0.5) for i, s in enumerate(((T, K), (T, N), (T, r), (1, N, r))))
+    a, w = _rand((1, r, K), 5), _rand((N, K), 6)
+    ad = torch.zeros(S, dtype=torch.int32, device="cuda")
+    du, da, db = torch.zeros_like(u), torch.zeros_like(a), torch.zeros_like(b)
+    ws = torch.zeros(M.moe_lora_workspace_size(T, S, 1, r, N, K), dtype=torch.uint8, device="cuda")
+    M.moe_lora_linear_backward(dy, N, x, K, w, u, off, ad, a, b, None, T, S, 1, r, N, K, du, None, K, da, db, ws, ws.numel())
+    assert M.moe_read_device_error(ws) == 0
+    ra, rb = torch.zeros(r, K, dtype=torch.float64, device="cuda"), torch.zeros(N, r, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 1 << 16):
+        s = slice(i, i + (1 << 16))
+        ra += du[s].double().T @ x[s].double()   # of the inner gradient as the call rounded it
+        rb += dy[s].double().T @ u[s].double()
+    for got, ref in ((da[0], ra), (db[0], rb)):
+        half = torch.ldexp(torch.ones_like(ref), torch.frexp(ref).exponent - 9)
+        _within(got, ref, half + 2.0 ** -13.9 * ref, "gradient")

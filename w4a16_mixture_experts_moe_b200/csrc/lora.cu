@@ -614,6 +614,12 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   cluster.sync();  // no CTA leaves while its sums are read
 }
 
+__device__ __forceinline__ void add_shared(float *p, float v) {
+  asm volatile("{\n .reg .f32 s;\n ld.shared.f32 s, [%0];\n add.rn.f32 s, s, %1;\n st.shared.f32 [%0], s;\n}\n" ::"r"(tma::smem_u32(p)),
+               "f"(v)
+               : "memory");
+}
+
 struct AdapterGradArgs {
   const int32_t *seg_offsets, *seg_adapter;
   int segs, n_adapters, T, N, K, rank;
@@ -624,6 +630,11 @@ struct AdapterGradArgs {
 };
 
 constexpr int AG_COLS = 64;
+// The matrix unit adds with truncation: its sums pass on to fp32 sums in shared
+// memory, rounded to nearest, behind this many additions of 16 rows' products
+// (gradients of one adapter with a million rows, all products of one sign: off by
+// up to 3.3e-3 of the value beyond the BF16 rounding without, 4e-6 with it).
+constexpr int AG_ADDITIONS = 256;
 
 template <int RJ, int AG_ROWS>
 struct AdapterGradCfg {
@@ -652,8 +663,10 @@ struct AdapterGradMaps {
 // ranks, K = rows (two warps share a chunk's). The rows behind a
 // segment's end are cleared in the fragments. The segments are taken in order
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
+// (Registers for about as many CTAs an SM as the rings leave room for: left to
+// itself the compiler spills at ranks of 16 and takes 132 at 64, one CTA an SM.)
 template <int RJ, int AG_ROWS>
-__global__ void __launch_bounds__(CONSUMERS + 32)
+__global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : RJ <= 64 ? 2 : 1)
     adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ AdapterGradMaps maps) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   extern __shared__ uint8_t smem_raw[];
@@ -713,10 +726,6 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
   const int lo = lane & 7, m8 = (lane >> 3) & 1, hi = lane >> 4;
   for (int ad = blockIdx.y; ad < a.n_adapters; ad += gridDim.y) {
     float acc[RJ / 8][4];
-#pragma unroll
-    for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
     auto release = [&]() {
       __syncwarp();
       if (lane == 0) tma::mbar_arrive(&ring.empty[slot]);
@@ -758,10 +767,44 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       else if (rows > kg * (AG_ROWS / 2)) products(std::true_type{});
       release();
     };
-    // (the meeting at a group's end is also behind the reads of the last group's sums)
-    const int got = take_group(next, stage, consumer_all);
-    if (got < 0) return;
-    if (got == 0) {  // no rows: zeros
+    // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
+    auto at = [&](int j, int q) -> float & {
+      return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8];
+    };
+    bool first = true;
+    int got;
+    do {
+#pragma unroll
+      for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+      // (the meeting at its end is also behind the reads of the last group's sums)
+      got = take_stages(AG_ADDITIONS, next, stage, consumer_all);
+      if (got >= TAKEN_NOTHING) break;
+      if (kg == 1) {
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
+        } else {  // (one after the other: this path is rare, and must not cost the others registers)
+#pragma unroll
+          for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) add_shared(&at(j, q), acc[j][q]);
+        }
+      }
+      consumer_sync();
+      if (kg == 0) {
+#pragma unroll
+        for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+      }
+      first = false;
+    } while (got == TAKEN_MORE);
+    if (got == TAKEN_GAVE_UP) return;
+    if (first) {  // no rows: zeros
       const uint4 zero = make_uint4(0, 0, 0, 0);
       for (int p = tid; p < AG_COLS * a.rank / 8; p += CONSUMERS) {
         if (is_a) {
@@ -772,23 +815,6 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
         }
       }
       continue;
-    }
-    // accumulator (c0, c1) = column g, ranks 2t, 2t+1; (c2, c3) = column g + 8
-    auto at = [&](int j, int q) -> float & {
-      return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8];
-    };
-    if (kg == 1) {
-#pragma unroll
-      for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
-    }
-    consumer_sync();
-    if (kg == 0) {
-#pragma unroll
-      for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
     }
     consumer_sync();
     if (is_a) {  // [rank][K]: 64 columns of each row

@@ -10,20 +10,23 @@
 
 namespace moe {
 
-// Takes a group's stages from the ring. wait(): the rows of the next stage, 0
-// at the group's end, below 0 if the wait gave up. products(rows): takes the
-// stage. all(ok): a meeting of all consumers; whether each of them passed true.
-// Returns 1, 0 for a group without rows, or -1 if any consumer gave up: the same
-// for all, because what follows holds barriers, which a consumer that went
-// another way would leave the others waiting at.
+// Takes a group's stages from the ring, all or the next of them. wait(): the rows
+// of the next stage, 0 at the group's end, below 0 if the wait gave up.
+// products(rows): takes the stage, (rows + 15) / 16 additions to the consumer's
+// sums. all(ok): a meeting of all consumers; whether each of them passed true.
+// Returns how the sums stand, the same for all consumers, because what follows
+// holds barriers, which one that went another way would leave the others waiting
+// at: more of the group follows (behind `most` additions), its end, its end
+// without further rows, or some consumer gave up.
+enum { TAKEN_MORE, TAKEN_END, TAKEN_NOTHING, TAKEN_GAVE_UP };
 template <class Wait, class Products, class All>
-MOE_FLOW int take_group(Wait wait, Products products, All all) {
-  int any = 0, rows;
+MOE_FLOW int take_stages(int most, Wait wait, Products products, All all) {
+  int sums = 0, rows;
   while ((rows = wait()) > 0) {
     products(rows);
-    any = 1;
+    if ((sums += (rows + 15) / 16) >= most) break;
   }
-  return all(rows == 0) ? any : -1;
+  return !all(rows >= 0) ? TAKEN_GAVE_UP : rows > 0 ? TAKEN_MORE : sums ? TAKEN_END : TAKEN_NOTHING;
 }
 
 // wait(slot, parity) for the last use of each slot of a ring that has been used:
