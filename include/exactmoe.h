@@ -327,12 +327,16 @@ int moe_grouped_bf16_ffn(const moe_bf16 *x, const int32_t *sorted_pair,
  *                MOE_GEMM_ACCUMULATE the product is added to what they hold.
  *                They must not overlap an input.
  *   ws           at least moe_grouped_gemm_workspace_size(R, E, N, K) bytes
- *                (one size for the three), 256-byte aligned, zeroed once before
- *                first use; word 0 is the device error word. Calls that may
- *                overlap on the GPU need a workspace each.
- * Sums are fp32 and rounded once, in an order that depends on the shape alone:
- * equal calls give equal bits. fp32 outputs are within about 1e-6 of the exact
- * sums (2-norms) at any length; what is added to one counts as zero below
+ *                (one size for the three; beyond 256 bytes only a BF16 output
+ *                whose own sums are longer than 16,384 products asks for it),
+ *                256-byte aligned, zeroed once before first use; word 0 is the
+ *                device error word. Calls that may overlap on the GPU need a
+ *                workspace each.
+ * Sums are fp32, in an order that depends on the sizes and offsets alone: equal
+ * calls give equal bits. A BF16 output is rounded once from its sum, which is
+ * within about 1e-4 of the exact one (relative to the sum of magnitudes) at any
+ * length. fp32 outputs add up long sums in parts and are within about 1e-6 of the
+ * exact sums (2-norms) at any length; what is added to one counts as zero below
  * 2^-126. N and K are multiples of 8, strides multiples of 8, pointers 16-byte
  * aligned. R may be 0.
  */

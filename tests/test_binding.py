@@ -256,3 +256,27 @@ def test_words_beyond_their_arguments_are_refused(N):
             assert words(struct.pack(f"{len(a)}q", *a)) == N.MOE_ERR_SHAPE
             assert b"32 bits" in N.lib.moe_last_error() and name.encode() in N.lib.moe_last_error()
         assert words(None) == N.MOE_ERR_INVALID_ARG
+
+
+def test_workspace_of_long_reductions(N):
+    """BF16 sums of more than 16,384 products pass through the workspace; a call whose own sums are short, or whose
+    output is fp32, does not ask for that."""
+    small = N.moe_grouped_gemm_workspace_size(16384, 8, 16384, 16384)
+    assert small == 256
+    long = [N.moe_grouped_gemm_workspace_size(*a) for a in ((16385, 8, 64, 64), (8, 8, 16392, 64), (8, 8, 64, 16392))]
+    assert long == [long[0]] * 3 and long[0] > small + 100 * 256 * 128 * 4
+    L, ok = 16392, (N.MOE_ERR_UNSUPPORTED, N.MOE_ERR_CUDA)
+    fwd = lambda n, k, flags, size: N.lib.moe_grouped_gemm(P, k, P, P, n * k, 400, 2, n, k, flags, P, n, P, size, None)
+    dgrad = lambda n, k, flags, size: N.lib.moe_grouped_gemm_dgrad(P, n, P, P, n * k, 400, 2, n, k, flags, P, k, P, size, None)
+    wgrad = lambda r, flags, size: N.lib.moe_grouped_gemm_wgrad(P, 64, P, 64, P, r, 2, 64, 64, flags, P, 64 * 64, P, size, None)
+    f32 = N.MOE_GEMM_OUT_F32
+    for call in (lambda s: fwd(64, L, 0, s), lambda s: dgrad(L, 64, 0, s), lambda s: wgrad(L, 0, s)):
+        assert call(long[0] - 1) == N.MOE_ERR_INVALID_ARG and b"workspace" in N.lib.moe_last_error()
+        assert torch.cuda.is_available() or call(long[0]) in ok
+    if not torch.cuda.is_available():
+        for call in (lambda s: fwd(L, 64, 0, s), lambda s: dgrad(64, L, 0, s), lambda s: fwd(64, L, f32, s),
+                     lambda s: dgrad(L, 64, f32, s), lambda s: wgrad(L, f32, s), lambda s: wgrad(16384, 0, s)):
+            assert call(256) in ok
+    base = N.moe_lora_workspace_size(400, 3, 2, 16, 4096, 4096)
+    assert N.moe_lora_workspace_size(400, 1, 2, 16, 64, L) == N.moe_lora_workspace_size(400, 1, 2, 16, L, 64) == long[0]
+    assert N.moe_lora_workspace_size(400, 3, 2, 16, 64, L) == long[0] + (base - 256 - 1600) // 4096 * L + 1600

@@ -26,12 +26,11 @@ def _compile(tmp, source):
 def parts(tmp_path_factory):
     return _compile(str(tmp_path_factory.mktemp("parts")), """
 #include "gemm_parts.h"
-extern "C" int parts(int steps) { return moe::reduction_parts<true>(steps); }
-extern "C" int whole(int steps) { return moe::reduction_parts<false>(steps); }
+extern "C" int parts(int steps, int f32) { return f32 ? moe::reduction_parts<true>(steps) : moe::reduction_parts<false>(steps); }
 extern "C" int start(int steps, int parts, int p) { return moe::part_start(steps, parts, p); }
 // 0: parts begin at 0, end at `steps`, rise, and hold 1 to `most` k-steps each
-extern "C" int check(int steps, int most) {
-  const int n = moe::reduction_parts<true>(steps);
+extern "C" int check(int steps, int most, int f32) {
+  const int n = parts(steps, f32);
   if (moe::part_start(steps, n, 0) != 0) return 1;
   if (moe::part_start(steps, n, n) != steps) return 2;
   for (int p = 0; p < n; ++p) {
@@ -44,19 +43,17 @@ extern "C" int check(int steps, int most) {
 
 
 # up to 2^24 k-steps of 64: 2^30 rows in one group
-@pytest.mark.parametrize("steps", [17, 18, 28, 29, 224, 1025, 16384, 173_399, 173_400, 175_000, 1 << 20, (1 << 24) - 1, 1 << 24])
+@pytest.mark.parametrize("steps", [17, 18, 28, 29, 224, 257, 512, 513, 1025, 16384, 173_399, 173_400, 175_000, 1 << 20, (1 << 24) - 1, 1 << 24])
 def test_parts_cover_long_reductions(parts, steps):
-    assert parts.check(steps, 14) == 0
+    assert parts.check(steps, 14, 1) == 0
+    assert parts.check(steps, 256, 0) == 0
 
 
-@pytest.mark.parametrize("steps", [1, 2, 15, 16])
-def test_short_reductions_are_one_part(parts, steps):
-    assert parts.parts(steps) == 1 and parts.start(steps, 1, 0) == 0 and parts.start(steps, 1, 1) == steps
-
-
-@pytest.mark.parametrize("steps", [1, 17, 1 << 24])
-def test_16_bit_outputs_are_one_part(parts, steps):
-    assert parts.whole(steps) == 1
+@pytest.mark.parametrize("f32,most", [(1, 16), (0, 256)])
+def test_short_reductions_are_one_part(parts, f32, most):
+    for steps in (1, 2, most - 1, most):
+        assert parts.parts(steps, f32) == 1 and parts.start(steps, 1, 0) == 0 and parts.start(steps, 1, 1) == steps
+    assert parts.parts(most + 1, f32) > 1
 
 
 @pytest.fixture(scope="module")

@@ -5,7 +5,7 @@ of the value."""
 import pytest
 import torch
 
-from tests.test_gpu_lora import HALF, SUM, _rand, _within
+from tests.test_gpu_lora import HALF, SUM, Problem, _rand, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -63,5 +63,63 @@ def test_gradients_of_an_adapter_with_a_million_rows(M, lens):
         ra += du[s].double().T @ x[s].double()   # of the inner gradient as the call rounded it
         rb += dy[s].double().T @ u[s].double()
     for got, ref in ((da[0], ra), (db[0], rb)):
-        half = torch.ldexp(torch.ones_like(ref), torch.frexp(ref).exponent - 9)
-        _within(got, ref, half + 2.0 ** -13.9 * ref, "gradient")
+        _within(got, ref, _half_step(ref) + 2.0 ** -13.9 * ref, "gradient")
+
+
+def _half_step(ref):
+    return torch.ldexp(torch.ones_like(ref), torch.frexp(ref.abs()).exponent - 9)
+
+
+@pytest.mark.parametrize("direction,counts,N,K", [
+    ("wgrad", [1 << 20], 256, 264), ("wgrad", [40_000, 0, 32_769, 100, 32_768, 77], 520, 328),
+    ("wgrad", [16_384, 16_385, 0, 16_400], 72, 136),
+    ("fwd", [300, 0, 45], 264, 80_008), ("dgrad", [300, 17], 32_776, 264), ("dgrad", [5, 40], 16_392, 1032)])
+def test_long_reductions_of_bf16_outputs(M, direction, counts, N, K):
+    """All products of one sign, so that what additions cut off adds up. A part of a reduction has at most 256 k-steps,
+    1024 additions of 16 products. Each cuts the products and the running sum off at the sum's last place, and as the
+    sum grows evenly to its end, loses 1e-7 of that end on average, below 2^-23: 2^-13 a part. Parts are added rounded
+    to nearest, 2^-24 each for at most 64 parts: 2^-18. So before its own rounding, half a BF16 step of its binade, a
+    value is within 2^-12.9 of the exact sum."""
+    E, R = len(counts), sum(counts)
+    off_l = [sum(counts[:i]) for i in range(E + 1)]
+    off = torch.tensor(off_l, dtype=torch.int32, device="cuda")
+    x, dy, w = (_rand(s, i).abs_().add_(0.5) for i, s in enumerate(((R, K), (R, N), (E, N, K))))
+    ws = torch.zeros(M.moe_grouped_gemm_workspace_size(R, E, N, K), dtype=torch.uint8, device="cuda")
+    out = torch.full({"fwd": (R, N), "dgrad": (R, K), "wgrad": (E, N, K)}[direction], 3.0, dtype=torch.bfloat16, device="cuda")
+    def call():
+        if direction == "fwd":
+            M.moe_grouped_gemm(x, K, off, w, N * K, R, E, N, K, 0, out, N, ws, ws.numel())
+        elif direction == "dgrad":
+            M.moe_grouped_gemm_dgrad(dy, N, off, w, N * K, R, E, N, K, 0, out, K, ws, ws.numel())
+        else:
+            M.moe_grouped_gemm_wgrad(dy, N, x, K, off, R, E, N, K, 0, out, N * K, ws, ws.numel())
+    call()
+    assert M.moe_read_device_error(ws) == 0
+    for e in range(E):
+        r = slice(off_l[e], off_l[e + 1])
+        if direction == "wgrad":
+            got, ref = out[e], torch.zeros(N, K, dtype=torch.float64, device="cuda")
+            for i in range(off_l[e], off_l[e + 1], 1 << 16):
+                s = slice(i, min(i + (1 << 16), off_l[e + 1]))
+                ref += dy[s].double().T @ x[s].double()
+        else:
+            got, ref = out[r], x[r].double() @ w[e].double().T if direction == "fwd" else dy[r].double() @ w[e].double()
+        _within(got, ref, _half_step(ref) + 2.0 ** -12.9 * ref, f"{direction} {e}")
+    first = out.clone()
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("N,K", [(136, 40_008), (40_008, 136)])
+def test_adapters_beside_a_long_projection(M, N, K):
+    # the reduction in parts, with adapters' k-steps behind the last and blocks that segments share
+    p = Problem([300, 3, 0, 90, 411], [1, 0, -1, -1, 1], 2, 24, N, K, tail=5, seed=3)
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_forward()
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_backward()

@@ -29,6 +29,7 @@ struct TcGemmArgs {
   const float *delta;
   int delta_by_seg;
   const int32_t *row_seg;  // [R] the rows' segments (with delta)
+  float *sums;  // what the parts of a long reduction add up in (long_sums_bytes), BF16 outputs
   int late;  // the launches before this one wait for everything but u / du, delta and the output
   int32_t *err;
 };
@@ -57,6 +58,9 @@ __device__ __forceinline__ int first_segment(const int32_t *off, int segs, int r
 // MOE_OK, or MOE_ERR_UNSUPPORTED where the current device is not sm_100 or the
 // driver encodes no tensor maps (also: there is none).
 int check_device(const char *what);
+
+// Workspace of the engine's BF16 outputs for reductions of up to `length` products.
+size_t long_sums_bytes(int length);
 
 // A BF16 tensor map with the 128-byte swizzle: dimension 0 contiguous, the
 // others with strides in elements; out-of-range elements read as zero.

@@ -345,6 +345,21 @@ __device__ __forceinline__ void add_shared_block(const TcGemmArgs &a, int row, i
   for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + add[j]);
 }
 
+// Part p of a long reduction: adds what the parts before it left in the workspace
+// to 16 accumulator rows of one column, and leaves them there itself unless it
+// is the last (true: nothing to store yet). A thread meets its own values only.
+__device__ __forceinline__ bool add_part(const TcGemmArgs &a, int p, int parts, int row, int col, uint32_t (&v)[16]) {
+  float *s = a.sums + (int64_t(blockIdx.x) * BN + row) * BMC + col;
+  if (p > 0) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + s[j * BMC]);
+  }
+  if (p + 1 == parts) return false;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s[j * BMC] = __uint_as_float(v[j]);
+  return true;
+}
+
 __device__ __forceinline__ void out_sync(int part) {
   asm volatile("bar.sync %0, 128;" ::"r"(OUT_BAR + part) : "memory");
 }
@@ -459,11 +474,11 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
     };
     bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
     const int parts = reduction_parts<F32>(nsteps);
-    int part = 0, part_end = part_start(nsteps, parts, 1);
+    int part = 0, part_end = parts == 1 ? nsteps : part_start(nsteps, parts, 1);
     bool part_first = true;
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
       if (ADAPTERS<MODE, F32> && ks + 1 == nsteps) { more = next_seg(); known = true; }
-      const bool part_last = ks + 1 == (F32 ? part_end : nsteps);
+      const bool part_last = ks + 1 == part_end;
       uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
       const int left = min(BK, red - ks * BK);
       const bool fix = MODE == GEMM_WGRAD && (left & 15);
@@ -511,8 +526,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       }
       __syncwarp();
       next();
-      part_first = F32 && part_last;
-      if (F32 && part_last) part_end = part_start(nsteps, parts, ++part + 1);
+      part_first = part_last;
+      if (part_last && parts > 1) part_end = part_start(nsteps, parts, ++part + 1);
     }
     if constexpr (ADAPTERS<MODE, F32>) {
       if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
@@ -681,6 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0;
           }
+          if (!F32 && parts > 1 && add_part(a, p, parts, j0, q * 32 + lane, v)) return;
           const int n = min(16, tl.nvalid - j0);
           if (ADAPTERS<MODE, F32> && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
           store_block<F32>(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
@@ -720,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
           const int rows = min(OUT_ROWS, tl.nvalid - j0);
-          if ((MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
+          if (parts == 1 && (MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
               !(ADAPTERS<MODE, F32> && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
             // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
             // warps write 128 columns of them to shared memory, one thread sends
@@ -866,6 +882,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace gt
+
+// Every CTA of the grid keeps one tile's sums.
+size_t long_sums_bytes(int length) {
+  return length > BF16_WHOLE * gt::BK ? size_t(sm_count() & ~1) * gt::BN * gt::BMC * 4 : 0;
+}
 
 int check_device(const char *what) {
   int dev = 0, major = 0;

@@ -20,8 +20,9 @@ static bool use_gemv(int R, int E, int N) {
   return int64_t(R) <= int64_t(E) * (most < 2 ? 2 : most > 32 ? 32 : most);
 }
 
-static int check_grouped(const char *who, int R, int E, int N, int K, int flags, const void *offsets, const void *ws,
-                         size_t ws_bytes) {
+// `reduction`: the length of the direction's sums.
+static int check_grouped(const char *who, int R, int E, int N, int K, int reduction, int flags, const void *offsets,
+                         const void *ws, size_t ws_bytes) {
   if (R < 0 || R > (1 << 30) || E < 1 || E > MAX_E)
     return set_error(MOE_ERR_SHAPE, "%s: R=%d E=%d (need 0<=R<=2^30, 1<=E<=256)", who, R, E);
   if (N < 8 || K < 8 || N % 8 || K % 8)
@@ -32,7 +33,7 @@ static int check_grouped(const char *who, int R, int E, int N, int K, int flags,
     return set_error(MOE_ERR_INVALID_ARG, "%s: MOE_GEMM_ACCUMULATE needs MOE_GEMM_OUT_F32", who);
   if (!offsets || !ws) return set_error(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(ws, 256)) return set_error(MOE_ERR_INVALID_ARG, "%s: ws needs 256-byte alignment", who);
-  const size_t need = moe_grouped_gemm_workspace_size(R, E, N, K);
+  const size_t need = WS_HEADER + ((flags & MOE_GEMM_OUT_F32) ? 0 : long_sums_bytes(reduction));
   if (ws_bytes < need) return set_error(MOE_ERR_INVALID_ARG, "%s: workspace %zu B < %zu B", who, ws_bytes, need);
   return MOE_OK;
 }
@@ -58,14 +59,16 @@ static TcGemmArgs grouped_args(const int32_t *offsets, int R, int E, int flags, 
   a.out = out;
   a.ldo = ldo;
   a.err = static_cast<int32_t *>(ws);
+  a.sums = reinterpret_cast<float *>(static_cast<char *>(ws) + WS_HEADER);  // there if a reduction is long
   return a;
 }
 
 }  // namespace moe
 
 extern "C" size_t moe_grouped_gemm_workspace_size(int R, int E, int N, int K) {
-  (void)R; (void)E; (void)N; (void)K;
-  return moe::WS_HEADER;
+  (void)E;
+  const int most = R > N ? R : N;  // the longest reduction of the three directions
+  return moe::WS_HEADER + moe::long_sums_bytes(most > K ? most : K);
 }
 
 extern "C" int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *offsets, const moe_bf16 *w,
@@ -74,7 +77,7 @@ extern "C" int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *o
   moe::NvtxScope nvtx_scope("moe_grouped_gemm");
   using namespace moe;
   const char *who = "moe_grouped_gemm";
-  int st = check_grouped(who, R, E, N, K, flags, offsets, ws, ws_bytes);
+  int st = check_grouped(who, R, E, N, K, K, flags, offsets, ws, ws_bytes);
   if (st != MOE_OK || R == 0) return st;
   if ((st = check_matrix(who, "x", x, ldx, K)) != MOE_OK || (st = check_matrix(who, "y", y, ldy, N)) != MOE_OK ||
       (st = check_matrix(who, "w", w, w_stride, int64_t(N) * K)) != MOE_OK)
@@ -103,7 +106,7 @@ extern "C" int moe_grouped_gemm_dgrad(const moe_bf16 *dy, int64_t lddy, const in
   moe::NvtxScope nvtx_scope("moe_grouped_gemm_dgrad");
   using namespace moe;
   const char *who = "moe_grouped_gemm_dgrad";
-  int st = check_grouped(who, R, E, N, K, flags, offsets, ws, ws_bytes);
+  int st = check_grouped(who, R, E, N, K, N, flags, offsets, ws, ws_bytes);
   if (st != MOE_OK || R == 0) return st;
   if ((st = check_matrix(who, "dy", dy, lddy, N)) != MOE_OK || (st = check_matrix(who, "dx", dx, lddx, K)) != MOE_OK ||
       (st = check_matrix(who, "w", w, w_stride, int64_t(N) * K)) != MOE_OK)
@@ -120,7 +123,7 @@ extern "C" int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const mo
   moe::NvtxScope nvtx_scope("moe_grouped_gemm_wgrad");
   using namespace moe;
   const char *who = "moe_grouped_gemm_wgrad";
-  int st = check_grouped(who, R, E, N, K, flags, offsets, ws, ws_bytes);
+  int st = check_grouped(who, R, E, N, K, R, flags, offsets, ws, ws_bytes);
   if (st != MOE_OK) return st;
   if ((st = check_matrix(who, "dw", dw, dw_stride, int64_t(N) * K)) != MOE_OK) return st;
   cudaStream_t s = as_stream(stream);

@@ -992,9 +992,13 @@ static size_t delta_rows(int T, int S) {
   return by_seg < by_row ? by_seg : by_row;
 }
 
-// The rows' segments, behind those sums.
+// The workspace: the error word, what long reductions of the engine add up in,
+// those sums, and the rows' segments.
+static char *shared_sums(int N, int K, void *ws) {
+  return static_cast<char *>(ws) + WS_HEADER + long_sums_bytes(N > K ? N : K);
+}
 static int32_t *row_segments(int T, int S, int N, int K, void *ws) {
-  return reinterpret_cast<int32_t *>(static_cast<char *>(ws) + WS_HEADER + delta_rows(T, S) * size_t(N > K ? N : K) * 4);
+  return reinterpret_cast<int32_t *>(shared_sums(N, K, ws) + delta_rows(T, S) * size_t(N > K ? N : K) * 4);
 }
 
 // The arguments both entry points share.
@@ -1076,6 +1080,7 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
   g.ldo = ldo;
   g.late = 1;
   g.err = err;
+  g.sums = reinterpret_cast<float *>(reinterpret_cast<char *>(err) + WS_HEADER);  // there if N or K is long
   return g;
 }
 
@@ -1084,7 +1089,7 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
 template <bool COLS>
 static int shared_blocks(TcGemmArgs &g, int T, int S, int N, int K, void *ws, cudaStream_t s, const char *what) {
   if (S < 2) return MOE_OK;
-  g.delta = reinterpret_cast<const float *>(static_cast<char *>(ws) + WS_HEADER);
+  g.delta = reinterpret_cast<const float *>(shared_sums(N, K, ws));
   g.delta_by_seg = int64_t(S) * 16 < (int64_t(T) + 15) / 16 * 16;
   g.row_seg = row_segments(T, S, N, K, ws);
   const DeltaArgs d = {g.offsets, g.adapter, g.row_seg, g.ext_b, g.ext_a, S, g.n_adapters, T, g.rank, g.M, g.delta_by_seg,
@@ -1097,7 +1102,8 @@ static int shared_blocks(TcGemmArgs &g, int T, int S, int N, int K, void *ws, cu
 
 extern "C" size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K) {
   (void)n_adapters; (void)rank;
-  return moe::WS_HEADER + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4 + (T < 1 || S < 2 ? 0 : size_t(T) * 4);
+  return moe::WS_HEADER + moe::long_sums_bytes(N > K ? N : K) + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4 +
+         (T < 1 || S < 2 ? 0 : size_t(T) * 4);
 }
 
 extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w, const int32_t *seg_offsets,
