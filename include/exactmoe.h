@@ -337,7 +337,7 @@ int moe_grouped_bf16_ffn(const moe_bf16 *x, const int32_t *sorted_pair,
  * within about 1e-4 of the exact one (relative to the sum of magnitudes) at any
  * length. fp32 outputs add up long sums in parts and are within about 1e-6 of the
  * exact sums (2-norms) at any length; what is added to one counts as zero below
- * 2^-126. N and K are multiples of 8, strides multiples of 8, pointers 16-byte
+ * 2^-126. N and K are multiples of 8 up to 2^30, strides multiples of 8, pointers 16-byte
  * aligned. R may be 0.
  */
 size_t moe_grouped_gemm_workspace_size(int R, int E, int N, int K);
@@ -389,7 +389,7 @@ int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
  *                word. Calls that may overlap on the GPU need a workspace each.
  * Sums are fp32; u and du are rounded to BF16 once, as operands of the product
  * they enter, and every other output once at the end. Equal calls give equal
- * bits. N and K are multiples of 8, rank a multiple of 8 from 8 to 128, S <=
+ * bits. N and K are multiples of 8 up to 2^30, rank a multiple of 8 from 8 to 128, S <=
  * 65535, strides multiples of 8, pointers 16-byte aligned. T and S may be 0.
  */
 size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K);

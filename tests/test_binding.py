@@ -280,3 +280,16 @@ def test_workspace_of_long_reductions(N):
     base = N.moe_lora_workspace_size(400, 3, 2, 16, 4096, 4096)
     assert N.moe_lora_workspace_size(400, 1, 2, 16, 64, L) == N.moe_lora_workspace_size(400, 1, 2, 16, L, 64) == long[0]
     assert N.moe_lora_workspace_size(400, 3, 2, 16, 64, L) == long[0] + (base - 256 - 1600) // 4096 * L + 1600
+
+
+def test_columns_beyond_the_kernels_arithmetic_are_refused(N):
+    most = 1 << 30
+    for n, k in ((most + 8, 8), (8, most + 8), ((1 << 31) - 8, 8), (8, (1 << 31) - 8)):
+        size, st = 1 << 60, N.MOE_ERR_SHAPE
+        for R in (1, 400):
+            assert N.lib.moe_grouped_gemm(P, k, P, P, n * k, R, 1, n, k, 0, P, n, P, size, None) == st
+            assert N.lib.moe_grouped_gemm_dgrad(P, n, P, P, n * k, R, 1, n, k, 0, P, k, P, size, None) == st
+            assert N.lib.moe_grouped_gemm_wgrad(P, n, P, k, P, R, 1, n, k, 0, P, n * k, P, size, None) == st
+            assert N.lib.moe_lora_linear(P, k, P, P, P, P, P, None, R, 1, 1, 8, n, k, P, P, n, P, size, None) == st
+            assert N.lib.moe_lora_linear_backward(P, n, P, k, P, P, P, P, P, P, None, R, 1, 1, 8, n, k, P, P, k, P, P, P, size, None) == st
+            assert b"2^30" in N.lib.moe_last_error()

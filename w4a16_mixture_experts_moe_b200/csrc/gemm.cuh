@@ -8,6 +8,9 @@
 
 namespace moe {
 
+// The largest N and K: column counts are rounded up to tiles in 32 bits.
+constexpr int MAX_COLS = 1 << 30;
+
 enum GemmMode { GEMM_FWD = 0, GEMM_DGRAD = 1, GEMM_WGRAD = 2 };
 
 // One product for the tensor-core engine (gemm_tc.cu), passed by value.

@@ -25,8 +25,8 @@ static int check_grouped(const char *who, int R, int E, int N, int K, int reduct
                          const void *ws, size_t ws_bytes) {
   if (R < 0 || R > (1 << 30) || E < 1 || E > MAX_E)
     return set_error(MOE_ERR_SHAPE, "%s: R=%d E=%d (need 0<=R<=2^30, 1<=E<=256)", who, R, E);
-  if (N < 8 || K < 8 || N % 8 || K % 8)
-    return set_error(MOE_ERR_SHAPE, "%s: N=%d K=%d must be positive multiples of 8", who, N, K);
+  if (N < 8 || K < 8 || N % 8 || K % 8 || N > MAX_COLS || K > MAX_COLS)
+    return set_error(MOE_ERR_SHAPE, "%s: N=%d K=%d must be multiples of 8 from 8 to 2^30", who, N, K);
   if (flags & ~(MOE_GEMM_OUT_F32 | MOE_GEMM_ACCUMULATE))
     return set_error(MOE_ERR_INVALID_ARG, "%s: unknown flag bits 0x%x", who, flags);
   if ((flags & MOE_GEMM_ACCUMULATE) && !(flags & MOE_GEMM_OUT_F32))

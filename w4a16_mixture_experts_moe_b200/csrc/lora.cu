@@ -1010,8 +1010,8 @@ static int check_common(const char *who, const void *w, const void *seg_offsets,
                      who, T, S, n_adapters);
   if (rank < 8 || rank > MAX_RANK || rank % 8)
     return set_error(MOE_ERR_SHAPE, "%s: rank=%d must be a multiple of 8 from 8 to 128", who, rank);
-  if (N < 8 || K < 8 || N % 8 || K % 8)
-    return set_error(MOE_ERR_SHAPE, "%s: N=%d K=%d must be positive multiples of 8", who, N, K);
+  if (N < 8 || K < 8 || N % 8 || K % 8 || N > MAX_COLS || K > MAX_COLS)
+    return set_error(MOE_ERR_SHAPE, "%s: N=%d K=%d must be multiples of 8 from 8 to 2^30", who, N, K);
   if (!ws || !w || !lora_a || !lora_b || !seg_offsets || (S > 0 && !seg_adapter))
     return set_error(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(ws, 256) || !aligned(w, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16))
