@@ -423,7 +423,7 @@ __device__ __forceinline__ int sched_pos(int i) {
 // warp issuing both took 490 cycles a k-step, as long as its MMAs.) The warp
 // stays converged and elects the issuing lane, which keeps the loads' operands
 // in uniform registers.
-template <int MODE, bool F32, bool A_SIDE>
+template <int MODE, bool F32, bool LONG, bool A_SIDE>
 __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const Maps &m, uint8_t *smem, uint32_t rank,
                                         int total) {
   int s = 0, round = 0;  // ring slot and its use
@@ -473,12 +473,12 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       return true;
     };
     bool more = false, known = false;  // another adapter step follows (looked up behind the first loads)
-    const int parts = reduction_parts<F32>(nsteps);
+    const int parts = LONG ? reduction_parts<F32>(nsteps) : 1;
     int part = 0, part_end = parts == 1 ? nsteps : part_start(nsteps, parts, 1);
     bool part_first = true;
     for (int ks = 0; ks < nsteps && slot(); ++ks) {
       if (ADAPTERS<MODE, F32> && ks + 1 == nsteps) { more = next_seg(); known = true; }
-      const bool part_last = ks + 1 == part_end;
+      const bool part_last = ks + 1 == (LONG ? part_end : nsteps);
       uint8_t *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
       const int left = min(BK, red - ks * BK);
       const bool fix = MODE == GEMM_WGRAD && (left & 15);
@@ -526,8 +526,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
       }
       __syncwarp();
       next();
-      part_first = part_last;
-      if (part_last && parts > 1) part_end = part_start(nsteps, parts, ++part + 1);
+      part_first = LONG && part_last;
+      if (LONG && part_last && parts > 1) part_end = part_start(nsteps, parts, ++part + 1);
     }
     if constexpr (ADAPTERS<MODE, F32>) {
       if (more && a.late) pdl_wait();  // u is there; returns at once when the launches before are done
@@ -578,7 +578,8 @@ __device__ __forceinline__ void produce(Shared &sh, const TcGemmArgs &a, const M
   __syncwarp();
 }
 
-template <int MODE, bool F32>
+// LONG: some reduction may be longer than one part (fp32 outputs: always taken to be).
+template <int MODE, bool F32, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     gemm_kernel(const TcGemmArgs a, const __grid_constant__ Maps m) {
   extern __shared__ __align__(1024) uint8_t smem[];  // all of the block's shared memory: swizzled tiles first
@@ -675,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int t = sched_pos(i);
       if (t >= total) break;
       const Tile tl = decode_tile<MODE>(sh, a, t);
-      const int parts = reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt(tl.e) : a.KD) + BK - 1) / BK);
+      const int parts = LONG ? reduction_parts<F32>(((MODE == GEMM_WGRAD ? sh.cnt(tl.e) : a.KD) + BK - 1) / BK) : 1;
       for (int p = 0; p < parts; ++p, ++unit) {
         const bool add = F32 && (p > 0 || a.accumulate);
         // what this warp has stored of the tile is there before more is added to it
@@ -696,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0;
           }
-          if (!F32 && parts > 1 && add_part(a, p, parts, j0, q * 32 + lane, v)) return;
+          if (LONG && !F32 && parts > 1 && add_part(a, p, parts, j0, q * 32 + lane, v)) return;
           const int n = min(16, tl.nvalid - j0);
           if (ADAPTERS<MODE, F32> && a.delta) add_shared_block(a, tl.row + j0, n, f, v);
           store_block<F32>(a, base + int64_t(j0) * a.ldo, n, f, fw + 32 <= a.M, add, v);
@@ -736,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         else for (int j0 = part * OUT_ROWS; j0 < tl.nvalid; j0 += 2 * OUT_ROWS) {
           const int rows = min(OUT_ROWS, tl.nvalid - j0);
-          if (parts == 1 && (MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
+          if ((!LONG || parts == 1) && (MODE == GEMM_WGRAD || rows == OUT_ROWS) &&
               !(ADAPTERS<MODE, F32> && a.delta && (shared_block(a, tl.row + j0, 16) || shared_block(a, tl.row + j0 + 16, 16)))) {
             // BF16, 32 rows (wgrad: the map cuts them at the matrix's end): four
             // warps write 128 columns of them to shared memory, one thread sends
@@ -782,9 +783,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     if (F32 ? lane == 0 : issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == A_WARP) {
-    produce<MODE, F32, true>(sh, a, m, smem, rank, total);
+    produce<MODE, F32, LONG, true>(sh, a, m, smem, rank, total);
   } else if (warp == B_WARP) {
-    produce<MODE, F32, false>(sh, a, m, smem, rank, total);
+    produce<MODE, F32, LONG, false>(sh, a, m, smem, rank, total);
   } else if (warp == FIX_WARP) {
     // ================================================================ tails
     if (MODE == GEMM_WGRAD) {
@@ -962,10 +963,13 @@ static int launch_mode(const TcGemmArgs &a, const TcGemmOperands &op, cudaStream
       ok &= map_bf16(&m.eb[i], a.ext_b, 2, {a.rank, a.R, 1, 1}, {a.rank, 0, 0}, {64, 32 << i, 1, 1});
   }
   if (!ok) return set_error(MOE_ERR_INVALID_ARG, "%s: tensor map encoding failed (pointers or strides)", what);
-  int st = allow_dynamic_smem(reinterpret_cast<const void *>(gt::gemm_kernel<MODE, F32>), gt::SMEM, what);
+  // (the parts' code costs calls that need none 1 us: 18 -> 19 us of a projection of 512 rows, K = N = 2048)
+  const bool is_long = F32 || (MODE == GEMM_WGRAD ? a.R : a.KD) > BF16_WHOLE * gt::BK;
+  auto *kernel = is_long ? gt::gemm_kernel<MODE, F32, true> : gt::gemm_kernel<MODE, F32, F32>;
+  int st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), gt::SMEM, what);
   if (st != MOE_OK) return st;
   const int grid = sm_count() & ~1;
-  const cudaError_t e = launch_pdl(gt::gemm_kernel<MODE, F32>, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, m);
+  const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(gt::THREADS), gt::SMEM, s, a, m);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
