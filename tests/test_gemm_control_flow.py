@@ -71,11 +71,13 @@ def flow(tmp_path_factory):
 struct Meeting {
   std::mutex m;
   std::condition_variable cv;
-  int n, in = 0, turn = 0;
-  bool all = true, last = true, stuck = false;
-  bool meet(bool ok) {
+  int n, in = 0, turn = 0, kind = 0;
+  bool all = true, last = true, stuck = false, mixed = false;
+  bool meet(int kind_, bool ok) {
     std::unique_lock<std::mutex> l(m);
     const int mine = turn;
+    if (in && kind != kind_) mixed = true;  // a vote and a plain meeting at once
+    kind = kind_;
     all = all && ok;
     if (++in == n) {
       last = all; all = true; in = 0; ++turn;
@@ -91,44 +93,45 @@ struct Meeting {
 
 // n consumers go through groups of stages[g] stages of 10, 11, ... rows; consumer
 // c's wait number fail_at[c] (and all behind it) gives up. Sums pass on behind
-// `most` additions, which takes a meeting, and a group with rows ends with one more.
-// Returns 0: all of them ended alike, 1: some group was left differently, 2: a
-// meeting that not all came to, 3: rows that are not the group's, or too many
-// before a pass.
+// `most` additions: odd consumers put theirs, even ones add theirs. Returns 0: all
+// of them left alike, 1: some did not, 2: a meeting that not all came to, or that
+// some came to for a vote and some not, 3: group sums that are not the group's.
 extern "C" int run(int n, int groups, const int *stages, const int *fail_at, int most) {
   Meeting meeting;
   meeting.n = n;
-  std::vector<std::vector<int>> got(n);
+  std::vector<int> left(n, -1);
+  std::vector<std::atomic<int>> sum(groups);
+  for (auto &v : sum) v = -1000000;
   std::atomic<int> wrong{0};
   std::vector<std::thread> t;
   for (int c = 0; c < n; ++c)
     t.emplace_back([&, c] {
       int waits = 0;
       for (int g = 0; g < groups; ++g) {
-        int i = 0, passed = 0, r;
-        bool first = true;
-        do {
-          int taken = 0, sums = 0;
-          r = moe::take_stages(
-              most, [&] { return waits++ >= fail_at[c] ? -1 : i < stages[g] ? 10 + i++ : 0; },
-              [&](int rows) { taken += rows; sums += (rows + 15) / 16; },
-              [&](bool ok) { return meeting.meet(ok); });
-          got[c].push_back(r);
-          if (r == moe::TAKEN_GAVE_UP) return;
-          if (sums > most + 3 || (r == moe::TAKEN_MORE && sums < most) || (r == moe::TAKEN_NOTHING && sums)) wrong = 1;
-          if (r == moe::TAKEN_NOTHING) break;
-          meeting.meet(true);
-          passed += taken;
-          first = false;
-        } while (r == moe::TAKEN_MORE);
-        if (passed != 10 * stages[g] + stages[g] * (stages[g] - 1) / 2 || first != (stages[g] == 0)) wrong = 1;
-        if (!first) meeting.meet(true);
+        int i = 0, mine = 0, adds = 0;
+        const int r = moe::sum_group<true>(
+            most, [&] { return waits++ >= fail_at[c] ? -1 : i < stages[g] ? 10 + i++ : 0; }, [&] { mine = adds = 0; },
+            [&](int rows) { mine += rows; adds += (rows + 15) / 16; },
+            [&](bool first) {
+              if (adds > most + 3) wrong = 1;
+              if (c == 1 && first) sum[g] = mine;
+              else if (c == 1) sum[g] += mine;
+            },
+            [&](bool ok) { return meeting.meet(1, ok); }, [&] { if (c == 0) sum[g] += mine; }, [&] { meeting.meet(2, true); });
+        if (r < 0) { left[c] = g; return; }
+        if (r != (stages[g] > 0)) wrong = 1;
+        if (r) {
+          if (sum[g] != 2 * (10 * stages[g] + stages[g] * (stages[g] - 1) / 2)) wrong = 1;
+          meeting.meet(2, true);
+        }
       }
+      left[c] = meeting.meet(1, true) ? 1000 : 2000;
     });
   for (auto &x : t) x.join();
-  if (meeting.stuck) return 2;
-  for (int c = 1; c < n; ++c)
-    if (got[c] != got[0]) return 1;
+  if (meeting.stuck || meeting.mixed) return 2;
+  bool some = false, every = true;
+  for (int c = 0; c < n; ++c) { some |= left[c] != 1000; every &= left[c] != 1000; }
+  if (some != every) return 1;
   return wrong ? 3 : 0;
 }
 
@@ -159,7 +162,7 @@ def test_groups_without_failures(flow, stages, most):
 @pytest.mark.parametrize("late", [[0], [3], [0, 7], [1, 2, 3, 4, 5, 6, 7], list(range(8))])
 def test_a_wait_that_gives_up_takes_every_consumer_out(flow, stages, late, most):
     """Some consumers' waits give up, at every place where they can, the others' do not (a stage that lands just at
-    the limit): all leave at the same group, and none stays at a meeting."""
+    the limit): all leave, and none stays at a meeting."""
     for at in range(sum(stages) + len(stages)):
         assert _run_flow(flow, stages, [at if c in late else NEVER for c in range(8)], most) == 0, at
         # ... and the others one wait later

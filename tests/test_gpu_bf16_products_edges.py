@@ -123,3 +123,42 @@ def test_adapters_beside_a_long_projection(M, N, K):
     p.backward(M, ws)
     assert M.moe_read_device_error(ws) == 0
     p.check_backward()
+
+
+@pytest.mark.parametrize("S,n,r,N,K,long", [
+    (300, 40, 16, 2056, 2048, 0), (700, 300, 8, 2048, 2056, 500), (2100, 700, 32, 1032, 1040, 90), (1024, 4, 64, 136, 72, 0),
+    (40, 1200, 16, 264, 136, 3), (5000, 90, 128, 264, 520, 40), (33_000, 5000, 8, 72, 136, 0)])
+def test_many_adapters_and_segments(M, S, n, r, N, K, long):
+    """More adapters than a block of the gradients' kernel looks up at a time, in no order, some without a segment, some
+    with many; segments of one row, of none and long ones."""
+    g = torch.Generator().manual_seed(S + n)
+    lens = torch.randint(0, 3, (S,), generator=g)
+    lens[torch.randint(0, S, (5,), generator=g)] = long + 1
+    ads = torch.randint(-1, n, (S,), generator=g)
+    ads[::7] = n - 1
+    p = Problem(lens.tolist(), ads.tolist(), n, r, N, K, tail=3, seed=S)
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_forward()
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_backward()
+
+
+def test_adapters_out_of_range_among_many(M):
+    # values far outside count as none, at any place of a look
+    S, n = 600, 200
+    ads = [(7 * i) % n for i in range(S)]
+    for i, v in ((3, 2 ** 31 - 1), (64, -2 ** 31), (130, n), (255, -2), (511, n + 592), (599, 2 ** 30)):
+        ads[i] = v
+    p = Problem([1] * S, ads, n, 8, 2048, 2048, seed=4)
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    assert M.moe_read_device_error(ws) == M.MOE_DEVERR_EXPERT_ID
+    p.check_forward()
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) == M.MOE_DEVERR_EXPERT_ID
+    p.check_backward()

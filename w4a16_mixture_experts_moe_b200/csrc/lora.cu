@@ -625,6 +625,7 @@ struct AdapterGradArgs {
   int segs, n_adapters, T, N, K, rank;
   int slabs_a;        // 64-column slabs of x; the others are dy's
   int stages;
+  int batch;          // adapters of a CTA whose segments are looked up together; 0: each by itself
   uint16_t *da, *db;  // [n][rank][K], [n][N][rank]
   int32_t *err;
 };
@@ -656,6 +657,31 @@ struct AdapterGradMaps {
   CUtensorMap x[2], dy[2], u[2], du[2];
 };
 
+// Which groups of 32 segments hold one of the next a.batch adapters ad, ad + step,
+// ...: bit g of an adapter's words. A warp marks them with eight segments a lane
+// in flight. Where a CTA would look at more than AG_LOOKS groups for its adapters
+// one by one, each a load's latency, this is faster (backward, K = N = 2048, rank
+// 16: 4096 segments of one row, 1024 adapters 5.3 -> 1.0 ms, 256 and 64 71 -> 65
+// us), with fewer slower (58 and 48: 43 us, 44 with the marks).
+constexpr int AG_LOOKS = 48, AG_WORDS = 1024;
+__device__ __forceinline__ void mark_segments(const AdapterGradArgs &a, int ad, int step, int words, uint32_t *bits) {
+  const int lane = threadIdx.x & 31;
+  for (int p = lane; p < a.batch * words; p += 32) bits[p] = 0;
+  __syncwarp();
+  for (int s0 = 0; s0 < a.segs; s0 += 8 * 32) {
+    uint32_t q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      q[k] = s0 + 32 * k + lane < a.segs ? uint32_t(a.seg_adapter[s0 + 32 * k + lane]) - uint32_t(ad) : 0xffffffffu;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = int(min(q[k], 0x7fffffffu)) / step, g = (s0 >> 5) + k;
+      if (i < a.batch && i * step == int(q[k])) atomicOr(&bits[i * words + (g >> 5)], 1u << (g & 31));
+    }
+  }
+  __syncwarp();
+}
+
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
 // with p = du, z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
@@ -663,10 +689,12 @@ struct AdapterGradMaps {
 // ranks, K = rows (two warps share a chunk's). The rows behind a
 // segment's end are cleared in the fragments. The segments are taken in order
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
-// (Registers for about as many CTAs an SM as the rings leave room for: left to
-// itself the compiler spills at ranks of 16 and takes 132 at 64, one CTA an SM.)
-template <int RJ, int AG_ROWS>
-__global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : RJ <= 64 ? 2 : 1)
+// LONG: some adapter may need more additions than AG_ADDITIONS. MARK: see
+// mark_segments. (The least CTAs an SM are what its shared memory holds, set where
+// the compiler by itself spills or takes registers for fewer: T = 4096, rank 64,
+// 24.2 -> 22.5 us, rank 32, 128 segments 26.0 -> 22.5.)
+template <int RJ, int AG_ROWS, bool LONG, bool MARK>
+__global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : 0)
     adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ AdapterGradMaps maps) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   extern __shared__ uint8_t smem_raw[];
@@ -684,9 +712,12 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : 
   bool ok = true;
   if (warp == 8) {
     const CUtensorMap *tz = is_a ? maps.x : maps.dy, *tp = is_a ? maps.du : maps.u;
+    uint32_t *bits = reinterpret_cast<uint32_t *>(&ring + 1);  // [batch][words]
+    const int words = (a.segs + 1023) >> 10;
+    int in_batch = 0;
     for (int ad = blockIdx.y; ad < a.n_adapters && ok; ad += gridDim.y) {
-      for (int s0 = 0; s0 < a.segs && ok; s0 += 32) {  // the lanes look at 32 segments
-        const int s = s0 + lane;
+      if (MARK && in_batch == 0) mark_segments(a, ad, gridDim.y, words, bits);
+      auto look = [&](int s) {  // at 32 segments, one a lane
         int lo = 0, hi = 0;
         if (s < a.segs && a.seg_adapter[s] == ad) {
           lo = max(a.seg_offsets[s], 0);
@@ -709,6 +740,19 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : 
             if (++slot == a.stages) { slot = 0; ++round; }
           }
         }
+      };
+      if constexpr (!MARK) {
+        for (int s0 = 0; s0 < a.segs && ok; s0 += 32) look(s0 + lane);
+      } else {
+        for (int h = 0; h < words && ok; h += 32) {  // the lanes' words: 32 times 32 such groups
+          const uint32_t word = h + lane < words ? bits[in_batch * words + h + lane] : 0u;
+          for (uint32_t nz = __ballot_sync(0xffffffffu, word != 0); nz && ok; nz &= nz - 1) {
+            const int l = __ffs(nz) - 1;
+            for (uint32_t m = __shfl_sync(0xffffffffu, word, l); m && ok; m &= m - 1)
+              look((32 * (h + l) + __ffs(m) - 1) * 32 + lane);
+          }
+        }
+        if (++in_batch == a.batch) in_batch = 0;
       }
       if (!ok) break;
       ok = ring_wait(ring, &ring.empty[slot], (round & 1) ^ 1, a.err);  // the adapter's end: a stage without rows
@@ -771,40 +815,36 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : 
     auto at = [&](int j, int q) -> float & {
       return red[(j * 8 + 2 * t4 + (q & 1)) * Cfg::LD + cg * 16 + g + (q >> 1) * 8];
     };
-    bool first = true;
-    int got;
-    do {
+    auto clear = [&]() {
 #pragma unroll
       for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-      // (the meeting at its end is also behind the reads of the last group's sums)
-      got = take_stages(AG_ADDITIONS, next, stage, consumer_all);
-      if (got >= TAKEN_NOTHING) break;
-      if (kg == 1) {
-        if (first) {
-#pragma unroll
-          for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
-        } else {  // (one after the other: this path is rare, and must not cost the others registers)
-#pragma unroll
-          for (int j = 0; j < RJ / 8; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) add_shared(&at(j, q), acc[j][q]);
-        }
-      }
-      consumer_sync();
-      if (kg == 0) {
+    };
+    auto put = [&](bool first) {
+      if (kg != 1) return;
+      if (!LONG || first) {
 #pragma unroll
         for (int j = 0; j < RJ / 8; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+          for (int q = 0; q < 4; ++q) at(j, q) = acc[j][q];
+      } else {  // (one after the other: this path is rare, and must not cost the others registers)
+#pragma unroll
+        for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) add_shared(&at(j, q), acc[j][q]);
       }
-      first = false;
-    } while (got == TAKEN_MORE);
-    if (got == TAKEN_GAVE_UP) return;
-    if (first) {  // no rows: zeros
+    };
+    auto add = [&]() {
+      if (kg != 0) return;
+#pragma unroll
+      for (int j = 0; j < RJ / 8; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
+    };
+    const int got = sum_group<LONG>(AG_ADDITIONS, next, clear, stage, put, consumer_all, add, consumer_sync);
+    if (got < 0) return;
+    if (got == 0) {  // no rows: zeros
       const uint4 zero = make_uint4(0, 0, 0, 0);
       for (int p = tid; p < AG_COLS * a.rank / 8; p += CONSUMERS) {
         if (is_a) {
@@ -816,7 +856,6 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : 
       }
       continue;
     }
-    consumer_sync();
     if (is_a) {  // [rank][K]: 64 columns of each row
       for (int p = tid; p < a.rank * (AG_COLS / 2); p += CONSUMERS) {
         const int j = p / (AG_COLS / 2), c = p % (AG_COLS / 2) * 2;
@@ -832,7 +871,9 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ <= 16 ? 4 : RJ <= 32 ? 3 : 
               pack_bf16x2(red[j * Cfg::LD + c], red[(j + 1) * Cfg::LD + c]);
       }
     }
+    consumer_sync();  // the sums are read
   }
+  consumer_all(true);
 }
 
 // Small-rank operands of one call, for the tensor maps.
@@ -966,11 +1007,18 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   int ny = (4 * sm_count() + slabs - 1) / slabs;
   ny = ny > a.n_adapters ? a.n_adapters : ny;
   a.stages = slabs * ny <= sm_count() ? Cfg::DEEP : Cfg::SHALLOW;
+  const int per = (a.n_adapters + ny - 1) / ny, words = (a.segs + 1023) / 1024;  // adapters a CTA; words an adapter
+  a.batch = int64_t(per) * ((a.segs + 31) / 32) <= AG_LOOKS ? 0 : per < AG_WORDS / words ? per : AG_WORDS / words;
+  const size_t smem = Cfg::smem(a.stages) + size_t(a.batch) * words * 4;
   const dim3 grid{unsigned(slabs), unsigned(ny)};
-  st = allow_dynamic_smem(reinterpret_cast<const void *>(adapter_grad_kernel<RJ, AG_ROWS>), Cfg::smem(Cfg::DEEP), what);
+  // additions of the longest adapter: 16 rows each, and one more for each chunk
+  const bool far = int64_t(a.T) / 16 + a.T / AG_ROWS + a.segs > AG_ADDITIONS;
+  auto *kernel = a.batch ? adapter_grad_kernel<RJ, AG_ROWS, true, true>
+                 : far   ? adapter_grad_kernel<RJ, AG_ROWS, true, false>
+                         : adapter_grad_kernel<RJ, AG_ROWS, false, false>;
+  st = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), Cfg::smem(Cfg::DEEP) + AG_WORDS * 4, what);
   if (st != MOE_OK) return st;
-  const cudaError_t e = launch_pdl(adapter_grad_kernel<RJ, AG_ROWS>, grid, dim3(CONSUMERS + 32), size_t(Cfg::smem(a.stages)), s, a,
-                                   maps);
+  const cudaError_t e = launch_pdl(kernel, grid, dim3(CONSUMERS + 32), smem, s, a, maps);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -1210,7 +1258,7 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
   }
   if (d_lora_a) {
     const int slabs_a = (K + lora::AG_COLS - 1) / lora::AG_COLS;
-    const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, slabs_a, 0, d_lora_a, d_lora_b, err};
+    const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, slabs_a, 0, 0, d_lora_a, d_lora_b, err};
     const char *what = "moe_lora_linear_backward (adapters)";
     const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
     // loads of 128 rows, or of 32 where segments are short on average
