@@ -92,6 +92,7 @@ BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
 @pytest.fixture
 def cpu(N, monkeypatch):
+    current = N._current_device
     monkeypatch.setattr(N, "_current_device", lambda: -1)
     calls = []
 
@@ -99,9 +100,7 @@ def cpu(N, monkeypatch):
         def __getattr__(self, name):
             return lambda *args: calls.append((name, args)) or 0
     monkeypatch.setattr(N, "lib", Lib())
-    monkeypatch.setattr(N, "_torch", torch)
-    for name, kinds in (("_BF16", (torch.bfloat16, torch.uint16, torch.int16)), ("_I32", (torch.int32,)), ("_F32", (torch.float32,))):
-        monkeypatch.setattr(N, name, kinds)
+    current()  # fills in the dtypes
     return calls
 
 
@@ -195,8 +194,11 @@ def test_views_that_hold_what_the_call_reaches(N, cpu):
     _grouped(N, "fwd", x=wide[:, :k], ldx=k + 40)          # a strided view, its rows' padding in the storage
     _grouped(N, "fwd", x=wide[:, 40:], ldx=k + 40)         # (the last row ends with the storage)
     _grouped(N, "fwd", x=torch.zeros(R, k, dtype=torch.int16))  # 16-bit patterns
-    assert len(cpu) == 3
+    record = torch.zeros(E * n * k * 2 + 64, dtype=torch.uint8)  # the bytes of a bank
+    _grouped(N, "fwd", w=record[64:], offsets=record[:4 * E + 4])
+    assert len(cpu) == 4
     del cpu[:]
+    _refused(N, cpu, "w", lambda: _grouped(N, "fwd", w=record[65:]))
     _refused(N, cpu, "x", lambda: _grouped(N, "fwd", x=wide[:, 41:], ldx=k + 40))
     _refused(N, cpu, "x", lambda: _grouped(N, "fwd", x=wide[1:, :k], ldx=k + 40))
     _refused(N, cpu, "ws", lambda: _grouped(N, "fwd", ws_bytes=257))

@@ -138,7 +138,7 @@ def _dev_slow(x, cur, name, kinds, need):
 
 
 _torch = None
-_BF16 = _I32 = _F32 = ()  # dtypes of the arguments (filled with torch's): BF16 values or their 16-bit patterns
+_BF16 = _I32 = _F32 = ()  # dtypes of the arguments (filled with torch's): BF16 also as 16-bit patterns, each as plain bytes
 
 
 def _current_device() -> int:
@@ -148,7 +148,8 @@ def _current_device() -> int:
     if _torch is None:
         import torch
         _torch = torch
-        _BF16, _I32, _F32 = (torch.bfloat16, torch.uint16, torch.int16), (torch.int32,), (torch.float32,)
+        _BF16 = (torch.bfloat16, torch.uint16, torch.int16, torch.uint8)
+        _I32, _F32 = (torch.int32, torch.uint8), (torch.float32, torch.uint8)
     try:
         return _torch._C._cuda_getDevice()
     except (RuntimeError, AttributeError):  # no driver or device; a torch built without CUDA has no such function
