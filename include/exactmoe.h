@@ -387,8 +387,10 @@ int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
  *   ws           at least moe_lora_workspace_size bytes, 256-byte aligned,
  *                zeroed once before first use; word 0 is the device error
  *                word. Calls that may overlap on the GPU need a workspace each.
- * Sums are fp32; u and du are rounded to BF16 once, as operands of the product
- * they enter, and every other output once at the end. Equal calls give equal
+ * Sums are fp32, within about 1e-4 of the exact ones (relative to the sum of
+ * magnitudes) at any length up to 2^17. u and du are rounded to BF16 once, as
+ * operands of the product they enter (d_lora_a takes du with 16 bits of fraction),
+ * and every other output once at the end. Equal calls give equal
  * bits. N and K are multiples of 8 up to 2^30, rank a multiple of 8 from 8 to 128, S <=
  * 65535, strides multiples of 8, pointers 16-byte aligned. T and S may be 0.
  */

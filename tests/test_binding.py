@@ -279,9 +279,12 @@ def test_workspace_of_long_reductions(N):
         for call in (lambda s: fwd(L, 64, 0, s), lambda s: dgrad(64, L, 0, s), lambda s: fwd(64, L, f32, s),
                      lambda s: dgrad(L, 64, f32, s), lambda s: wgrad(L, f32, s), lambda s: wgrad(16384, 0, s)):
             assert call(256) in ok
-    base = N.moe_lora_workspace_size(400, 3, 2, 16, 4096, 4096)
-    assert N.moe_lora_workspace_size(400, 1, 2, 16, 64, L) == N.moe_lora_workspace_size(400, 1, 2, 16, L, 64) == long[0]
-    assert N.moe_lora_workspace_size(400, 3, 2, 16, 64, L) == long[0] + (base - 256 - 1600) // 4096 * L + 1600
+    # the adapters': beside that a megabyte at least for the split inner gradient, 4 bytes for each row and rank
+    MB = 1 << 20
+    assert N.moe_lora_workspace_size(1, 1, 2, 8, 64, 64) == N.moe_lora_workspace_size(2048, 1, 9, 128, 64, 64) == 256 + MB
+    assert N.moe_lora_workspace_size(2049, 1, 9, 128, 64, 64) == 256 + 2049 * 512
+    assert N.moe_lora_workspace_size(400, 1, 2, 16, 64, L) == N.moe_lora_workspace_size(400, 1, 2, 16, L, 64) == long[0] + MB
+    assert N.moe_lora_workspace_size(400, 3, 2, 16, 64, L) == long[0] + MB + 48 * L * 4 + 1600
 
 
 def test_columns_beyond_the_kernels_arithmetic_are_refused(N):

@@ -44,8 +44,7 @@ def test_gradients_of_an_adapter_with_a_million_rows(M, lens):
     """All products of one sign, so that what additions cut off adds up. A matrix unit's additions may cut off up to
     2^-23 of the running sum each, and there are at most 256 and a stage's before a sum passes on: 2^-14.9. The sums
     passed on, two for each 4096 rows, are rounded to nearest, 2^-24 each: 2^-15. So before its own rounding, half a
-    BF16 step of its binade, a value is within 2^-13.9 of the exact sum of the operands that the call read (with the
-    inner gradient as it rounded it). A sum never passed on loses up to 3e-3."""
+    BF16 step of its binade, a value is within 2^-13.9 of the exact sum. A sum never passed on loses up to 3e-3."""
     N = K = 512
     r, S = 64, len(lens)
     off = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
@@ -60,7 +59,7 @@ def test_gradients_of_an_adapter_with_a_million_rows(M, lens):
     ra, rb = torch.zeros(r, K, dtype=torch.float64, device="cuda"), torch.zeros(N, r, dtype=torch.float64, device="cuda")
     for i in range(0, T, 1 << 16):
         s = slice(i, i + (1 << 16))
-        ra += du[s].double().T @ x[s].double()   # of the inner gradient as the call rounded it
+        ra += (dy[s].double() @ b[0].double()).T @ x[s].double()
         rb += dy[s].double().T @ u[s].double()
     for got, ref in ((da[0], ra), (db[0], rb)):
         _within(got, ref, _half_step(ref) + 2.0 ** -13.9 * ref, "gradient")
@@ -162,3 +161,47 @@ def test_adapters_out_of_range_among_many(M):
     p.backward(M, ws)
     assert M.moe_read_device_error(ws) == M.MOE_DEVERR_EXPERT_ID
     p.check_backward()
+
+
+@pytest.mark.parametrize("lens,r,N,K", [([40, 0, 33, 9], 8, 264, 200), ([1] * 60, 24, 520, 136), ([300, 211], 32, 136, 520),
+                                        ([300, 211], 40, 264, 200), ([90, 5, 200], 64, 1032, 264), ([64] * 9, 96, 264, 136),
+                                        ([5000, 17], 128, 264, 200), ([4000, 100, 900], 16, 200, 264)])
+def test_inner_gradient_enters_dA_unrounded(M, lens, r, N, K):
+    """dA within its own rounding, half a BF16 step of its binade, and what precedes it: du's fp32 sums of N products,
+    what its two BF16 values leave of it (half a step of the second: 2^-9 of the first's half step, 2^-8 of du: 2^-17
+    and less), and dA's own sums."""
+    n = 2
+    p = Problem(lens, [i % n for i in range(len(lens))], n, r, N, K, tail=3, seed=r)
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    p.check_forward()
+    p.check_backward()
+    rows, ads, sc = p.per_row()
+    for q in range(n):
+        t = rows[ads == q]
+        x, g, b = p.x[t].double(), p.dy[t].double(), p.b[q].double()
+        s = float(p.scale[q])
+        du, mag = s * (g @ b), abs(s) * (g.abs() @ b.abs())
+        ref = du.T @ x
+        err = (N + 1) * SUM * mag + 2.0 ** -17 * du.abs()
+        before = err.T @ x.abs()
+        before = before + len(t) * SUM * (du.abs().T @ x.abs() + before)
+        _within(p.da[q], ref, _half_step(ref) + (1 + HALF) * before, f"dA[{q}]")
+
+
+def test_infinite_inner_gradients_stay_infinite(M):
+    # what a rounding to infinity cuts off is not a number: dA is infinite where du is, and its neighbours' is as before
+    p = Problem([20, 30], [0, 1], 2, 16, 72, 64, seed=6, with_scale=False)
+    p.x.abs_()
+    p.dy[3] = 3e38
+    p.b[0].abs_()
+    p.strided()
+    ws = p.workspace(M)
+    p.forward(M, ws)
+    p.backward(M, ws)
+    assert M.moe_read_device_error(ws) == 0
+    assert torch.isinf(p.du[3]).all() and (p.da[0][:, p.x[3] > 0] == float("inf")).all()
+    assert torch.isfinite(p.da[1]).all()

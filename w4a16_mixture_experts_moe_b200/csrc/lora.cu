@@ -8,10 +8,12 @@
 // gemm_gemv.cu's (a few rows).
 //
 // u and du are rounded to BF16 once: they are operands of the BF16 matrix
-// instructions that follow, and the adapter's part is a small share of y, so
-// the rounding (at most 2^-8 relative, independent from value to value) stays
-// below y's own. dA and dB, which they enter alone, carry that half step beside
-// their own.
+// instructions that follow, and the adapter's part is a small share of y and dx,
+// so the rounding (at most 2^-8 relative, independent from value to value) stays
+// below their own. dA is made of du alone: it takes du as two BF16 values, the
+// rounded one and what the rounding cut off (16 bits of fraction in all), since
+// one would cost dA 1.4 times the error of its own rounding. dB takes u as the
+// caller kept it.
 //
 // The small-rank products read each row of x (dy) once and do 2 rank
 // operations per value: at rank 64 that is 64 operations a byte, far below the
@@ -111,6 +113,7 @@ struct ShrinkArgs {
   const float *scale;
   int segs, n_adapters, T, C, rank;
   uint16_t *out;      // [T][rank]
+  uint16_t *split;    // [T][2 rank]: the same, and what the rounding cut off, rounded (or nullptr)
   int32_t *row_seg;   // [T] the rows' segments, written for the launches behind (or nullptr)
   int32_t *err;
 };
@@ -183,6 +186,9 @@ __device__ __forceinline__ int find_piece(const int32_t *off, int segs, int T, i
   if (s < 1 || t < 1 || t > tiles) hi = lo;
   return s - 1;
 }
+
+// What a rounding of v to `rounded` cut off (0 behind infinities and NaN).
+__device__ __forceinline__ float cut_off(float v, float rounded) { return isfinite(rounded) ? v - rounded : 0.f; }
 
 // out[t][j] = bf16(scale_a sum_c z[t][c] P_a[j][c]), z = x and P = lora_a, or
 // z = dy and P_a[j][c] = lora_b[a][c][j] (TRANS). A CTA takes one segment's rows
@@ -285,7 +291,15 @@ __global__ void __launch_bounds__(CONSUMERS + 32)
       v0 += red[(k * ROWS + r) * (BJ + 1) + jj];
       v1 += red[(k * ROWS + r) * (BJ + 1) + jj + 1];
     }
-    *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = pack_bf16x2(v0 * sc, v1 * sc);
+    v0 *= sc;
+    v1 *= sc;
+    const uint32_t hi = pack_bf16x2(v0, v1);
+    *reinterpret_cast<uint32_t *>(a.out + int64_t(row0 + r) * a.rank + j0 + jj) = hi;
+    if (a.split) {
+      uint16_t *o = a.split + int64_t(row0 + r) * 2 * a.rank + j0 + jj;
+      *reinterpret_cast<uint32_t *>(o) = hi;
+      *reinterpret_cast<uint32_t *>(o + a.rank) = pack_bf16x2(cut_off(v0, bf16_lo(hi)), cut_off(v1, bf16_hi(hi)));
+    }
   }
 }
 
@@ -639,7 +653,10 @@ constexpr int AG_ADDITIONS = 256;
 
 template <int RJ, int AG_ROWS>
 struct AdapterGradCfg {
-  static constexpr int Z = AG_ROWS * 128, P = AG_ROWS * (RJ == 128 ? 256 : 128);
+  static constexpr int BOX = AG_ROWS * 128;              // bytes of 64 columns
+  // boxes of u, and of du beside what its rounding cut off (twice the columns)
+  static constexpr int U_BOXES = RJ == 128 ? 2 : 1, DU_BOXES = RJ <= 32 ? 1 : RJ / 32;
+  static constexpr int Z = BOX, P = DU_BOXES * BOX;
   static constexpr int STAGE = Z + P;
   static constexpr int LD = AG_COLS + 2;                 // fp32 partial sums [RJ][LD]
   static constexpr int RED = RJ * LD * 4;
@@ -684,17 +701,17 @@ __device__ __forceinline__ void mark_segments(const AdapterGradArgs &a, int ad, 
 
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
-// with p = du, z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
+// with p = du (both of its values), z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
 // memory, read transposed (ldmatrix.trans): M = columns (16 per warp), N =
 // ranks, K = rows (two warps share a chunk's). The rows behind a
 // segment's end are cleared in the fragments. The segments are taken in order
 // by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
 // LONG: some adapter may need more additions than AG_ADDITIONS. MARK: see
 // mark_segments. (The least CTAs an SM are what its shared memory holds, set where
-// the compiler by itself spills or takes registers for fewer: T = 4096, rank 64,
-// 24.2 -> 22.5 us, rank 32, 128 segments 26.0 -> 22.5.)
+// the compiler by itself spills or takes registers for fewer: backward at T =
+// 4096, K = N = 2048, 256 segments, rank 16, 100 -> 88 us.)
 template <int RJ, int AG_ROWS, bool LONG, bool MARK>
-__global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : 0)
+__global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : RJ == 16 && LONG ? (AG_ROWS == 32 ? 4 : 3) : 0)
     adapter_grad_kernel(const AdapterGradArgs a, const __grid_constant__ AdapterGradMaps maps) {
   using Cfg = AdapterGradCfg<RJ, AG_ROWS>;
   extern __shared__ uint8_t smem_raw[];
@@ -731,10 +748,10 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : 
               uint8_t *z = sm + slot * Cfg::STAGE, *p = z + Cfg::Z;
               const int few = e - r <= AG_SHORT;
               ring.rows[slot] = min(AG_ROWS, e - r);
-              tma::mbar_arrive_expect_tx(&ring.full[slot], few ? Cfg::STAGE / AG_ROWS * AG_SHORT : Cfg::STAGE);
+              const int boxes = is_a ? Cfg::DU_BOXES : Cfg::U_BOXES, bytes = Cfg::BOX * (1 + boxes);
+              tma::mbar_arrive_expect_tx(&ring.full[slot], few ? bytes / AG_ROWS * AG_SHORT : bytes);
               tma::tma_load_2d(z, tz + few, c0, r, &ring.full[slot]);
-              tma::tma_load_2d(p, tp + few, 0, r, &ring.full[slot]);
-              if (RJ == 128) tma::tma_load_2d(p + AG_ROWS * 128, tp + few, 64, r, &ring.full[slot]);
+              for (int q = 0; q < boxes; ++q) tma::tma_load_2d(p + q * Cfg::BOX, tp + few, 64 * q, r, &ring.full[slot]);
             }
             __syncwarp();
             if (++slot == a.stages) { slot = 0; ++round; }
@@ -799,11 +816,15 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : 
           if (cut) { af[0] &= m0; af[1] &= m0; af[2] &= m1; af[3] &= m1; }
 #pragma unroll
           for (int jp = 0; jp < RJ / 16; ++jp) {
-            uint32_t bf[4];
-            ldsm4<true>(bf, sw128(p + (jp >> 2) * AG_ROWS * 128, kk * 16 + lo + m8 * 8, (jp & 3) * 2 + hi));
-            if (cut) { bf[0] &= m0; bf[1] &= m1; bf[2] &= m0; bf[3] &= m1; }
-            mma_16816(acc[2 * jp], af, bf[0], bf[1]);
-            mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
+            auto ranks = [&](int piece) {  // 16 ranks from the piece-th 8 columns of P on
+              uint32_t bf[4];
+              ldsm4<true>(bf, sw128(p + (piece >> 3) * Cfg::BOX, kk * 16 + lo + m8 * 8, piece & 7));
+              if (cut) { bf[0] &= m0; bf[1] &= m1; bf[2] &= m0; bf[3] &= m1; }
+              mma_16816(acc[2 * jp], af, bf[0], bf[1]);
+              mma_16816(acc[2 * jp + 1], af, bf[2], bf[3]);
+            };
+            ranks(2 * jp + hi);
+            if (is_a) ranks((a.rank >> 3) + 2 * jp + hi);  // (behind a rank that fills no 16, into sums that nobody stores)
           }
         }
       };
@@ -842,7 +863,7 @@ __global__ void __launch_bounds__(CONSUMERS + 32, RJ == 64 ? 2 : RJ == 32 ? 3 : 
 #pragma unroll
         for (int q = 0; q < 4; ++q) at(j, q) += acc[j][q];
     };
-    const int got = sum_group<LONG>(AG_ADDITIONS, next, clear, stage, put, consumer_all, add, consumer_sync);
+    const int got = sum_group<LONG>(is_a ? AG_ADDITIONS / 2 : AG_ADDITIONS, next, clear, stage, put, consumer_all, add, consumer_sync);
     if (got < 0) return;
     if (got == 0) {  // no rows: zeros
       const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -1011,8 +1032,8 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   a.batch = int64_t(per) * ((a.segs + 31) / 32) <= AG_LOOKS ? 0 : per < AG_WORDS / words ? per : AG_WORDS / words;
   const size_t smem = Cfg::smem(a.stages) + size_t(a.batch) * words * 4;
   const dim3 grid{unsigned(slabs), unsigned(ny)};
-  // additions of the longest adapter: 16 rows each, and one more for each chunk
-  const bool far = int64_t(a.T) / 16 + a.T / AG_ROWS + a.segs > AG_ADDITIONS;
+  // additions of the longest adapter: 16 rows each, and one more for each chunk; dA's twice
+  const bool far = int64_t(a.T) / 16 + a.T / AG_ROWS + a.segs > AG_ADDITIONS / 2;
   auto *kernel = a.batch ? adapter_grad_kernel<RJ, AG_ROWS, true, true>
                  : far   ? adapter_grad_kernel<RJ, AG_ROWS, true, false>
                          : adapter_grad_kernel<RJ, AG_ROWS, false, false>;
@@ -1023,13 +1044,16 @@ static int launch_adapter_grad_as(AdapterGradArgs a, const Rows &x, const Rows &
   return check_launch(what);
 }
 
-template <int AG_ROWS>
+// WIDE: long loads, 128 rows or, at ranks whose stages would leave no room for a
+// second one, 64.
+template <bool WIDE>
 static int launch_adapter_grad(const AdapterGradArgs &a, const Rows &x, const Rows &dy, const Rows &u,
                                const Rows &du, cudaStream_t s, const char *what) {
-  return a.rank <= 16   ? launch_adapter_grad_as<16, AG_ROWS>(a, x, dy, u, du, s, what)
-         : a.rank <= 32 ? launch_adapter_grad_as<32, AG_ROWS>(a, x, dy, u, du, s, what)
-         : a.rank <= 64 ? launch_adapter_grad_as<64, AG_ROWS>(a, x, dy, u, du, s, what)
-                        : launch_adapter_grad_as<128, AG_ROWS>(a, x, dy, u, du, s, what);
+  constexpr int ROWS = WIDE ? 128 : 32, HIGH = WIDE ? 64 : 32;
+  return a.rank <= 16   ? launch_adapter_grad_as<16, ROWS>(a, x, dy, u, du, s, what)
+         : a.rank <= 32 ? launch_adapter_grad_as<32, ROWS>(a, x, dy, u, du, s, what)
+         : a.rank <= 64 ? launch_adapter_grad_as<64, HIGH>(a, x, dy, u, du, s, what)
+                        : launch_adapter_grad_as<128, HIGH>(a, x, dy, u, du, s, what);
 }
 
 // Rows of the fp32 sums for shared 16-row blocks: 16 per segment, or one per
@@ -1040,13 +1064,32 @@ static size_t delta_rows(int T, int S) {
   return by_seg < by_row ? by_seg : by_row;
 }
 
-// The workspace: the error word, what long reductions of the engine add up in,
-// those sums, and the rows' segments.
-static char *shared_sums(int N, int K, void *ws) {
-  return static_cast<char *>(ws) + WS_HEADER + long_sums_bytes(N > K ? N : K);
+// du beside what its rounding cut off, [T][2 rank]. A megabyte at least, so that
+// calls of a few rows ask for one size.
+static size_t split_bytes(int T, int rank) {
+  const size_t need = T < 1 ? 0 : (size_t(T) * rank * 4 + 255) / 256 * 256;
+  return need < (size_t(1) << 20) ? size_t(1) << 20 : need;
 }
-static int32_t *row_segments(int T, int S, int N, int K, void *ws) {
-  return reinterpret_cast<int32_t *>(shared_sums(N, K, ws) + delta_rows(T, S) * size_t(N > K ? N : K) * 4);
+
+// The workspace: the error word, what long reductions of the engine add up in,
+// the split du, those sums, and the rows' segments.
+struct Workspace {
+  char *sums;
+  uint16_t *split;
+  float *delta;
+  int32_t *row_seg;
+  size_t bytes;
+};
+static Workspace workspace(int T, int S, int rank, int N, int K, void *ws) {
+  const int most = N > K ? N : K;
+  Workspace w;
+  w.sums = static_cast<char *>(ws) + WS_HEADER;
+  w.split = reinterpret_cast<uint16_t *>(w.sums + long_sums_bytes(most));
+  w.delta = reinterpret_cast<float *>(reinterpret_cast<char *>(w.split) + split_bytes(T, rank));
+  char *end = reinterpret_cast<char *>(w.delta) + delta_rows(T, S) * size_t(most) * 4;
+  w.row_seg = reinterpret_cast<int32_t *>(end);
+  w.bytes = size_t(end - static_cast<char *>(ws)) + (T < 1 || S < 2 ? 0 : size_t(T) * 4);
+  return w;
 }
 
 // The arguments both entry points share.
@@ -1102,7 +1145,8 @@ static bool use_proj(int T, int M, int C) {
 }
 
 static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const int32_t *seg_adapter, int T, int S,
-                             int n_adapters, int rank, int N, int K, void *out, int64_t ldo, int32_t *err) {
+                             int n_adapters, int rank, int N, int K, void *out, int64_t ldo, const Workspace &ws,
+                             int32_t *err) {
   TcGemmArgs g = {};
   g.offsets = seg_offsets;
   g.adapter = seg_adapter;
@@ -1128,20 +1172,20 @@ static TcGemmArgs projection(GemmMode mode, const int32_t *seg_offsets, const in
   g.ldo = ldo;
   g.late = 1;
   g.err = err;
-  g.sums = reinterpret_cast<float *>(reinterpret_cast<char *>(err) + WS_HEADER);  // there if N or K is long
+  g.sums = reinterpret_cast<float *>(ws.sums);  // there if N or K is long
   return g;
 }
 
 // Launches the sums of the blocks that several segments share and points the
 // projection at them (one segment shares no block).
 template <bool COLS>
-static int shared_blocks(TcGemmArgs &g, int T, int S, int N, int K, void *ws, cudaStream_t s, const char *what) {
+static int shared_blocks(TcGemmArgs &g, int T, int S, const Workspace &ws, cudaStream_t s, const char *what) {
   if (S < 2) return MOE_OK;
-  g.delta = reinterpret_cast<const float *>(shared_sums(N, K, ws));
+  g.delta = ws.delta;
   g.delta_by_seg = int64_t(S) * 16 < (int64_t(T) + 15) / 16 * 16;
-  g.row_seg = row_segments(T, S, N, K, ws);
+  g.row_seg = ws.row_seg;
   const DeltaArgs d = {g.offsets, g.adapter, g.row_seg, g.ext_b, g.ext_a, S, g.n_adapters, T, g.rank, g.M, g.delta_by_seg,
-                       const_cast<float *>(g.delta)};
+                       ws.delta};
   return launch_delta<COLS>(d, s, what);
 }
 
@@ -1149,9 +1193,8 @@ static int shared_blocks(TcGemmArgs &g, int T, int S, int N, int K, void *ws, cu
 }  // namespace moe
 
 extern "C" size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K) {
-  (void)n_adapters; (void)rank;
-  return moe::WS_HEADER + moe::long_sums_bytes(N > K ? N : K) + moe::lora::delta_rows(T, S) * size_t(N > K ? N : K) * 4 +
-         (T < 1 || S < 2 ? 0 : size_t(T) * 4);
+  (void)n_adapters;
+  return moe::lora::workspace(T, S, rank, N, K, nullptr).bytes;
 }
 
 extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w, const int32_t *seg_offsets,
@@ -1169,8 +1212,9 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     return st;
   cudaStream_t s = as_stream(stream);
   int32_t *err = static_cast<int32_t *>(ws);
+  const lora::Workspace space = lora::workspace(T, S, rank, N, K, ws);
   const bool engine = T > lora::GEMV_MAX_T && !lora::use_proj(T, N, K);
-  int32_t *row_seg = engine && S > 1 ? lora::row_segments(T, S, N, K, ws) : nullptr;
+  int32_t *row_seg = engine && S > 1 ? space.row_seg : nullptr;
 
   if (T <= lora::GEMV_MAX_T || (rank <= 16 && T < 4 * int64_t(S))) {
     // short segments of small rank: each streams its adapter's A (whole call,
@@ -1185,7 +1229,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     v.row_seg = row_seg;
     st = launch_gemm_gemv(v, s, "moe_lora_linear (adapters)");
   } else {
-    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, u, row_seg, err};
+    const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, K, rank, u, nullptr, row_seg, err};
     st = lora::launch_shrink<false>(h, {x, ldx, K}, lora_a, s, "moe_lora_linear (adapters)");
   }
   if (st != MOE_OK) return st;
@@ -1201,10 +1245,10 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
     const lora::ProjArgs v = {seg_offsets, seg_adapter, S, n_adapters, T, K, N, rank, u, lora_b, y, ldy, err};
     return lora::launch_proj<false>(v, {x, ldx, K}, w, s, who);
   }
-  TcGemmArgs g = lora::projection(GEMM_FWD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, y, ldy, err);
+  TcGemmArgs g = lora::projection(GEMM_FWD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, y, ldy, space, err);
   g.ext_a = lora_b;
   g.ext_b = u;
-  if ((st = lora::shared_blocks<false>(g, T, S, N, K, ws, s, "moe_lora_linear (shared blocks)")) != MOE_OK) return st;
+  if ((st = lora::shared_blocks<false>(g, T, S, space, s, "moe_lora_linear (shared blocks)")) != MOE_OK) return st;
   const TcGemmOperands op = {w, x, K, int64_t(N) * K, ldx};
   return launch_gemm_tc(GEMM_FWD, g, op, s, who);
 }
@@ -1239,14 +1283,16 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
     return st;
   int32_t *err = static_cast<int32_t *>(ws);
   const bool engine = dx && !lora::use_proj(T, K, N);
-  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, du, engine && S > 1 ? lora::row_segments(T, S, N, K, ws) : nullptr, err};
+  const lora::Workspace space = lora::workspace(T, S, rank, N, K, ws);
+  const lora::ShrinkArgs h = {seg_offsets, seg_adapter, scale, S, n_adapters, T, N, rank, du,
+                              d_lora_a ? space.split : nullptr, engine && S > 1 ? space.row_seg : nullptr, err};
   if ((st = lora::launch_shrink<true>(h, {dy, lddy, N}, lora_b, s, "moe_lora_linear_backward (du)")) != MOE_OK) return st;
   TcGemmArgs g = {};
   if (engine) {
-    g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, err);
+    g = lora::projection(GEMM_DGRAD, seg_offsets, seg_adapter, T, S, n_adapters, rank, N, K, dx, lddx, space, err);
     g.ext_a = lora_a;
     g.ext_b = du;
-    if ((st = lora::shared_blocks<true>(g, T, S, N, K, ws, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
+    if ((st = lora::shared_blocks<true>(g, T, S, space, s, "moe_lora_linear_backward (shared blocks)")) != MOE_OK) return st;
   }
   // The engine goes behind the adapters' gradients: it starts while they end and
   // waits for them only in its epilogue (six adapters of rank 16 at T = 2041, one
@@ -1260,10 +1306,10 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
     const int slabs_a = (K + lora::AG_COLS - 1) / lora::AG_COLS;
     const lora::AdapterGradArgs q = {seg_offsets, seg_adapter, S, n_adapters, T, N, K, rank, slabs_a, 0, 0, d_lora_a, d_lora_b, err};
     const char *what = "moe_lora_linear_backward (adapters)";
-    const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {du, rank, rank};
-    // loads of 128 rows, or of 32 where segments are short on average
-    st = T >= 64 * int64_t(S) ? lora::launch_adapter_grad<128>(q, rx, rdy, ru, rdu, s, what)
-                              : lora::launch_adapter_grad<32>(q, rx, rdy, ru, rdu, s, what);
+    const lora::Rows rx = {x, ldx, K}, rdy = {dy, lddy, N}, ru = {u, rank, rank}, rdu = {space.split, 2 * rank, 2 * rank};
+    // long loads, or loads of 32 rows where segments are short on average
+    st = T >= 64 * int64_t(S) ? lora::launch_adapter_grad<true>(q, rx, rdy, ru, rdu, s, what)
+                              : lora::launch_adapter_grad<false>(q, rx, rdy, ru, rdu, s, what);
     if (st != MOE_OK) return st;
   }
   return engine ? launch_gemm_tc(GEMM_DGRAD, g, TcGemmOperands{w, dy, K, int64_t(N) * K, lddy}, s, who) : MOE_OK;
