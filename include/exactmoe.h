@@ -315,9 +315,9 @@ int moe_grouped_bf16_ffn(const moe_bf16 *x, const int32_t *sorted_pair,
  *   moe_grouped_gemm_wgrad  dW_e  = sum_r dy[r]^T x[r]   (the weights' gradient)
  *   x, dx        [R][K], dy, y [R][N]: row strides ldx, lddx, lddy, ldy in elements.
  *   offsets      [E+1] int32, 0 <= offsets[0] <= ... <= offsets[E] <= R. Rows
- *                outside [offsets[0], offsets[E]) are neither read nor
- *                written. Offsets outside [0, R] or falling ones are cut to
- *                the rows and set MOE_DEVERR_OFFSETS.
+ *                outside [offsets[0], offsets[E]) are not written, and what
+ *                they hold does not matter. Offsets outside [0, R] or falling
+ *                ones are cut to the rows and set MOE_DEVERR_OFFSETS.
  *   w, dw        matrix e starts at element e * w_stride (dw_stride), rows of
  *                K elements without gaps: a stack [E][N][K], or one part of
  *                the records of a BF16 bank (moe_bf16_record_layout; stride =
@@ -337,8 +337,8 @@ int moe_grouped_bf16_ffn(const moe_bf16 *x, const int32_t *sorted_pair,
  * within about 1e-4 of the exact one (relative to the sum of magnitudes) at any
  * length. fp32 outputs add up long sums in parts and are within about 1e-6 of the
  * exact sums (2-norms) at any length; what is added to one counts as zero below
- * 2^-126. N and K are multiples of 8 up to 2^30, strides multiples of 8, pointers 16-byte
- * aligned. R may be 0.
+ * 2^-126. N and K are multiples of 8 up to 2^30, strides multiples of 8, pointers
+ * 16-byte aligned. R may be 0.
  */
 size_t moe_grouped_gemm_workspace_size(int R, int E, int N, int K);
 int moe_grouped_gemm(const moe_bf16 *x, int64_t ldx, const int32_t *offsets,
@@ -371,8 +371,8 @@ int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
  *   w            [N][K] BF16, frozen (no gradient).
  *   seg_offsets  [S+1] int32, 0 = seg_offsets[0] <= ... <= seg_offsets[S] <= T.
  *                A segment may be empty. Rows behind the last segment are
- *                neither read nor written. Other offsets are cut to the rows
- *                and set MOE_DEVERR_OFFSETS.
+ *                not written, and what they hold does not matter. Other
+ *                offsets are cut to the rows and set MOE_DEVERR_OFFSETS.
  *   seg_adapter  [S] int32 in [-1, n_adapters); any other value counts as -1
  *                and sets MOE_DEVERR_EXPERT_ID.
  *   lora_a       [n_adapters][rank][K], lora_b [n_adapters][N][rank] BF16; an
@@ -387,12 +387,12 @@ int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
  *   ws           at least moe_lora_workspace_size bytes, 256-byte aligned,
  *                zeroed once before first use; word 0 is the device error
  *                word. Calls that may overlap on the GPU need a workspace each.
- * Sums are fp32, within about 1e-4 of the exact ones (relative to the sum of
- * magnitudes) at any length up to 2^17. u and du are rounded to BF16 once, as
+ * Sums are fp32, within about 2e-4 of the exact ones (relative to the sum of
+ * magnitudes) for N and K up to 2^17. u and du are rounded to BF16 once, as
  * operands of the product they enter (d_lora_a takes du with 16 bits of fraction),
- * and every other output once at the end. Equal calls give equal
- * bits. N and K are multiples of 8 up to 2^30, rank a multiple of 8 from 8 to 128, S <=
- * 65535, strides multiples of 8, pointers 16-byte aligned. T and S may be 0.
+ * and every other output once at the end. Equal calls give equal bits. N and K are
+ * multiples of 8 up to 2^30, rank a multiple of 8 from 8 to 128, S <= 65535,
+ * strides multiples of 8, pointers 16-byte aligned. T and S may be 0.
  */
 size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K);
 int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w,

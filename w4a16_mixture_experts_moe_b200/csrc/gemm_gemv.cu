@@ -223,10 +223,7 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) gemv_kernel(const Gemv
 template <int WARPS>
 static int launch_as(const GemvArgs &a, int grid_groups, cudaStream_t s, const char *what) {
   constexpr size_t smem = Cfg<WARPS>::SMEM;
-  if (smem > 48 * 1024) {
-    const int st = allow_dynamic_smem(reinterpret_cast<const void *>(gemv_kernel<WARPS>), smem, what);
-    if (st != MOE_OK) return st;
-  }
+  static_assert(smem <= 48 * 1024, "shared memory without a raised limit");
   const dim3 grid(unsigned((a.N + COLS - 1) / COLS), unsigned(grid_groups));
   const cudaError_t e = launch_pdl(gemv_kernel<WARPS>, grid, dim3(WARPS * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));

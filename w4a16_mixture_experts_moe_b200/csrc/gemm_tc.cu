@@ -713,8 +713,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // 16 rows of the warp's 32 columns, through two buffers of its own (stores
             // straight from the registers, a row of 32 columns each, cost the epilogue
             // 8 cycles apiece and twice that where rows are not multiples of 128
-            // bytes: wgrad of 64 experts x 10 rows, N = 3592, K = 968, 262 -> 178 us;
-            // dgrad of 64 x 256 rows, K = 2048, N = 1024, 92 -> 80)
+            // bytes: wgrad of 64 experts x 10 rows, N = 3592, K = 968, 262 -> 165 us;
+            // dgrad of 64 x 256 rows, K = 2048, N = 1024, 92 -> 76)
             uint32_t v[16];
             tmem_ld16(tb + j0, v);
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
