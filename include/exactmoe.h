@@ -384,7 +384,9 @@ int moe_grouped_gemm_wgrad(const moe_bf16 *dy, int64_t lddy, const moe_bf16 *x,
  *   d_lora_a/b   shaped as lora_a and lora_b, BF16; every adapter's gradient
  *                is written, zeros for one without rows. Both may be NULL (x
  *                and u are then not read and may be NULL too), and so may dx.
- *   ws           at least moe_lora_workspace_size bytes, 256-byte aligned,
+ *   ws           at least moe_lora_workspace_size bytes (one size for both
+ *                calls; its last part, max(1 MiB, 4 T rank) bytes, is only for
+ *                d_lora_a and not asked for otherwise), 256-byte aligned,
  *                zeroed once before first use; word 0 is the device error
  *                word. Calls that may overlap on the GPU need a workspace each.
  * Sums are fp32, within about 2e-4 of the exact ones (relative to the sum of

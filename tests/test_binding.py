@@ -285,6 +285,15 @@ def test_workspace_of_long_reductions(N):
     assert N.moe_lora_workspace_size(2049, 1, 9, 128, 64, 64) == 256 + 2049 * 512
     assert N.moe_lora_workspace_size(400, 1, 2, 16, 64, L) == N.moe_lora_workspace_size(400, 1, 2, 16, L, 64) == long[0] + MB
     assert N.moe_lora_workspace_size(400, 3, 2, 16, 64, L) == long[0] + MB + 48 * L * 4 + 1600
+    # ... which only a call that asks for the adapters' gradients needs
+    T, S, n, r, no, k = 400, 3, 2, 16, 64, 1024
+    whole = N.moe_lora_workspace_size(T, S, n, r, no, k)
+    fwd = lambda s: N.lib.moe_lora_linear(P, k, P, P, P, P, P, None, T, S, n, r, no, k, P, P, no, P, s, None)
+    bwd = lambda d, s: N.lib.moe_lora_linear_backward(P, no, P, k, P, P, P, P, P, P, None, T, S, n, r, no, k, P, P, k, d, d, P, s, None)
+    bad = N.MOE_ERR_INVALID_ARG
+    assert fwd(whole - MB - 1) == bwd(None, whole - MB - 1) == bwd(P, whole - 1) == bad
+    if not torch.cuda.is_available():
+        assert fwd(whole - MB) in ok and bwd(None, whole - MB) in ok and bwd(P, whole) in ok
 
 
 def test_columns_beyond_the_kernels_arithmetic_are_refused(N):

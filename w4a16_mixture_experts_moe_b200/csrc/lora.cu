@@ -1074,30 +1074,28 @@ static size_t split_bytes(int T, int rank) {
 }
 
 // The workspace: the error word, what long reductions of the engine add up in,
-// the split du, those sums, and the rows' segments.
+// the shared blocks' sums, the rows' segments, and the split du, which only calls
+// that ask for the adapters' gradients need.
 struct Workspace {
   char *sums;
-  uint16_t *split;
   float *delta;
   int32_t *row_seg;
-  size_t bytes;
+  uint16_t *split;
+  size_t plain, whole;  // bytes without and with the split du
 };
 static Workspace workspace(int T, int S, int rank, int N, int K, void *ws) {
   const int most = N > K ? N : K;
-  Workspace w;
-  w.sums = static_cast<char *>(ws) + WS_HEADER;
-  w.split = reinterpret_cast<uint16_t *>(w.sums + long_sums_bytes(most));
-  w.delta = reinterpret_cast<float *>(reinterpret_cast<char *>(w.split) + split_bytes(T, rank));
-  char *end = reinterpret_cast<char *>(w.delta) + delta_rows(T, S) * size_t(most) * 4;
-  w.row_seg = reinterpret_cast<int32_t *>(end);
-  w.bytes = size_t(end - static_cast<char *>(ws)) + (T < 1 || S < 2 ? 0 : size_t(T) * 4);
-  return w;
+  const size_t delta = WS_HEADER + long_sums_bytes(most), seg = delta + delta_rows(T, S) * size_t(most) * 4;
+  const size_t plain = seg + (T < 1 || S < 2 ? 0 : size_t(T) * 4), split = (plain + 15) / 16 * 16;
+  char *p = static_cast<char *>(ws);
+  return {p + WS_HEADER, reinterpret_cast<float *>(p + delta), reinterpret_cast<int32_t *>(p + seg),
+          reinterpret_cast<uint16_t *>(p + split), plain, split + split_bytes(T, rank)};
 }
 
-// The arguments both entry points share.
+// The arguments both entry points share; `grads`: the adapters' gradients are asked for.
 static int check_common(const char *who, const void *w, const void *seg_offsets, const void *seg_adapter,
                         const void *lora_a, const void *lora_b, int T, int S, int n_adapters, int rank, int N, int K,
-                        const void *ws, size_t ws_bytes) {
+                        bool grads, const void *ws, size_t ws_bytes) {
   if (T < 0 || T > (1 << 30) || S < 0 || S > MAX_SEGS || n_adapters < 1 || n_adapters > MAX_SEGS)
     return set_error(MOE_ERR_SHAPE, "%s: T=%d S=%d n_adapters=%d (need 0<=T<=2^30, 0<=S<=65535, 1<=n_adapters<=65535)",
                      who, T, S, n_adapters);
@@ -1109,7 +1107,8 @@ static int check_common(const char *who, const void *w, const void *seg_offsets,
     return set_error(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(ws, 256) || !aligned(w, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16))
     return set_error(MOE_ERR_INVALID_ARG, "%s: ws needs 256-byte, w, lora_a and lora_b 16-byte alignment", who);
-  const size_t need = moe_lora_workspace_size(T, S, n_adapters, rank, N, K);
+  const Workspace space = workspace(T, S, rank, N, K, nullptr);
+  const size_t need = grads ? space.whole : space.plain;
   if (ws_bytes < need) return set_error(MOE_ERR_INVALID_ARG, "%s: workspace %zu B < %zu B", who, ws_bytes, need);
   return MOE_OK;
 }
@@ -1196,7 +1195,7 @@ static int shared_blocks(TcGemmArgs &g, int T, int S, const Workspace &ws, cudaS
 
 extern "C" size_t moe_lora_workspace_size(int T, int S, int n_adapters, int rank, int N, int K) {
   (void)n_adapters;
-  return moe::lora::workspace(T, S, rank, N, K, nullptr).bytes;
+  return moe::lora::workspace(T, S, rank, N, K, nullptr).whole;
 }
 
 extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w, const int32_t *seg_offsets,
@@ -1206,7 +1205,7 @@ extern "C" int moe_lora_linear(const moe_bf16 *x, int64_t ldx, const moe_bf16 *w
   moe::NvtxScope nvtx_scope("moe_lora_linear");
   using namespace moe;
   const char *who = "moe_lora_linear";
-  int st = lora::check_common(who, w, seg_offsets, seg_adapter, lora_a, lora_b, T, S, n_adapters, rank, N, K, ws, ws_bytes);
+  int st = lora::check_common(who, w, seg_offsets, seg_adapter, lora_a, lora_b, T, S, n_adapters, rank, N, K, false, ws, ws_bytes);
   if (st != MOE_OK) return st;
   if (T == 0 || S == 0) return MOE_OK;
   if ((st = lora::check_rows(who, "x", x, ldx, K)) != MOE_OK || (st = lora::check_rows(who, "y", y, ldy, N)) != MOE_OK ||
@@ -1264,7 +1263,8 @@ extern "C" int moe_lora_linear_backward(const moe_bf16 *dy, int64_t lddy, const 
   moe::NvtxScope nvtx_scope("moe_lora_linear_backward");
   using namespace moe;
   const char *who = "moe_lora_linear_backward";
-  int st = lora::check_common(who, w, seg_offsets, seg_adapter, lora_a, lora_b, T, S, n_adapters, rank, N, K, ws, ws_bytes);
+  int st = lora::check_common(who, w, seg_offsets, seg_adapter, lora_a, lora_b, T, S, n_adapters, rank, N, K, d_lora_a && T > 0 && S > 0, ws,
+                              ws_bytes);
   if (st != MOE_OK) return st;
   if (!d_lora_a != !d_lora_b)
     return set_error(MOE_ERR_INVALID_ARG, "%s: d_lora_a and d_lora_b are given together or not at all", who);
