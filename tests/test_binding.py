@@ -236,6 +236,8 @@ def test_words_give_the_answers_of_the_call(N, name, args):
     refused = 0
     for i in range(len(args) - 1):            # the stream is not looked at
         for value in (0, -1, 4, 12, P + 2, (1 << 31) - 1):
+            if i == len(args) - 2 and value < 0:
+                continue                      # (bytes)
             a = list(args)
             a[i] = value
             plain = [v or None if t is N._p else v for v, t in zip(a, N.SIGNATURES[name][1])]
@@ -257,6 +259,9 @@ def test_words_beyond_their_arguments_are_refused(N):
             a[i] += 1 << 32                   # would be the same number in 32 bits
             assert words(struct.pack(f"{len(a)}q", *a)) == N.MOE_ERR_SHAPE
             assert b"32 bits" in N.lib.moe_last_error() and name.encode() in N.lib.moe_last_error()
+        a = list(args)
+        a[-2] = -1                            # would be the largest workspace there is
+        assert words(struct.pack(f"{len(a)}q", *a)) == N.MOE_ERR_SHAPE
         assert words(None) == N.MOE_ERR_INVALID_ARG
 
 

@@ -13,7 +13,7 @@ static T from_word(int64_t v, bool *fits) {
   if constexpr (std::is_pointer_v<T>) {
     return reinterpret_cast<T>(static_cast<uintptr_t>(v));
   } else {
-    *fits &= static_cast<int64_t>(static_cast<T>(v)) == v;
+    *fits &= static_cast<int64_t>(static_cast<T>(v)) == v && (std::is_signed_v<T> || v >= 0);
     return static_cast<T>(v);
   }
 }
@@ -23,7 +23,7 @@ static int call_words(const char *who, int (*f)(A...), const int64_t *words, std
   if (!words) return set_error(MOE_ERR_INVALID_ARG, "%s: NULL pointer", who);
   bool fits = true;
   (from_word<A>(words[I], &fits), ...);
-  if (!fits) return set_error(MOE_ERR_SHAPE, "%s: a size or flag beyond 32 bits", who);
+  if (!fits) return set_error(MOE_ERR_SHAPE, "%s: a size or flag beyond 32 bits, or a negative number of bytes", who);
   return f(from_word<A>(words[I], &fits)...);
 }
 template <size_t WORDS, class... A>
