@@ -678,7 +678,7 @@ struct AdapterGradMaps {
 // ...: bit g of an adapter's words. A warp marks them with eight segments a lane
 // in flight. Where a CTA would look at more than AG_LOOKS groups for its adapters
 // one by one, each a load's latency, this is faster (backward, K = N = 2048, rank
-// 16: 4096 segments of one row, 1024 adapters 5.3 -> 1.0 ms, 256 and 64 71 -> 65
+// 16: 4096 segments of one row, 1024 adapters 5.3 -> 1.0 ms, 256 and 64 74 -> 67
 // us), with fewer slower (58 and 48: 43 us, 44 with the marks).
 constexpr int AG_LOOKS = 48, AG_WORDS = 1024;
 __device__ __forceinline__ void mark_segments(const AdapterGradArgs &a, int ad, int step, int words, uint32_t *bits) {
@@ -701,11 +701,11 @@ __device__ __forceinline__ void mark_segments(const AdapterGradArgs &a, int ad, 
 
 // The gradients of one adapter for a slab of 64 columns c of x (dA) or dy (dB):
 // G[j][c] = sum over the rows t of the adapter's segments of p[t][j] z[t][c],
-// with p = du (both of its values), z = x or p = u, z = dy. Rows pass AG_ROWS at a time through shared
-// memory, read transposed (ldmatrix.trans): M = columns (16 per warp), N =
-// ranks, K = rows (two warps share a chunk's). The rows behind a
-// segment's end are cleared in the fragments. The segments are taken in order
-// by one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
+// with p = du (both of its values), z = x or p = u, z = dy. Rows pass AG_ROWS at a
+// time through shared memory, read transposed (ldmatrix.trans): M = columns (16
+// per warp), N = ranks, K = rows (two warps share a chunk's). The rows behind a
+// segment's end are cleared in the fragments. The segments are taken in order by
+// one CTA, so the sum's order is fixed. An adapter without rows gets zeros.
 // LONG: some adapter may need more additions than AG_ADDITIONS. MARK: see
 // mark_segments. (The least CTAs an SM are what its shared memory holds, set where
 // the compiler by itself spills or takes registers for fewer: backward at T =
