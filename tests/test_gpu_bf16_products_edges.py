@@ -205,3 +205,54 @@ def test_infinite_inner_gradients_stay_infinite(M):
     assert M.moe_read_device_error(ws) == 0
     assert torch.isinf(p.du[3]).all() and (p.da[0][:, p.x[3] > 0] == float("inf")).all()
     assert torch.isfinite(p.da[1]).all()
+
+
+def test_long_sums_on_two_streams_and_from_graphs(M):
+    """Calls whose sums pass through their workspaces, at once on two streams and replayed: the bits of one call alone."""
+    R, N, K, n, r = 40_000, 264, 520, 70, 64
+    off = torch.tensor([0, 20_001, 20_001, R], dtype=torch.int32, device="cuda")
+    seg = torch.arange(0, R + 1, 400, dtype=torch.int32, device="cuda")
+    S = seg.numel() - 1
+    ad = (torch.arange(S, device="cuda") * 7 % n).to(torch.int32)
+    a, b, w = _rand((n, r, K), 1, 0.1), _rand((n, N, r), 2, 0.1), _rand((N, K), 3)
+    jobs = []
+    for i in range(2):
+        x, dy, u = _rand((R, K), 10 + i), _rand((R, N), 20 + i), _rand((R, r), 30 + i)
+        dw = torch.zeros(3, N, K, dtype=torch.bfloat16, device="cuda")
+        du, da, db = torch.zeros_like(u), torch.zeros_like(a), torch.zeros_like(b)
+        gws = torch.zeros(M.moe_grouped_gemm_workspace_size(R, 3, N, K), dtype=torch.uint8, device="cuda")
+        lws = torch.zeros(M.moe_lora_workspace_size(R, S, n, r, N, K), dtype=torch.uint8, device="cuda")
+
+        def job(stream=None, x=x, dy=dy, u=u, dw=dw, du=du, da=da, db=db, gws=gws, lws=lws):
+            M.moe_grouped_gemm_wgrad(dy, N, x, K, off, R, 3, N, K, 0, dw, N * K, gws, gws.numel(), stream)
+            M.moe_lora_linear_backward(dy, N, x, K, w, u, seg, ad, a, b, None, R, S, n, r, N, K, du, None, K, da, db, lws,
+                                       lws.numel(), stream)
+        job()
+        torch.cuda.synchronize()
+        jobs.append((job, (dw, da, db), [t.clone() for t in (dw, da, db)], (gws, lws), torch.cuda.Stream()))
+
+    def check():
+        torch.cuda.synchronize()
+        for _, out, ref, spaces, _ in jobs:
+            assert all(M.moe_read_device_error(ws) == 0 for ws in spaces)
+            assert all(torch.equal(t, q) for t, q in zip(out, ref))
+            for t in out:
+                t.fill_(3.0)
+        torch.cuda.synchronize()
+
+    check()
+    for _ in range(3):
+        for job, _, _, _, s in jobs:
+            job(s)
+        check()
+    graphs = []
+    for job, _, _, _, s in jobs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            job(s)
+        graphs.append(g)
+    for _ in range(3):
+        for g, (_, _, _, _, s) in zip(graphs, jobs):
+            with torch.cuda.stream(s):
+                g.replay()
+        check()
